@@ -81,7 +81,8 @@ typedef enum {
   SDPA_ERR_UNSUPPORTED = 2,    /* valid but unsupported dtype / head dim / shape */
   SDPA_ERR_CUDA = 3,           /* a CUDA runtime call or kernel launch failed */
   SDPA_ERR_DEVICE_TIMEOUT = 4, /* a kernel's bounded wait ran out (reported by poll) */
-  SDPA_ERR_WORKSPACE = 5       /* workspace missing or smaller than required */
+  SDPA_ERR_WORKSPACE = 5,      /* workspace missing or smaller than required */
+  SDPA_ERR_DEVICE_INDEX = 6    /* a kernel met a page, length or axis out of range (poll) */
 } sdpa_status_t;
 
 /*
@@ -265,9 +266,118 @@ int sdpa_bwd_noalloc(const void* q, const void* k, const void* v, const void* ou
                      int dtype, void* stream);
 
 /*
+ * Rotary embedding: rotates pairs of elements of q and k by angles that grow with the
+ * rows' positions.  For pair p (0 <= p < rot/2) of row i of batch b,
+ *     t = positions[axes[p], b, i] · inv_freq[p]
+ *     y_a = x_a·cos t − x_b·sin t,   y_b = x_b·cos t + x_a·sin t
+ * with (a, b) = (p, p + rot/2), or (2p, 2p + 1) with SDPA_ROTARY_ADJACENT.  Elements rot and
+ * up are copied.  SDPA_ROTARY_INVERSE turns by −t, which is the inverse and, since the
+ * rotation is orthogonal, also the vector-Jacobian product: given the gradients of the
+ * outputs it writes those of the inputs.  Several axes (time, height and width of a video's
+ * patches, say) are rows of `positions`; `axes` says which one turns each pair.
+ *   q, q_out [B,Hq,L,D], k, k_out [B,Hkv,L,D] dtype, through `strides`.  k may be NULL (with
+ *   k_out NULL): only q is rotated.  In place (q_out == q with equal strides) is allowed;
+ *   otherwise outputs share no element with any of the others.  Address ranges decide that,
+ *   except for views of one buffer of tokens (equal batch and row strides) whose heads lie
+ *   side by side in each token, as q and k in a fused projection's output do.
+ *   positions [naxes,B,L] signed integers of position_bits (32 or 64), element strides
+ *   (axis, batch, row) in position_strides; a stride of 0 broadcasts.  inv_freq [rot/2] fp32,
+ *   axes [rot/2] int32 or NULL (axis 0 for all).  Each may overlap inputs, not outputs.
+ *   1 <= naxes, rot even, 2 <= rot <= D.
+ * Angles are exact to 2^-32 turns plus |position·inv_freq|·2^-64 turns: they are computed
+ * modulo one turn in integers, however far the position.  Rotations run in fp32 and are
+ * rounded once.  An axis outside 0..naxes-1 is read as axis 0 and reported by
+ * sdpa_poll_status (SDPA_ERR_DEVICE_INDEX).  A frequency that is not finite gives NaN.
+ */
+typedef struct {
+  sdpa_layout_t q, k, q_out, k_out; /* k and k_out are not read when k is NULL */
+} sdpa_rotary_strides_t;
+#define SDPA_ROTARY_ADJACENT 1 /* pairs (2p, 2p + 1) instead of (p, p + rot/2) */
+#define SDPA_ROTARY_INVERSE 2  /* turn by the negative angles */
+int sdpa_rotary(const void* q, const void* k, void* q_out, void* k_out, const void* positions,
+                int position_bits, const int64_t* position_strides, const float* inv_freq,
+                const int* axes, int naxes, int B, int Hq, int Hkv, int L, int D, int rot, int flags,
+                int dtype, const sdpa_rotary_strides_t* strides, void* stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  Its memory is an array
+ * [num_pages][Hkv][page_size / 16] of tiles; a tile holds 16 consecutive tokens' keys and
+ * values of one KV head in 20·D bytes (5 bits an element, 4 of code and 1 of parameters).
+ * Position j of sequence b lies in page pages[b][j / page_size], at place j % page_size.
+ *  - Format.  A row of D elements is D/32 groups of 32.  Each group has a zero z, its
+ *    smallest element, and a scale s = (largest − z) / 15, both of `dtype`, and its elements
+ *    are codes c in 0..15 that stand for z + s·c: c = (x − z) / s rounded to even (0 where s
+ *    is 0).  A group with an element that is not finite, or whose range overflows fp32, reads
+ *    back as NaN.  With NG = D/32, W = min(NG, 4) and group j = W·jb + w, a tile is
+ *      K codes  [row / 8][jb][row % 8][t][w] 32-bit words, nibble n = element 32j + 8t + n
+ *      V codes  [row / 8][jb][g][t][w] words, low half row 8·(row/8) + 2t, high half the row
+ *               after it; nibble n of a half = element 32j + 4g + n
+ *      K parameters [jb][row][w] pairs (s, z), then V parameters the same
+ *    (t in 0..3, g in 0..7): the order in which warp-level MMA fragments read them.
+ *  - Rows of a call are the LAST rows of each sequence: with lens[b] tokens in sequence b
+ *    after the call's own, row i of L is position lens[b] − L + i.  Rows of negative position
+ *    are padding, on the left.
+ *  - dtype is SDPA_F16 or SDPA_BF16 (others: SDPA_ERR_UNSUPPORTED), D one of the supported
+ *    head dims, page_size a multiple of 16, at most 2^16; every call on a cache uses one
+ *    dtype.  data is 16-byte aligned; pages and lens are 4-byte aligned.
+ *  - A page outside 0..num_pages−1, where a position needs it, or a length below 0 or above
+ *    pages_per_seq·page_size is reported by sdpa_poll_status (SDPA_ERR_DEVICE_INDEX) and never
+ *    read or written through: such tokens are not written, read as 0 and are hidden from
+ *    attention (a length above the table is read as the table's end, one below 0 as 0).
+ */
+typedef struct {
+  void* data;
+  int num_pages, page_size, Hkv, D, dtype;
+  const int* pages;      /* device, [B][pages_stride], the first pages_per_seq of each row */
+  int64_t pages_stride;  /* elements */
+  int pages_per_seq;
+  const int* lens;       /* device, [B] */
+} sdpa_cache_t;
+
+/* Bytes of one page of all heads (Hkv · page_size/16 · 20·D); 0 for invalid arguments. */
+size_t sdpa_cache_page_bytes(int page_size, int Hkv, int D, int dtype);
+
+/*
+ * Quantises the rows of k and v [B,Hkv,L,D] into the cache.  layouts[0] and [1] are those of
+ * k and v.  counts (device int32 [B], or NULL for L each): only the last counts[b] rows of
+ * sequence b are written.  No other token's codes change; two tokens of one call must not
+ * share a place (their codes and parameters could come from different tokens).
+ */
+int sdpa_cache_write(const sdpa_cache_t* cache, const void* k, const void* v,
+                     const sdpa_layout_t* layouts, const int* counts, int B, int L, void* stream);
+
+/*
+ * Reads the last L rows of each sequence back into k and v [B,Hkv,L,D] (every row is
+ * written: 0 where the position is negative), layouts as in sdpa_cache_write.  Values are
+ * z + s·c in fp32, rounded once.
+ */
+int sdpa_cache_read(const sdpa_cache_t* cache, void* k, void* v, const sdpa_layout_t* layouts, int B,
+                    int L, void* stream);
+
+/*
+ * Attention of q [B,Hq,Lq,D] over the cached keys and values, as sdpa_fwd_sinks defines it
+ * (scale, sinks, lse, grouped heads), for any Lq >= 1; meant for few rows a KV head
+ * (Hq/Hkv·Lq): each 32 of them (16 at D = 256) read the cache once.  layouts[0] and [1] are
+ * those of q and out.  is_causal: SDPA_CAUSAL_NONE (every query sees all lens[b] tokens) or
+ * SDPA_CAUSAL_BOTTOM_RIGHT (query i sees positions up to lens[b] − Lq + i, its own);
+ * SDPA_CAUSAL_TOP_LEFT is SDPA_ERR_UNSUPPORTED.  A row that sees nothing gets out = 0 and
+ * lse = −inf (with a sink, the sink's).
+ * max_len bounds lens (<= 0: the table's end) and fixes the launch; longer sequences are
+ * reported and read as max_len long, from their first token.
+ * workspace as in sdpa_bwd, of sdpa_cache_attn_workspace_size bytes (may be 0, then it may
+ * be NULL); that size depends on the current device and needs no GPU memory.
+ */
+size_t sdpa_cache_attn_workspace_size(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len);
+int sdpa_cache_attn(const sdpa_cache_t* cache, const void* q, void* out, float* lse,
+                    const float* sinks, const sdpa_layout_t* layouts, int B, int Hq, int Lq,
+                    float scale, int is_causal, int max_len, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word that kernels set
- * when a bounded wait gives up.  Returns SDPA_OK, SDPA_ERR_DEVICE_TIMEOUT, or
- * SDPA_ERR_CUDA if the synchronisation itself reported an error.
+ * when a bounded wait gives up or an index that they read is out of range (the first of
+ * them since the last poll).  Returns SDPA_OK, SDPA_ERR_DEVICE_TIMEOUT,
+ * SDPA_ERR_DEVICE_INDEX, or SDPA_ERR_CUDA if the synchronisation itself reported an error.
  */
 int sdpa_poll_status(void* stream);
 
@@ -311,7 +421,11 @@ typedef enum {
   SDPA_KERNEL_VEC_FWD = 4,  /* short-query forward */
   SDPA_KERNEL_VEC_BWD = 5,  /* short-query backward */
   SDPA_KERNEL_SINK_GRAD = 6, /* sink-logit gradients */
-  SDPA_KERNEL_COUNT = 7
+  SDPA_KERNEL_ROTARY = 7,
+  SDPA_KERNEL_CACHE_WRITE = 8,
+  SDPA_KERNEL_CACHE_READ = 9,
+  SDPA_KERNEL_CACHE_ATTN = 10, /* attention over the 4-bit cache */
+  SDPA_KERNEL_COUNT = 11
 } sdpa_kernel_t;
 int sdpa_timing_enable(int on);
 int sdpa_timing_read(int kernel, double* total_ms, uint64_t* launches);

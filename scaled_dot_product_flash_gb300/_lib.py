@@ -20,6 +20,7 @@ STATUS_NAMES = {
     3: "SDPA_ERR_CUDA",
     4: "SDPA_ERR_DEVICE_TIMEOUT",
     5: "SDPA_ERR_WORKSPACE",
+    6: "SDPA_ERR_DEVICE_INDEX",
 }
 PATH_AUTO, PATH_TENSOR, PATH_SIMT, PATH_VECTOR = 0, 1, 2, 3
 
@@ -43,6 +44,20 @@ class Mask(ctypes.Structure):
                 ("head", ctypes.c_int64), ("row", ctypes.c_int64)]
 
 
+class Cache(ctypes.Structure):
+    """sdpa_cache_t: a 4-bit paged cache and the page table and lengths of one call."""
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_int64), ("pages_per_seq", ctypes.c_int),
+                ("lens", ctypes.c_void_p)]
+
+
+# Element strides handed over as plain int64 arrays: sdpa_layout_t[2] (6 values),
+# sdpa_rotary_strides_t (12) and the three strides of rotary positions.
+Int64x3, Int64x6, Int64x12 = (ctypes.c_int64 * n for n in (3, 6, 12))
+
+ROTARY_ADJACENT, ROTARY_INVERSE = 1, 2
 MASK_NONE, MASK_BOOL, MASK_ADDITIVE = 0, 1, 2
 _sp = ctypes.POINTER(Strides)
 _mp = ctypes.POINTER(Mask)
@@ -74,9 +89,18 @@ SIGNATURES = {
                              _i, _sp, _vp]),
     "sdpa_bwd_masked": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _mp, _vp, _vp, _vp, _vp,
                              _i, _i, _i, _i, _i, _i, _f, _i, _i, _sp, _vp, _sz, _vp]),
+    "sdpa_rotary": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                         _i, _i, _vp, _vp]),
+    "sdpa_cache_page_bytes": (_sz, [_i, _i, _i, _i]),
+    "sdpa_cache_write": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "sdpa_cache_read": (_i, [_vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "sdpa_cache_attn_workspace_size": (_sz, [_vp, _i, _i, _i, _i]),
+    "sdpa_cache_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _vp, _sz,
+                             _vp]),
 }
 BWD_NOALLOC_MAX_ROWS = 1 << 20
-KERNELS = {"fwd": 0, "delta": 1, "dq": 2, "dkdv": 3, "vec_fwd": 4, "vec_bwd": 5, "sink_grad": 6}
+KERNELS = {"fwd": 0, "delta": 1, "dq": 2, "dkdv": 3, "vec_fwd": 4, "vec_bwd": 5, "sink_grad": 6,
+           "rotary": 7, "cache_write": 8, "cache_read": 9, "cache_attn": 10}
 
 _lib = None
 
@@ -182,6 +206,38 @@ def sdpa_bwd_noalloc(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Lq, Lkv, D
     """sdpa_bwd with its scratch in the library's static device array (no workspace)."""
     return load().sdpa_bwd_noalloc(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Lq, Lkv, D,
                                    scale, is_causal, dtype, stream)
+
+
+def sdpa_rotary(q, k, q_out, k_out, positions, position_bits, position_strides, inv_freq, axes,
+                naxes, B, Hq, Hkv, L, D, rot, flags, dtype, strides, stream):
+    """position_strides: Int64x3 (axis, batch, row); strides: Int64x12 of q, k, q_out, k_out."""
+    return load().sdpa_rotary(q, k, q_out, k_out, positions, position_bits, position_strides,
+                              inv_freq, axes, naxes, B, Hq, Hkv, L, D, rot, flags, dtype, strides,
+                              stream)
+
+
+def sdpa_cache_page_bytes(page_size, Hkv, D, dtype) -> int:
+    return load().sdpa_cache_page_bytes(page_size, Hkv, D, dtype)
+
+
+def sdpa_cache_write(cache, k, v, layouts, counts, B, L, stream):
+    """cache: a ``Cache``; layouts: Int64x6 of k and v."""
+    return load().sdpa_cache_write(ctypes.byref(cache), k, v, layouts, counts, B, L, stream)
+
+
+def sdpa_cache_read(cache, k, v, layouts, B, L, stream):
+    return load().sdpa_cache_read(ctypes.byref(cache), k, v, layouts, B, L, stream)
+
+
+def sdpa_cache_attn_workspace_size(cache, B, Hq, Lq, max_len) -> int:
+    return load().sdpa_cache_attn_workspace_size(ctypes.byref(cache), B, Hq, Lq, max_len)
+
+
+def sdpa_cache_attn(cache, q, out, lse, sinks, layouts, B, Hq, Lq, scale, is_causal, max_len,
+                    workspace, workspace_bytes, stream):
+    """cache: a ``Cache``; layouts: Int64x6 of q and out."""
+    return load().sdpa_cache_attn(ctypes.byref(cache), q, out, lse, sinks, layouts, B, Hq, Lq,
+                                  scale, is_causal, max_len, workspace, workspace_bytes, stream)
 
 
 def sdpa_poll_status(stream):

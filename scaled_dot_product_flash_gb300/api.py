@@ -211,8 +211,261 @@ def attention_backward(q, k, v, out, dout, lse, scale=None, is_causal=False, wor
     return dq, dk, dv
 
 
+# ---- rotary embedding
+
+
+def _same_device(q, **others):
+    """q must be on the current device (its context runs the kernels), the others beside it."""
+    if q.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {q.device}, not on the current device: "
+                         "select it with torch.cuda.device")
+    for name, t in others.items():
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} must be on {q.device}")
+
+
+def _dense(t):
+    """(batch, head, row) strides of a [B, H, L, D] tensor; those of size-1 dimensions, which
+    torch leaves undefined, are replaced by D."""
+    B, H, L, D = t.shape
+    b, h, r, _ = t.stride()
+    return (b if B > 1 else D, h if H > 1 else D, r if L > 1 else D)
+
+
+def rotary_axes(sections, device="cuda"):
+    """int32 [sum(sections)] axis of each pair: the first sections[0] pairs turn by axis 0's
+    positions, the next sections[1] by axis 1's, and so on."""
+    if any(n < 0 for n in sections) or sum(sections) < 1:
+        raise ValueError("sections must be counts of pairs")
+    return torch.tensor([a for a, n in enumerate(sections) for _ in range(n)],
+                        dtype=torch.int32, device=device)
+
+
+def _positions(positions, B, L):
+    """(axes, strides) of positions [L], [B, L] or [axes, B, L]; B may be 1 for all batches."""
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be int32 or int64")
+    shape, strides = (1,) * (3 - positions.dim()) + tuple(positions.shape), positions.stride()
+    if len(shape) != 3 or shape[1] not in (1, B) or shape[2] != L or shape[0] < 1:
+        raise ValueError(f"positions {tuple(positions.shape)} must be [L], [B, L] or [axes, B, L] "
+                         f"with L = {L} and B = {B} or 1")
+    strides = (0,) * (3 - len(strides)) + strides
+    return shape[0], [0 if n == 1 else s for n, s in zip(shape, strides)]
+
+
+def _rotary(q, k, positions, inv_freq, axes, adjacent, inverse, q_out, k_out, stream):
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):  # outputs then belong to that stream
+            return _rotary(q, k, positions, inv_freq, axes, adjacent, inverse, q_out, k_out, None)
+    _check("q", q)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, L, D]")
+    B, Hq, L, D = q.shape
+    if k is not None:
+        _check("k", k, q.dtype)
+        if k.dim() != 4 or k.shape[0] != B or k.shape[2] != L or k.shape[3] != D:
+            raise ValueError("q and k disagree in batch, rows or head dim")
+    if q.dtype not in DTYPE_CODE:
+        raise ValueError(f"q has dtype {q.dtype}, expected fp32, fp16 or bf16")
+    _same_device(q, k=k, positions=positions, inv_freq=inv_freq, axes=axes, q_out=q_out, k_out=k_out)
+    naxes, at = _positions(positions, B, L)
+    _check("inv_freq", inv_freq, torch.float32)
+    if inv_freq.dim() != 1 or not 2 <= 2 * inv_freq.numel() <= D:
+        raise ValueError("inv_freq must be 1-D, one frequency a pair, at most D/2")
+    if axes is not None:
+        _check("axes", axes, torch.int32)
+        if axes.shape != inv_freq.shape:
+            raise ValueError("axes must have one axis for each of inv_freq's pairs")
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    _check("q_out", q_out, q.dtype)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    strides = (*_dense(q), 0, 0, 0, *_dense(q_out), 0, 0, 0)
+    if k is not None:
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        _check("k_out", k_out, q.dtype)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        strides = (*strides[:3], *_dense(k), *strides[6:9], *_dense(k_out))
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    st = _lib.sdpa_rotary(
+        q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+        None if k is None else k_out.data_ptr(), positions.data_ptr(),
+        64 if positions.dtype == torch.int64 else 32, _lib.Int64x3(*at), inv_freq.data_ptr(),
+        None if axes is None else axes.data_ptr(), naxes, B, Hq, 0 if k is None else k.shape[1], L,
+        D, 2 * inv_freq.numel(),
+        (_lib.ROTARY_ADJACENT if adjacent else 0) | (_lib.ROTARY_INVERSE if inverse else 0),
+        DTYPE_CODE[q.dtype], _lib.Int64x12(*strides), _stream(None))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_rotary")
+    return q_out, k_out
+
+
+def rotary(q, k, positions, inv_freq, axes=None, adjacent=False, q_out=None, k_out=None,
+           stream=None):
+    """q and k with each pair of elements turned by position·inv_freq; returns both.
+
+    q [B,Hq,L,D] and k [B,Hkv,L,D] (or None) in any layout with contiguous rows; positions
+    int32 or int64 [L], [B,L] or [axes,B,L] (B may be 1); inv_freq fp32 [rot/2], rot <= D;
+    axes int32 [rot/2] (see ``rotary_axes``): the row of ``positions`` that turns each pair,
+    the first for all by default.  Pair p is (p, p + rot/2), or (2p, 2p + 1) when
+    ``adjacent``; elements rot and up are copied.  ``q_out=q, k_out=k`` rotates in place.
+    """
+    return _rotary(q, k, positions, inv_freq, axes, adjacent, False, q_out, k_out, stream)
+
+
+def rotary_backward(dq_out, dk_out, positions, inv_freq, axes=None, adjacent=False, dq=None,
+                    dk=None, stream=None):
+    """(dq, dk) of ``rotary`` from the gradients of its outputs: the rotation by the negative
+    angles, which also undoes it."""
+    return _rotary(dq_out, dk_out, positions, inv_freq, axes, adjacent, True, dq, dk, stream)
+
+
+# ---- 4-bit paged cache
+
+
+def cache_empty(num_pages, num_kv_heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda"):
+    """Memory of a 4-bit paged cache of keys and values: a tensor of ``dtype`` (fp16 or bf16)
+    [num_pages, num_kv_heads, page_size/16, 10·head_dim] whose last dimension is one tile of
+    16 tokens, 5 bits an element (``sdpa.h`` has the layout).  Its values mean nothing to
+    torch; pages can be copied or moved whole."""
+    code = DTYPE_CODE.get(dtype, 0)
+    if not _lib.sdpa_cache_page_bytes(page_size, num_kv_heads, head_dim, code) or num_pages < 1:
+        raise ValueError("a cache needs fp16 or bf16, a supported head dim and pages of a "
+                         "multiple of 16 tokens")
+    return torch.empty((num_pages, num_kv_heads, page_size // 16, 10 * head_dim), dtype=dtype,
+                       device=device)
+
+
+def _cache(cache, pages, lens, B):
+    """The library's view of a cache with one call's page table [B, n] and lengths [B]."""
+    if not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 10:
+        raise ValueError("cache must be a contiguous CUDA tensor made by cache_empty")
+    if cache.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("cache must be fp16 or bf16")
+    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != B or pages.stride(1) != 1:
+        raise ValueError(f"pages must be an int32 [{B}, n] tensor with contiguous rows")
+    if lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+        raise ValueError(f"lens must be a contiguous int32 [{B}] tensor")
+    n, H, tiles, width = cache.shape
+    width_p = pages.shape[1]
+    return _lib.Cache(cache.data_ptr(), n, 16 * tiles, H, width // 10, DTYPE_CODE[cache.dtype],
+                      pages.data_ptr(), pages.stride(0) if B > 1 else width_p, width_p,
+                      lens.data_ptr())
+
+
+def _cache_rows(name, t, cache, B=None, L=None):
+    """Checks a [B, Hkv, L, D] tensor of rows of the cache."""
+    _check(name, t, cache.dtype)
+    if t.dim() != 4 or t.shape[1] != cache.shape[1] or 10 * t.shape[3] != cache.shape[3]:
+        raise ValueError(f"{name} must be [B, Hkv, L, D] of the cache's heads and head dim")
+    if B is not None and (t.shape[0], t.shape[2]) != (B, L):
+        raise ValueError(f"{name} must have {B} sequences of {L} rows")
+
+
+def cache_write(cache, k, v, pages, lens, counts=None, stream=None):
+    """Quantises the rows of k and v [B,Hkv,L,D] into the cache, in place.
+
+    pages int32 [B, n]: the pages of each sequence, in order.  lens int32 [B]: tokens of each
+    sequence INCLUDING these: row i of L is position lens[b] - L + i, so a padded batch is
+    padded on the left, and rows of negative position are not written.  counts int32 [B]: only
+    the last counts[b] rows are written.  Pages outside the cache are skipped and reported by
+    ``poll_status``.
+    """
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return cache_write(cache, k, v, pages, lens, counts)
+    _cache_rows("k", k, cache)
+    B, L = k.shape[0], k.shape[2]
+    _cache_rows("v", v, cache, B, L)
+    c = _cache(cache, pages, lens, B)
+    if counts is not None and (counts.dtype != torch.int32 or counts.shape != (B,)
+                               or not counts.is_contiguous()):
+        raise ValueError(f"counts must be a contiguous int32 [{B}] tensor")
+    _same_device(k, cache=cache, v=v, pages=pages, lens=lens, counts=counts)
+    st = _lib.sdpa_cache_write(c, k.data_ptr(), v.data_ptr(), _lib.Int64x6(*_dense(k), *_dense(v)),
+                               None if counts is None else counts.data_ptr(), B, L, _stream(None))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_cache_write")
+
+
+def cache_read(cache, pages, lens, rows, k=None, v=None, stream=None):
+    """(k, v) [B,Hkv,rows,D]: the last ``rows`` tokens of each sequence as the cache holds
+    them, in its dtype.  Row i is position lens[b] - rows + i, 0 where that is negative."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return cache_read(cache, pages, lens, rows, k, v)
+    B = lens.shape[0]
+    c = _cache(cache, pages, lens, B)
+    shape = (B, cache.shape[1], rows, cache.shape[3] // 10)
+    k = torch.empty(shape, dtype=cache.dtype, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=cache.dtype, device=cache.device) if v is None else v
+    _cache_rows("k", k, cache, B, rows)
+    _cache_rows("v", v, cache, B, rows)
+    _same_device(cache, k=k, v=v, pages=pages, lens=lens)
+    st = _lib.sdpa_cache_read(c, k.data_ptr(), v.data_ptr(), _lib.Int64x6(*_dense(k), *_dense(v)),
+                              B, rows, _stream(None))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_cache_read")
+    return k, v
+
+
+def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right", need_lse=False,
+                    out=None, lse=None, sinks=None, max_len=None, workspace=None, stream=None):
+    """Attention of q [B,Hq,L,D] over the cached keys and values; returns (out, lse or None).
+
+    pages and lens as in ``cache_write`` (write the rows of this step first).  With the
+    default ``is_causal`` query i sees the positions up to its own, lens[b] - L + i; False
+    lets it see all lens[b].  A row that sees none gets 0 (lse -inf).  ``sinks`` and the other
+    arguments as in ``attention_forward``.  ``max_len`` bounds lens (default: the table's
+    width); a tighter bound launches less.  Meant for few rows a KV head; for long chunks
+    read the prefix with ``cache_read`` and call ``attention_forward``.
+    """
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return cache_attention(q, cache, pages, lens, scale, is_causal, need_lse, out, lse,
+                                   sinks, max_len, workspace)
+    _check("q", q, cache.dtype)
+    if q.dim() != 4 or 10 * q.shape[3] != cache.shape[-1]:
+        raise ValueError("q must be [B, Hq, L, D] of the cache's head dim")
+    B, Hq, L, D = q.shape
+    c = _cache(cache, pages, lens, B)
+    out = torch.empty_like(q) if out is None else out
+    _check("out", out, q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if need_lse and lse is None:
+        lse = torch.empty((B, Hq, L), device=q.device, dtype=torch.float32)
+    if not need_lse:
+        lse = None
+    elif lse.shape != (B, Hq, L) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, Hq, L] tensor")
+    if sinks is not None:
+        _check_sinks("sinks", sinks, Hq)
+    _same_device(q, cache=cache, pages=pages, lens=lens, out=out, lse=lse, sinks=sinks,
+                 workspace=workspace)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    max_len = 0 if max_len is None else int(max_len)
+    need = _lib.sdpa_cache_attn_workspace_size(c, B, Hq, L, max_len)
+    if workspace is None and need:
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    st = _lib.sdpa_cache_attn(c, q.data_ptr(), out.data_ptr(),
+                              None if lse is None else lse.data_ptr(),
+                              None if sinks is None else sinks.data_ptr(),
+                              _lib.Int64x6(*_dense(q), *_dense(out)), B, Hq, L, scale,
+                              _causal(is_causal), max_len,
+                              None if workspace is None else workspace.data_ptr(),
+                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                              _stream(None))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_cache_attn")
+    return out, lse
+
+
 def poll_status(stream=None):
-    """Synchronise the stream; raise if a kernel reported a timed-out wait."""
+    """Synchronise the stream; raise if a kernel reported a timed-out wait or an index out of
+    range."""
     st = _lib.sdpa_poll_status(_stream(stream))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_poll_status")

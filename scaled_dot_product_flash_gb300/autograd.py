@@ -96,3 +96,48 @@ def scaled_dot_product_attention(query, key, value, attn_mask=None, dropout_p=0.
     # library); others are copied to [B, H, L, D] first.
     q, k, v = (t if t.stride(-1) == 1 else t.contiguous() for t in (query, key, value))
     return SDPAFunction.apply(q, k, v, sinks, attn_mask, s, bool(is_causal))
+
+
+def _passable(t):
+    """t, or a copy of it where the library cannot take its layout (rows that are not contiguous
+    or not 16-byte aligned, or dimensions that an expand folded onto one address)."""
+    if t is None:
+        return None
+    es, D = t.element_size(), t.shape[-1]
+    fine = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+        n == 1 or (s >= D and s * es % 16 == 0) for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
+
+
+class RotaryFunction(torch.autograd.Function):
+    """(q, k) turned by their positions; the gradient is the rotation by the negative angles."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, axes, adjacent, inverse):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions, inv_freq, axes)
+        ctx.adjacent, ctx.inverse = adjacent, inverse
+        turn = api.rotary_backward if inverse else api.rotary
+        out = turn(_passable(q), _passable(k), positions, inv_freq, axes, adjacent)
+        return out[0] if k is None else out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        positions, inv_freq, axes = ctx.saved_tensors
+        args = (positions, inv_freq, axes, ctx.adjacent, not ctx.inverse)
+        dq, dk = grads if len(grads) == 2 else (grads[0], None)
+        if dq is not None and dk is not None:
+            dq, dk = RotaryFunction.apply(dq, dk, *args)
+        elif dq is not None:
+            dq = RotaryFunction.apply(dq, None, *args)
+        elif dk is not None:
+            dk = RotaryFunction.apply(dk, None, *args)
+        return dq, dk, None, None, None, None, None
+
+
+def rotary_embedding(query, key, positions, inv_freq, axes=None, adjacent=False):
+    """``api.rotary`` (which documents the arguments), differentiable in query and key, any
+    number of times; key may be None, then the result is the query alone."""
+    if inv_freq.requires_grad:
+        raise NotImplementedError("no gradient is computed for inv_freq")
+    return RotaryFunction.apply(query, key, positions, inv_freq, axes, bool(adjacent), False)

@@ -18,6 +18,7 @@ enum DeviceError : unsigned {
   kDevErrNone = 0,
   kDevErrTimeout = 1,  // a bounded wait ran out
   kDevErrLayout = 2,   // a block found its shared memory placed other than its layout assumes
+  kDevErrIndex = 3,    // a page, length or axis read from device memory is out of range
 };
 
 // Kernel ids for the error word.
@@ -31,6 +32,10 @@ enum KernelId : unsigned {
   kKidTcFwd = 7,
   kKidTcDq = 8,
   kKidTcDkdv = 9,
+  kKidRotary = 10,
+  kKidCacheWrite = 11,
+  kKidCacheRead = 12,
+  kKidCacheAttn = 13,
 };
 
 __device__ __forceinline__ void report_error(unsigned* err, unsigned code, unsigned kid) {
@@ -112,9 +117,9 @@ __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000)
 // sink, so the no-sink arithmetic is unchanged).  m and l then describe the row with the
 // sink, so lse = ln2·(m + log2 l) includes it.  A sink of −inf is no sink (also for a row
 // that saw no key, where m = −inf too).  A NaN sink gives NaN outputs.
-__device__ __forceinline__ float fold_sink(const Problem& p, int h, float& m, float& l) {
-  if (!p.sinks) return 1.f;
-  const float s2 = p.sinks[h] * kLog2e;
+__device__ __forceinline__ float fold_sink(const float* sinks, int h, float& m, float& l) {
+  if (!sinks) return 1.f;
+  const float s2 = sinks[h] * kLog2e;
   if (s2 == minus_inf()) return 1.f;
   if (s2 <= m) {
     l += exp2f(s2 - m);
@@ -124,6 +129,10 @@ __device__ __forceinline__ float fold_sink(const Problem& p, int h, float& m, fl
   l = fmaf(l, a, 1.f);
   m = s2;
   return a;
+}
+
+__device__ __forceinline__ float fold_sink(const Problem& p, int h, float& m, float& l) {
+  return fold_sink(p.sinks, h, m, l);
 }
 
 // Mask term of one (query row, key) pair in the log2 domain: log2e·M, or −inf for a key a

@@ -8,8 +8,8 @@
 #include <utility>
 #include <vector>
 
+#include "host.h"
 #include "launch.h"
-#include "../../include/sdpa.h"
 
 namespace sdpa {
 namespace {
@@ -24,6 +24,35 @@ std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 constexpr int kMaxDevices = 64;
 std::atomic<unsigned*> g_err_ptr[kMaxDevices];
 std::mutex g_err_mu;
+
+// ---- optional per-kernel device timing (CUDA events bracketing each launch) ----
+struct PendingTiming {
+  int kernel;
+  EventPair ev;
+};
+std::mutex g_timing_mu;
+std::atomic<bool> g_timing_on{false};
+std::vector<EventPair> g_event_pool;
+std::vector<PendingTiming> g_pending;
+double g_total_ms[SDPA_KERNEL_COUNT] = {};
+uint64_t g_timed_launches[SDPA_KERNEL_COUNT] = {};
+
+bool take_pair(EventPair* ev) {
+  std::lock_guard<std::mutex> lock(g_timing_mu);
+  if (!g_event_pool.empty()) {
+    *ev = g_event_pool.back();
+    g_event_pool.pop_back();
+    return true;
+  }
+  if (cudaEventCreate(&ev->start) != cudaSuccess) return false;
+  if (cudaEventCreate(&ev->stop) != cudaSuccess) {
+    cudaEventDestroy(ev->start);
+    return false;
+  }
+  return true;
+}
+
+}  // namespace
 
 // Device address of the error word on the current device, looked up once per device (the
 // library assumes each device's primary context and no device reset while it is loaded).
@@ -57,15 +86,6 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 size_t elem_size(int dtype) { return dtype == SDPA_F32 ? 4 : 2; }
 
-sdpa_layout_t contiguous(int H, int L, int D) {
-  return sdpa_layout_t{(int64_t)H * L * D, (int64_t)L * D, (int64_t)D};
-}
-
-sdpa_strides_t contiguous_strides(int Hq, int Hkv, int Lq, int Lkv, int D) {
-  const sdpa_layout_t lq = contiguous(Hq, Lq, D), lk = contiguous(Hkv, Lkv, D);
-  return sdpa_strides_t{lq, lk, lk, lq, lq, lq, lk, lk};
-}
-
 // Validates the layout of one [B, H, L, D] tensor (strides positive, multiples of 16
 // bytes, no two elements at one address: sorted by stride, each stride covers the extent
 // of the smaller dimensions) and returns its byte extent in *bytes.
@@ -89,6 +109,43 @@ bool check_layout(const sdpa_layout_t& l, int B, int H, int L, int D, size_t es,
                     (int64_t)es);
   *out = Layout{l.batch, l.head, l.row};
   return true;
+}
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+bool begin_launch(EventPair* ev, cudaStream_t s) {
+  const bool timed = g_timing_on.load() && take_pair(ev);
+  if (timed) cudaEventRecord(ev->start, s);
+  return timed;
+}
+
+void end_launch(int kernel, const EventPair& ev, bool timed, cudaError_t e, cudaStream_t s) {
+  if (e == cudaSuccess) g_launches.fetch_add(1);
+  if (!timed) return;
+  cudaEventRecord(ev.stop, s);
+  std::lock_guard<std::mutex> lock(g_timing_mu);
+  if (e == cudaSuccess) g_pending.push_back({kernel, ev});
+  else g_event_pool.push_back(ev);
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA; }
+
+namespace {
+
+sdpa_layout_t contiguous(int H, int L, int D) {
+  return sdpa_layout_t{(int64_t)H * L * D, (int64_t)L * D, (int64_t)D};
+}
+
+sdpa_strides_t contiguous_strides(int Hq, int Hkv, int Lq, int Lkv, int D) {
+  const sdpa_layout_t lq = contiguous(Hq, Lq, D), lk = contiguous(Hkv, Lkv, D);
+  return sdpa_strides_t{lq, lk, lk, lq, lq, lq, lk, lk};
 }
 
 // Validates an attention mask (kind, alignment, strides) and fills p->mask, mask_kind and
@@ -134,10 +191,8 @@ int check_sizes(int B, int Hq, int Hkv, int Lq, int Lkv, int D, float scale, int
   p->G = Hq / Hkv;
   p->scale = scale;
   p->scale_log2 = scale * kLog2e;
-  p->wait_limit_ns = g_wait_limit_ns.load();
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    p->num_sms = 0;  // no prefetch hints
+  p->wait_limit_ns = wait_limit_ns();
+  p->num_sms = sm_count();  // 0 (unknown): no prefetch hints
   return SDPA_OK;
 }
 
@@ -178,56 +233,6 @@ int choose(const Problem& p, int dtype, Family* f) {
   else *f = Family::kSimt;
   return SDPA_OK;
 }
-
-// ---- optional per-kernel device timing (CUDA events bracketing each launch) ----
-struct EventPair {
-  cudaEvent_t start = nullptr, stop = nullptr;
-};
-struct PendingTiming {
-  int kernel;
-  EventPair ev;
-};
-std::mutex g_timing_mu;
-std::atomic<bool> g_timing_on{false};
-std::vector<EventPair> g_event_pool;
-std::vector<PendingTiming> g_pending;
-double g_total_ms[SDPA_KERNEL_COUNT] = {};
-uint64_t g_timed_launches[SDPA_KERNEL_COUNT] = {};
-
-bool take_pair(EventPair* ev) {
-  std::lock_guard<std::mutex> lock(g_timing_mu);
-  if (!g_event_pool.empty()) {
-    *ev = g_event_pool.back();
-    g_event_pool.pop_back();
-    return true;
-  }
-  if (cudaEventCreate(&ev->start) != cudaSuccess) return false;
-  if (cudaEventCreate(&ev->stop) != cudaSuccess) {
-    cudaEventDestroy(ev->start);
-    return false;
-  }
-  return true;
-}
-
-// Launches one kernel through `fn`, counting it and, when timing is on, bracketing it with
-// events on its stream.
-template <typename Fn>
-cudaError_t launch_one(int kernel, cudaStream_t s, Fn fn) {
-  EventPair ev;
-  const bool timed = g_timing_on.load() && take_pair(&ev);
-  if (timed) cudaEventRecord(ev.start, s);
-  cudaError_t e = fn();
-  if (e == cudaSuccess) g_launches.fetch_add(1);
-  if (timed) {
-    cudaEventRecord(ev.stop, s);
-    std::lock_guard<std::mutex> lock(g_timing_mu);
-    if (e == cudaSuccess) g_pending.push_back({kernel, ev});
-    else g_event_pool.push_back(ev);
-  }
-  return e;
-}
-
-int status_of(cudaError_t e) { return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA; }
 
 // ---- fork / join of the two tiled backward kernels ----
 // The dK/dV and dQ kernels both need only δ, so they run concurrently: the dK/dV kernel on
@@ -508,7 +513,7 @@ extern "C" int sdpa_poll_status(void* stream) {
   if (word == 0) return SDPA_OK;
   const unsigned zero = 0;
   if (cudaMemcpy(err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return SDPA_ERR_CUDA;
-  return SDPA_ERR_DEVICE_TIMEOUT;
+  return (word & 0xffffu) == kDevErrIndex ? SDPA_ERR_DEVICE_INDEX : SDPA_ERR_DEVICE_TIMEOUT;
 }
 
 extern "C" const char* sdpa_status_string(int status) {
@@ -519,6 +524,7 @@ extern "C" const char* sdpa_status_string(int status) {
     case SDPA_ERR_CUDA: return "CUDA error";
     case SDPA_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait timed out";
     case SDPA_ERR_WORKSPACE: return "workspace missing or too small";
+    case SDPA_ERR_DEVICE_INDEX: return "a kernel met an index out of range";
     default: return "unknown status";
   }
 }

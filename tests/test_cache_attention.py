@@ -1,0 +1,428 @@
+"""Attention over the 4-bit paged cache against the fp64 oracle on the values that the cache
+holds, and the cache, the rotary embedding and the attention as they are used together.
+
+Tolerances.  A row's output is sum_j w_j·v_j with v = z + s·c, T the element type:
+    eps(T)/2·|o|                  its rounding (2^-25 where fp16 has no smaller step)
+  + 2^-11·sum_j w_j·s·c           the products w·s enter the MMA rounded to fp16, the z term
+                                  stays in fp32
+  + 2^-16·max|v|                  the scores: D products and D/32 scalings summed in fp32, with
+                                  |S| up to about 20 off by some 20·2^-22, which moves each
+                                  weight by as much relative to itself, twice with the sum
+lse: 2^-16·max(1, |lse|), the scores' error and one logarithm.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from cache_util import TYPES, dirty_cache, draw_rows, held, ints, make_table
+from oracle import cache as ref
+from scaled_dot_product_flash_gb300 import _lib, api, autograd, build
+from scaled_dot_product_flash_gb300.inputs import as_f64
+
+INVALID, UNSUPPORTED, WORKSPACE, INDEX = 1, 2, 5, 6
+
+
+def fill(rng, lens, H, D, page, dtype, width=None, spread=1.0):
+    """A cache holding random keys and values of the lengths given, its table, and per sequence
+    the fp64 keys and values it holds."""
+    table, pages = make_table(rng, lens, page, width)
+    cache = dirty_cache(pages, H, page, D, dtype)
+    L = max(max(lens), 1)
+    k, v = (draw_rows(rng, (len(lens), H, L, D), dtype, spread) for _ in range(2))
+    k += torch.from_numpy(rng.standard_normal((1, H, 1, D))).to(k.dtype)     # channels off zero
+    api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints(lens).cuda())
+    api.poll_status()
+    ks, vs, low = [], [], []
+    for b, n in enumerate(lens):
+        ks.append(held(as_f64(k)[b, :, L - n:], dtype))
+        code, s, z = ref.quantise(as_f64(v)[b, :, L - n:], TYPES[dtype])
+        vs.append(ref.values(code, s, z))
+        low.append(ref.values(code, s, np.zeros_like(z)))                     # s·c alone
+    return cache, table, ks, vs, low
+
+
+def check(out, lse, q, ks, vs, low, scale, causal, sinks, dtype, rows=None):
+    o, want_lse = ref.cached_attention(as_f64(q), ks, vs, scale, causal, sinks)
+    part, _ = ref.cached_attention(as_f64(q), ks, low, scale, causal, sinks)
+    B, Hq = o.shape[:2]
+    top = np.zeros((B, Hq, 1, 1))
+    for b in range(B):
+        if vs[b].size:
+            top[b, :, 0, 0] = np.repeat(np.abs(vs[b]).max((1, 2)), Hq // vs[b].shape[0])
+    tol = torch.finfo(TYPES[dtype]).eps / 2 * np.abs(o) + 2.0**-11 * part + 2.0**-16 * top + (2.0**-25 if dtype == "f16" else 0)
+    got = as_f64(out)
+    worst = (np.abs(got - o) / np.maximum(tol, 1e-300)).max()
+    assert np.isfinite(got).all() and worst <= 1, f"out is {worst:.2f} of its tolerance"
+    if lse is not None:
+        got = as_f64(lse)
+        none = np.isneginf(want_lse)
+        assert np.array_equal(np.isneginf(got), none)
+        off = np.abs(np.where(none, 0, got) - np.where(none, 0, want_lse)) / np.maximum(1, np.abs(np.where(none, 0, want_lse)))
+        assert off.max() <= 2.0**-16, f"lse off by {off.max():.2e}"
+
+
+# ---- without a GPU
+
+DATA, TABLE, LENS, Q, OUT, LSE, SINKS, WS = (0x10000000 * (n + 1) for n in range(8))
+GOOD = dict(data=DATA, num_pages=4, page_size=32, Hkv=2, D=64, dtype=2, pages=TABLE, pages_stride=300, pages_per_seq=300, lens=LENS)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=0), INVALID), (dict(out=0), INVALID), (dict(q=Q + 8), INVALID), (dict(lse=LSE + 4), INVALID), (dict(sinks=SINKS + 2), INVALID),
+    (dict(lay=None), INVALID), (dict(lay=(256, 64, 60, 256, 64, 64)), INVALID), (dict(lay=(0, 64, 64, 256, 64, 64)), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID), (dict(causal=3), INVALID), (dict(causal=-1), INVALID),
+    (dict(causal=1), UNSUPPORTED), (dict(Hq=3), INVALID), (dict(Hq=0), INVALID), (dict(B=0), INVALID), (dict(Lq=0), INVALID),
+    (dict(B=65536), UNSUPPORTED), (dict(Hq=70000), UNSUPPORTED), (dict(dtype=0), UNSUPPORTED), (dict(D=80), UNSUPPORTED),
+    (dict(page_size=20), INVALID), (dict(pages_stride=2), INVALID), (dict(data=0), INVALID),
+    (dict(out=Q), INVALID), (dict(lse=OUT), INVALID), (dict(out=DATA), INVALID), (dict(out=SINKS - 16), INVALID), (dict(lse=TABLE), INVALID),
+    (dict(out=LENS), INVALID),
+])
+def test_refused(kw, code):
+    a = dict(GOOD, q=Q, out=OUT, lse=LSE, sinks=SINKS, lay=(256, 64, 64, 256, 64, 64), B=2, Hq=4, Lq=1, scale=0.125, causal=2, ws=WS, ws_bytes=1 << 26)
+    a.update(kw)
+    build.build()
+    c = _lib.Cache(*(a[n] for n in GOOD))
+    lay = None if a["lay"] is None else _lib.Int64x6(*a["lay"])
+    assert _lib.sdpa_cache_attn(c, a["q"], a["out"], a["lse"], a["sinks"], lay, a["B"], a["Hq"], a["Lq"], a["scale"], a["causal"], 0, a["ws"],
+                                a["ws_bytes"], None) == code
+
+
+def test_oracle_rows_that_see_nothing():
+    q = np.ones((1, 2, 3, 32))
+    empty = [np.zeros((1, 0, 32))]
+    o, lse = ref.cached_attention(q, empty, empty, 0.1, True)
+    assert not o.any() and np.isneginf(lse).all()
+    one = [np.full((1, 1, 32), 2.0)]
+    o, lse = ref.cached_attention(q, one, one, 0.1, True, np.array([0.5, -np.inf]))
+    assert not o[:, :, :2].any() and (lse[0, 0, :2] == 0.5).all() and np.isneginf(lse[0, 1, :2]).all()
+    assert np.allclose(o[0, 1, 2], 2.0) and np.allclose(lse[0, 1, 2], 6.4)
+
+
+# ---- on the GPU
+
+CASES = [
+    # dtype, Hq, Hkv, L, D, page, lens
+    ("bf16", 1, 1, 1, 64, 16, [1]),
+    ("f16", 4, 4, 1, 32, 16, [15, 16, 17, 0]),
+    ("bf16", 8, 2, 1, 128, 16, [33, 1, 250]),
+    ("f16", 7, 1, 1, 96, 48, [100, 47, 48, 49]),
+    ("bf16", 4, 1, 1, 256, 64, [129, 64]),
+    ("bf16", 8, 1, 1, 64, 32, [300]),
+    ("f16", 16, 2, 2, 128, 16, [2, 1, 65, 127]),          # 16 rows a head, the second before the start
+    ("bf16", 8, 2, 8, 128, 64, [200, 8, 3, 0]),           # 32 rows
+    ("bf16", 6, 2, 5, 96, 32, [77, 32, 4]),
+    ("f16", 8, 2, 3, 32, 16, [500, 31]),
+    ("f16", 4, 2, 6, 256, 16, [90, 6]),
+    ("bf16", 4, 1, 11, 128, 16, [40, 70]),                # 44 rows a head: more than one block's
+    ("f16", 3, 3, 40, 64, 16, [64, 39]),
+    ("bf16", 32, 8, 1, 128, 64, [1500, 700, 1029, 64]),
+    ("f16", 12, 3, 1, 64, 112, [3333]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("dtype,Hq,Hkv,L,D,page,lens", CASES)
+def test_attention(dtype, Hq, Hkv, L, D, page, lens, sinks, causal):
+    rng = np.random.default_rng(1000 * L + D + len(lens))
+    cache, table, ks, vs, low = fill(rng, lens, Hkv, D, page, dtype)
+    q = draw_rows(rng, (len(lens), Hq, L, D), dtype, 1.5)
+    sink = None
+    if sinks:
+        sink = rng.standard_normal(Hq).astype(np.float32) + 2
+        sink[0] = 30.0 if Hq > 1 else sink[0]
+        sink[-1] = -np.inf if Hq > 2 else sink[-1]
+    args = (cache, table.cuda(), ints(lens).cuda())
+    how = dict(need_lse=True, is_causal="bottom_right" if causal else False, sinks=None if sink is None else torch.from_numpy(sink).cuda())
+    out, lse = api.cache_attention(q.cuda(), *args, **how)
+    api.poll_status()
+    scale = 1 / math.sqrt(D)
+    check(out, lse, q, ks, vs, low, scale, causal, sink, dtype)
+    # A tight bound on the lengths gives the same, bit for bit or within the same tolerances.
+    out, lse = api.cache_attention(q.cuda(), *args, max_len=max(max(lens), 1), **how)
+    api.poll_status()
+    check(out, lse, q, ks, vs, low, scale, causal, sink, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_scales(dtype, scale):
+    rng = np.random.default_rng(21)
+    cache, table, ks, vs, low = fill(rng, [90, 17], 2, 64, 16, dtype)
+    q = draw_rows(rng, (2, 4, 2, 64), dtype, 0.4)
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([90, 17]).cuda(), scale=scale, need_lse=True)
+    api.poll_status()
+    check(out, lse, q, ks, vs, low, scale, True, None, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,sizes", [("bf16", (1e-20, 1e20)), ("bf16", (1e-3, 1e3)), ("f16", (1e-4, 500.0))])
+def test_values_of_any_size(dtype, sizes):
+    """Queries and values far from 1, and values whose scale changes by token and by group (the
+    keys stay plain, scaled against the queries' size)."""
+    rng = np.random.default_rng(22)
+    lens, H, D, page = [150], 1, 128, 16
+    for size in sizes:
+        table, pages = make_table(rng, lens, page)
+        cache = dirty_cache(pages, H, page, D, dtype)
+        k, v = (draw_rows(rng, (1, H, 150, D), dtype) for _ in range(2))
+        v = (v.double() * size * torch.from_numpy(np.exp2(rng.integers(-8, 5, (1, H, 150, 1))))).to(v.dtype)
+        v[..., :32] *= 0.03
+        q = (draw_rows(rng, (1, 4, 1, D), dtype).double() * size).to(v.dtype)
+        api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints(lens).cuda())
+        out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True, scale=0.1 / size)
+        api.poll_status()
+        code, s, z = ref.quantise(as_f64(v)[0], TYPES[dtype])
+        ks, vs, low = [held(as_f64(k)[0], dtype)], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
+        check(out, lse, q, ks, vs, low, float(np.float32(0.1 / size)), True, None, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_what_is_hidden_cannot_be_seen(dtype):
+    """NaN keys and values at positions behind a query's own leave it alone; the query that sees
+    them is NaN.  (The unused places of every cache of these tests are NaN as well.)"""
+    rng = np.random.default_rng(23)
+    lens, H, L, D, page = [53, 20], 2, 4, 64, 16
+    table, pages = make_table(rng, lens, page)
+    cache = dirty_cache(pages, H, page, D, dtype)
+    k, v = (draw_rows(rng, (2, H, 53, D), dtype) for _ in range(2))
+    k[:, :, -1, 5], v[:, :, -2, 40] = float("nan"), float("inf")
+    q = draw_rows(rng, (2, 4, L, D), dtype)
+    api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints(lens).cuda())
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True)
+    api.poll_status()
+    assert torch.isnan(out[:, :, 3]).all() and torch.isnan(lse[:, :, 3]).all()
+    assert torch.isnan(out[:, :, 2, 32:]).all() and not torch.isnan(out[:, :, 2, :32]).any()
+    ks = [held(as_f64(k)[b, :, 53 - n:53 - 2], dtype) for b, n in enumerate(lens)]
+    code = [ref.quantise(as_f64(v)[b, :, 53 - n:53 - 2], TYPES[dtype]) for b, n in enumerate(lens)]
+    vs = [ref.values(*c) for c in code]
+    low = [ref.values(c, s, np.zeros_like(z)) for c, s, z in code]
+    check(out[:, :, :2], lse[:, :, :2].contiguous(), q[:, :, :2], ks, vs, low, 1 / 8, True, None, dtype)
+
+
+@pytest.mark.gpu
+def test_a_query_that_is_not_finite_stays_alone():
+    rng = np.random.default_rng(24)
+    cache, table, ks, vs, low = fill(rng, [70], 1, 128, 16, "bf16")
+    q = draw_rows(rng, (1, 8, 1, 128), "bf16")
+    clean, _ = api.cache_attention(q.cuda(), cache, table.cuda(), ints([70]).cuda())
+    q[0, 3, 0, 17], q[0, 6, 0, 100] = float("nan"), float("inf")
+    out, _ = api.cache_attention(q.cuda(), cache, table.cuda(), ints([70]).cuda())
+    api.poll_status()
+    rows = [0, 1, 2, 4, 5, 7]
+    assert torch.equal(out[:, rows], clean[:, rows]) and torch.isnan(out[:, [3, 6]]).all()
+
+
+@pytest.mark.gpu
+def test_bad_pages_and_lengths():
+    """Tokens on pages outside the cache are hidden, lengths are cut, both are reported."""
+    rng = np.random.default_rng(25)
+    lens = [60, 60, 40]
+    cache, table, ks, vs, low = fill(rng, lens, 2, 64, 16, "bf16", width=4)
+    q = draw_rows(rng, (3, 4, 1, 64), "bf16")
+    table[0, 1], table[1, 2] = -1, cache.shape[0]
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True, is_causal=False)
+    with pytest.raises(_lib.SdpaError) as e:
+        api.poll_status()
+    assert e.value.status == INDEX
+    gone = {0: (16, 32), 1: (32, 48)}
+    for x in (ks, vs, low):
+        for b, (lo, hi) in gone.items():
+            x[b] = np.concatenate([x[b][:, :lo], x[b][:, hi:]], 1)
+    check(out, lse, q, ks, vs, low, 1 / 8, False, None, "bf16")
+    # Lengths below 0 and above max_len.
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([-3, -2**31, 40]).cuda(), need_lse=True, is_causal=False, max_len=24)
+    with pytest.raises(_lib.SdpaError):
+        api.poll_status()
+    none = [np.zeros((2, 0, 64))] * 2
+    check(out, lse, q, none + [ks[2][:, :24]], none + [vs[2][:, :24]], none + [low[2][:, :24]], 1 / 8, False, None, "bf16")
+    api.poll_status()
+
+
+@pytest.mark.gpu
+def test_layouts_and_another_stream():
+    rng = np.random.default_rng(26)
+    lens = [100, 37]
+    cache, table, *_ = fill(rng, lens, 2, 128, 16, "bf16")
+    table, lens = table.cuda(), ints(lens).cuda()
+    fused = draw_rows(rng, (2, 3, 12, 128), "bf16").cuda()
+    q = fused[:, :, 2:10].transpose(1, 2)                               # [B, H, L, D] out of [B, L, H, D]
+    want, want_lse = api.cache_attention(q.contiguous(), cache, table, lens, need_lse=True)
+    out = torch.full((2, 3, 12, 128), 7.0, dtype=q.dtype, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, lse = api.cache_attention(q, cache, table, lens, need_lse=True, out=out[:, :, 2:10].transpose(1, 2), stream=side)
+    side.synchronize()
+    api.poll_status()
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    assert (out[:, :, :2] == 7).all() and (out[:, :, 10:] == 7).all()
+
+
+@pytest.mark.gpu
+def test_long_sequences_and_the_workspace():
+    """A length that is split over many blocks, a workspace of the caller's, run-to-run equality,
+    and nothing written behind the outputs or the workspace."""
+    rng = np.random.default_rng(27)
+    lens, Hq, Hkv, D = [9000, 513], 4, 1, 128
+    cache, table, ks, vs, low = fill(rng, lens, Hkv, D, 64, "bf16")
+    table, dev = table.cuda(), ints(lens).cuda()
+    q = draw_rows(rng, (2, Hq, 2, D), "bf16")
+    c = api._cache(cache, table, dev, 2)
+    need = _lib.sdpa_cache_attn_workspace_size(c, 2, Hq, 2, 0)
+    band = torch.full((need + 256,), 113, dtype=torch.uint8, device="cuda")
+    outs = torch.full((2 * Hq * 2 * D + 64,), 5.0, dtype=q.dtype, device="cuda")
+    out = outs[:2 * Hq * 2 * D].view(2, Hq, 2, D)
+    lses = torch.full((2 * Hq * 2 + 16,), 5.0, device="cuda")
+    lse = lses[:2 * Hq * 2].view(2, Hq, 2)
+    got = api.cache_attention(q.cuda(), cache, table, dev, need_lse=True, out=out, lse=lse, workspace=band[:need])
+    api.poll_status()
+    check(*got, q, ks, vs, low, 1 / math.sqrt(D), True, None, "bf16")
+    assert (band[need:] == 113).all() and (outs[out.numel():] == 5).all() and (lses[lse.numel():] == 5).all()
+    again, _ = api.cache_attention(q.cuda(), cache, table, dev)
+    assert torch.equal(again, out)
+    if need:
+        with pytest.raises(_lib.SdpaError) as e:
+            api.cache_attention(q.cuda(), cache, table, dev, workspace=band[:need - 16])
+        assert e.value.status == WORKSPACE
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    cache = api.cache_empty(4, 2, 16, 64)
+    q = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table, lens = ints([[0]]).cuda(), ints([3]).cuda()
+    for kw in (dict(q=q.half()), dict(q=q[..., :32]), dict(q=q[0]), dict(out=q[:, :2]), dict(need_lse=True, lse=torch.zeros(1, 4, 2, device="cuda")),
+               dict(sinks=torch.zeros(3, device="cuda")), dict(is_causal=5), dict(pages=table.long()), dict(lens=lens.cpu())):
+        with pytest.raises(ValueError):
+            api.cache_attention(**dict(dict(q=q, cache=cache, pages=table, lens=lens), **kw))
+    with pytest.raises(_lib.SdpaError):
+        api.cache_attention(q, cache, table, lens, is_causal=True)
+    with pytest.raises(_lib.SdpaError):
+        api.cache_attention(q[:, :3], cache, table, lens)
+
+
+@pytest.mark.gpu
+def test_decoding_steps_in_a_graph():
+    """Rotary, write and attention of one decoding step, captured once and replayed for several
+    steps of a padded batch, against the oracle on everything written so far."""
+    rng = np.random.default_rng(28)
+    B, Hq, Hkv, D, page, start, steps = 3, 8, 2, 64, 16, [30, 0, 13], 5
+    inv = (10000.0 ** (-np.arange(D // 2) / (D // 2))).astype(np.float32)
+    dev_inv = torch.from_numpy(inv).cuda()
+    width = 3
+    table, pages = make_table(rng, [n + steps for n in start], page, width)
+    table = table.cuda()
+    cache = dirty_cache(pages, Hkv, page, D, "bf16")
+    # The prompts: left-padded to 30, rotated by each token's position.
+    L = max(start)
+    pos = np.array(start)[:, None] - L + np.arange(L)
+    k, v = (draw_rows(rng, (B, Hkv, L, D), "bf16") for _ in range(2))
+    ko, _ = api.rotary(k.cuda(), None, torch.from_numpy(pos).cuda(), dev_inv)
+    api.cache_write(cache, ko, v.cuda(), table, ints(start).cuda())
+    ks = [held(as_f64(ko)[b, :, L - n:], "bf16") for b, n in enumerate(start)]
+    vq = [ref.quantise(as_f64(v)[b, :, L - n:], torch.bfloat16) for b, n in enumerate(start)]
+    vs, low = [ref.values(*x) for x in vq], [ref.values(c, s, np.zeros_like(z)) for c, s, z in vq]
+    q1 = torch.zeros(B, Hq, 1, D, dtype=torch.bfloat16, device="cuda")
+    k1, v1 = (torch.zeros(B, Hkv, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lens = ints(start).cuda()
+
+    def step():
+        lens.add_(1)
+        q2, k2 = api.rotary(q1, k1, (lens - 1).view(B, 1), dev_inv)
+        api.cache_write(cache, k2, v1, table, lens)
+        return q2, k2, *api.cache_attention(q2, cache, table, lens, need_lse=True)
+
+    with torch.cuda.stream(torch.cuda.Stream()):                       # a first run, taken back
+        step()
+        lens.sub_(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q2, k2, out, lse = step()
+    for n in range(steps):
+        for x in (q1, k1, v1):
+            x.copy_(draw_rows(rng, tuple(x.shape), "bf16"))
+        graph.replay()
+        api.poll_status()
+        assert lens.tolist() == [x + n + 1 for x in start]
+        position = np.array([[[x + n] for x in start]])
+        turned = ref.rotary(as_f64(k1), position, inv)
+        assert np.abs(as_f64(k2) - turned).max() <= 2.0**-8 * np.abs(turned).max() + 1e-5
+        for b in range(B):
+            ks[b] = np.concatenate([ks[b], held(as_f64(k2)[b], "bf16")], 1)
+            code, s, z = ref.quantise(as_f64(v1)[b], torch.bfloat16)
+            vs[b] = np.concatenate([vs[b], ref.values(code, s, z)], 1)
+            low[b] = np.concatenate([low[b], ref.values(code, s, np.zeros_like(z))], 1)
+        check(out, lse, q2, ks, vs, low, 1 / 8, True, None, "bf16")
+
+
+@pytest.mark.gpu
+def test_two_graphs_on_their_own_workspaces():
+    """Two captured calls replayed at once on two streams give what each gives alone."""
+    rng = np.random.default_rng(29)
+    lens = [5000]
+    cache, table, *_ = fill(rng, lens, 1, 128, 64, "bf16")
+    table, dev = table.cuda(), ints(lens).cuda()
+    qs = [draw_rows(rng, (1, 4, 1, 128), "bf16").cuda() for _ in range(2)]
+    want = [api.cache_attention(q, cache, table, dev)[0] for q in qs]
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(api.cache_attention(q, cache, table, dev)[0])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    api.poll_status()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.gpu
+def test_a_chunk_through_the_tiled_kernels():
+    """A prompt in two chunks: the second reads the prefix back and runs the tiled attention,
+    bottom-right causal, and agrees with the attention over the cache."""
+    rng = np.random.default_rng(30)
+    H, D, n, L = 2, 128, 200, 72
+    cache, table, ks, vs, low = fill(rng, [n], H, D, 16, "bf16")
+    q = draw_rows(rng, (1, 2 * H, L, D), "bf16")
+    k, v = api.cache_read(cache, table.cuda(), ints([n]).cuda(), n)
+    tiled, _ = api.attention_forward(q.cuda(), k, v, is_causal="bottom_right")
+    direct, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda(), need_lse=True)
+    api.poll_status()
+    check(direct, lse, q, ks, vs, low, 1 / math.sqrt(D), True, None, "bf16")
+    o, _ = oracle.sdpa_forward(as_f64(q), as_f64(k), as_f64(v), 1 / math.sqrt(D), 2)
+    assert np.abs(as_f64(tiled) - o).max() <= 8e-3
+
+
+@pytest.mark.gpu
+def test_a_training_step():
+    """Rotary with two axes, then the attention, differentiated through both."""
+    rng = np.random.default_rng(31)
+    B, Hq, Hkv, L, D = 1, 4, 2, 50, 64
+    q, k, v, g = (torch.from_numpy(rng.standard_normal((B, H, L, D))).float() for H in (Hq, Hkv, Hkv, Hq))
+    positions, axes = rng.integers(0, 40, (2, B, L)), np.array([0] * 10 + [1] * 22, dtype=np.int32)
+    inv = (100.0 ** (-np.arange(32) / 32)).astype(np.float32)
+    leaves = [x.cuda().requires_grad_() for x in (q, k, v)]
+    args = (torch.from_numpy(positions).cuda(), torch.from_numpy(inv).cuda(), torch.from_numpy(axes).cuda())
+    q2, k2 = autograd.rotary_embedding(leaves[0], leaves[1], *args)
+    out = autograd.scaled_dot_product_attention(q2, k2, leaves[2], is_causal=True, enable_gqa=True)
+    out.backward(g.cuda())
+    api.poll_status()
+    qr, kr = (ref.rotary(as_f64(x), positions, inv, axes) for x in (q, k))
+    o, _ = oracle.sdpa_forward(qr, kr, as_f64(v), 1 / 8, 1)
+    dq, dk, dv = oracle.sdpa_backward(qr, kr, as_f64(v), as_f64(g), 1 / 8, 1)
+    dq, dk = (ref.rotary(x, positions, inv, axes, inverse=True) for x in (dq, dk))
+    assert np.abs(as_f64(out.detach()) - o).max() <= 1e-5
+    for x, want in zip(leaves, (dq, dk, dv)):
+        assert np.abs(as_f64(x.grad) - want).max() <= 1e-4
