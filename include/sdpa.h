@@ -425,7 +425,8 @@ typedef enum {
   SDPA_KERNEL_CACHE_WRITE = 8,
   SDPA_KERNEL_CACHE_READ = 9,
   SDPA_KERNEL_CACHE_ATTN = 10, /* attention over the 4-bit cache */
-  SDPA_KERNEL_COUNT = 11
+  SDPA_KERNEL_CACHE_JOIN = 11, /* its second kernel, where a sequence is split */
+  SDPA_KERNEL_COUNT = 12
 } sdpa_kernel_t;
 int sdpa_timing_enable(int on);
 int sdpa_timing_read(int kernel, double* total_ms, uint64_t* launches);

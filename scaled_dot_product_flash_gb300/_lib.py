@@ -100,7 +100,8 @@ SIGNATURES = {
 }
 BWD_NOALLOC_MAX_ROWS = 1 << 20
 KERNELS = {"fwd": 0, "delta": 1, "dq": 2, "dkdv": 3, "vec_fwd": 4, "vec_bwd": 5, "sink_grad": 6,
-           "rotary": 7, "cache_write": 8, "cache_read": 9, "cache_attn": 10}
+           "rotary": 7, "cache_write": 8, "cache_read": 9, "cache_attn": 10,
+           "cache_join": 11}
 
 _lib = None
 

@@ -58,8 +58,10 @@ struct CacheAttnArgs {
   float* workspace;
   uint64_t wait_limit_ns;
 };
-size_t cache_attn_workspace(const CacheAttnArgs& a);
+size_t cache_attn_workspace(const CacheAttnArgs& a);  // 0: one kernel does it all
+int cache_attn_row_tiles(const CacheAttnArgs& a);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_join(const CacheAttnArgs& a, int dtype, cudaStream_t s);  // after it, with a workspace
 
 constexpr int kTile = 16;   // tokens a tile
 constexpr int kGroup = 32;  // elements that share a scale and a zero

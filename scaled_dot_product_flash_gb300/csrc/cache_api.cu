@@ -208,6 +208,7 @@ int check_attn(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len, Ca
   a->G = Hq / a->c.Hkv;
   const int table = a->c.pages_per_seq * a->c.page_size;
   a->max_len = max_len <= 0 || max_len > table ? table : max_len;
+  if ((double)a->c.Hkv * cache_attn_row_tiles(*a) > 65535.0) return SDPA_ERR_UNSUPPORTED;
   return SDPA_OK;
 }
 
@@ -256,5 +257,7 @@ extern "C" int sdpa_cache_attn(const sdpa_cache_t* cache, const void* q, void* o
   a.wait_limit_ns = wait_limit_ns();
   if ((st = error_word(&a.c.err)) != SDPA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return status_of(launch_one(SDPA_KERNEL_CACHE_ATTN, s, [&] { return launch_cache_attn(a, cache->dtype, s); }));
+  const cudaError_t e = launch_one(SDPA_KERNEL_CACHE_ATTN, s, [&] { return launch_cache_attn(a, cache->dtype, s); });
+  if (e != cudaSuccess || !need) return status_of(e);
+  return status_of(launch_one(SDPA_KERNEL_CACHE_JOIN, s, [&] { return launch_cache_join(a, cache->dtype, s); }));
 }

@@ -1,112 +1,671 @@
 // Attention over a 4-bit paged cache (format and conventions in include/sdpa.h).
 //
-// One warp a query row: 32 keys at a time, a key a lane for the scores, the running maximum
-// and sum of the softmax, then the head dimension over the lanes for the values.
+// Rows.  The G·L query rows of a KV head (row r = query r % L of head r / L of the group) are
+// cut into row tiles of 8·NT; a block takes one row tile and one chunk of the sequence, and
+// its warps take units of UT tiles (16 tokens each) of that chunk in turn.  Chunks' partial
+// results are joined by a second kernel; a sequence of one chunk needs none.
+//
+// Bound.  5 bits an element from HBM, 1.25·D bytes a token and KV head; everything between
+// that and the result is made cheap enough to hide behind it:
+//  - A tile is stored in the order in which the lanes of a warp read MMA fragments, so each
+//    warp streams its tiles into a shared-memory ring of its own with plain bulk copies (one
+//    per tile, issued a few units ahead, no tensor map, no block barrier) and reads fragments
+//    with 16-byte loads.
+//  - Codes are not converted.  A nibble masked in place is a subnormal fp16 number, code·2^-24
+//    or, one nibble higher, 16·code·2^-24, which the tensor cores multiply exactly: one AND
+//    gives two operands (5 instructions for 8 codes).  The factors 16 and 2^-24 are undone in
+//    q, in the output and in fp32 scales.
+//  - The product is transposed, S^T = K·Q^T and O^T = V^T·P^T (m16n8k16), so that the cache is
+//    the 16-row operand and 8 query rows fill the other one.
+//  - Scales stay outside the products: S = sum_j s_j·(c_j·q_j) + sum_j z_j·sum(q_j) over the
+//    groups j, the first in fp32 FMAs over one accumulator a group, the second as one MMA in
+//    the element type whose q sums are split in three so that nothing is lost.  For the values
+//    the probabilities take the scale, P·s in fp16 (normalised by a power of two that follows
+//    the largest scale, rounded once, 2^-11 relative); P·z is summed in fp32 FMAs.
+//    So scores are exact up to fp32 sums, and P·s is the only rounding to fewer bits.
 #include "cache.h"
+#include "tc_common.cuh"
 
 namespace sdpa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 
-template <typename T, int D>
-__device__ __forceinline__ float cached(const uint8_t* tile, bool value, int r, int d) {
+template <int D, int NT>
+struct Cfg {
   using Tl = Tile<D>;
-  const int j = d / kGroup, e = d % kGroup;
-  uint32_t code, param;
-  if (value) {
-    code = (reinterpret_cast<const uint16_t*>(tile + Tl::kV)[Tl::v_half(r, e / 4, j)] >> (4 * (e % 4))) & 15u;
-    param = reinterpret_cast<const uint32_t*>(tile + Tl::kVp)[Tl::param(r, j)];
+  static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
+  static constexpr int kUnit = UT * kTile;                   // tokens a unit
+  static constexpr int kStages = 2;
+  static constexpr int kUnitBytes = UT * Tl::kBytes;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kRing = kWarps * kStages * kUnitBytes;
+  static constexpr int kMerge = kWarps * 8 * (D + 4) * 4;  // 8 rows of every warp's output
+  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kQ = NT > 1 ? NT * (D / kGroup) * 32 * 16 : 0;  // q fragments
+  static constexpr int kSmem = kBody + kQ;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* p) {
+  if constexpr (W == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+  } else if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x; r[1] = v.y;
   } else {
-    code = (reinterpret_cast<const uint32_t*>(tile + Tl::kK)[Tl::k_word(r, e / 8, j)] >> (4 * (e % 8))) & 15u;
-    param = reinterpret_cast<const uint32_t*>(tile + Tl::kKp)[Tl::param(r, j)];
+#pragma unroll
+    for (int w = 0; w < W; ++w) r[w] = reinterpret_cast<const uint32_t*>(p)[w];
   }
-  return fmaf(bits_to_f<T>(param & 0xffffu), (float)code, bits_to_f<T>(param >> 16));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) cache_attn_kernel(CacheAttnArgs a) {
-  __shared__ float qs[kWarps][D];
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+// Tokens that some row of row tile `rt` (rows a tile) sees: those before this position.
+__device__ __forceinline__ int tile_end(const CacheAttnArgs& a, int len, int rt, int rows) {
+  if (!a.causal) return len;
+  const int R = a.G * a.c.L, r0 = rt * rows, n = min(rows, R - r0), i0 = r0 % a.c.L;
+  const int last = i0 + n >= a.c.L ? a.c.L - 1 : i0 + n - 1;  // the latest query among them
+  return max(0, len - a.c.L + last + 1);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kernel(CacheAttnArgs a, int chunk, int splits, int row_tiles) {
+  using C = Cfg<D, NT>;
+  using Tl = Tile<D>;
+  constexpr int NG = Tl::NG, W = Tl::W, JB = Tl::JB, UT = C::UT;
+  constexpr bool kQSmem = NT > 1;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kWarps][C::kStages];
+  __shared__ float stat[kWarps][C::kRows][2];
+  __shared__ int abort_flag;
   const CacheArgs& c = a.c;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
-  if (row >= (int64_t)c.B * a.Hq * c.L) return;
-  const int i = (int)(row % c.L), hq = (int)(row / c.L % a.Hq), b = (int)(row / c.L / a.Hq), h = hq / a.G;
-  const T* q = row_ptr<T>(a.q, a.lq, b, hq, i);
-  for (int d = lane; d < D; d += 32) qs[warp][d] = Elem<T>::to_f(q[d]);
-  __syncwarp();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int split = blockIdx.x, rt = blockIdx.y % row_tiles, h = blockIdx.y / row_tiles, b = blockIdx.z;
   const int len = cache_len(c, b, a.max_len, kKidCacheAttn);
-  const int end = a.causal ? len - c.L + i + 1 : len;
-  float m = minus_inf(), l = 0.f, o[D / 32];
+  const int end_all = tile_end(a, len, rt, C::kRows);
+  const int64_t first = (int64_t)split * chunk;
+  if (first >= end_all && splits > 1) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    return;
+  }
+  const int start = (int)first, end = (int)min((int64_t)end_all, first + chunk);
+  const int units = end > start ? (end - start + C::kUnit - 1) / C::kUnit : 0;
+
+  if (lane < C::kStages) tc::mbar_init(&full[warp][lane], 1);
+  if (threadIdx.x == 0) abort_flag = 0;
+  tc::fence_mbar_init();
+  __syncthreads();
+  const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidCacheAttn};
+
+  uint8_t* ring = smem + warp * (C::kStages * C::kUnitBytes);
+  uint32_t there = 0;  // bit s·UT + tile: the tile in stage s was copied
+  // Starts the copies of unit u into stage s (all lanes call it).
+  auto issue = [&](int u, int s) {
+    const int pos = start + u * C::kUnit + lane * kTile;
+    int page = -1;
+    if (lane < UT && pos < end) page = cache_page(c, b, pos, kKidCacheAttn);
+    const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+    there = (there & ~(((1u << UT) - 1) << (s * UT))) | (ok << (s * UT));
+    if (lane == 0) tc::mbar_arrive_expect_tx(&full[warp][s], __popc(ok) * Tl::kBytes);
+    __syncwarp();
+    if (page >= 0)
+      bulk_copy(ring + s * C::kUnitBytes + lane * Tl::kBytes, cache_tile<D>(c, page, h, pos % c.page_size / kTile), Tl::kBytes, &full[warp][s]);
+  };
+  int issued = warp;  // next unit to start
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  for (int j0 = 0; j0 < end; j0 += 32) {
-    const int pos = j0 + lane;
-    const uint8_t* tile = nullptr;
-    if (pos < end) {
-      const int page = cache_page(c, b, pos, kKidCacheAttn);
-      if (page >= 0) tile = cache_tile<D>(c, page, h, pos % c.page_size / kTile);
+  for (int s = 0; s < C::kStages; ++s)
+    if (issued < units) {
+      issue(issued, s);
+      issued += kWarps;
     }
-    float s = minus_inf();
-    if (tile) {
-      float acc = 0.f;
-      for (int d = 0; d < D; ++d) acc = fmaf(qs[warp][d], cached<T, D>(tile, false, pos % kTile, d), acc);
-      s = acc * a.scale_log2;
+
+  // Query rows as the B operand: lane (g, t) holds, of row g and each group, elements 8t..8t+7,
+  // times a power of two that brings the row's largest to 2^13..2^14 (exact in fp16 down to
+  // 2^-27 of that); the odd nibbles' elements are divided by the 16 that their codes carry.
+  uint32_t qf[kQSmem ? 1 : NG][4];
+  uint4* qs = reinterpret_cast<uint4*>(smem + C::kBody);
+  uint32_t qz[NT][JB][2];  // group sums of the row, split in three (z term)
+  float f[NT][2];          // per column 2t, 2t+1: scale·log2e·2^(24 - e)
+  int lim[NT][2];          // per column: positions below this are visible
+  const int R = a.G * c.L, row0 = rt * C::kRows;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + 8 * nt + g;
+    float x[NG][8];
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r < R) w = *reinterpret_cast<const uint4*>(row_ptr<T>(a.q, a.lq, b, h * a.G + r / c.L, r % c.L) + 32 * j + 8 * t);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[j][e] = bits_to_f<T>((ws[e / 2] >> (16 * (e & 1))) & 0xffffu);
+        top = fmaxf(top, fabsf(x[j][e]));
+      }
     }
-    float top = s;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^e·top in [2^13, 2^14).  A row of zeros (or subnormals) takes 2^100, an infinite one
+    // 2^-100 and turns NaN by itself.
+    const int e = max(-100, min(100, 13 - ((__float_as_int(top) >> 23) - 127)));
+    const float up = pow2(e);
+    float sums[JB] = {};
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float m_new = fmaxf(m, top), ref = m_new == minus_inf() ? 0.f : m_new;
-    const float alpha = exp2f(m - ref), p = exp2f(s - ref);
-    float sum = p;
+    for (int j = 0; j < NG; ++j) {
+      float sum = 0.f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    l = l * alpha + sum;
-    m = m_new;
+      for (int n = 0; n < 8; ++n) {
+        x[j][n] *= up;
+        sum += x[j][n];
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (j % 4 == t) sums[j / 4] = sum;
+      const uint32_t f0 = pack_h2(x[j][0], x[j][4]), f1 = pack_h2(x[j][1] * 0.0625f, x[j][5] * 0.0625f);
+      const uint32_t f2 = pack_h2(x[j][2], x[j][6]), f3 = pack_h2(x[j][3] * 0.0625f, x[j][7] * 0.0625f);
+      if constexpr (kQSmem) {
+        if (warp == 0) qs[(j * NT + nt) * 32 + lane] = make_uint4(f0, f1, f2, f3);
+      } else {
+        qf[j][0] = f0; qf[j][1] = f1; qf[j][2] = f2; qf[j][3] = f3;
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] *= alpha;
-    for (int jj = 0; jj < 32; ++jj) {
-      const uint8_t* t = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(tile), jj));
-      const float pj = __shfl_sync(0xffffffffu, p, jj);
-      if (!t) continue;
+    for (int jb = 0; jb < JB; ++jb) {  // sums·2^-6 = hi + mid + lo in T (at most 2^13)
+      const float s6 = sums[jb] * 0.015625f;
+      const uint32_t hi = f_to_bits<T>(s6);
+      const float rest = s6 - bits_to_f<T>(hi);
+      const uint32_t mid = f_to_bits<T>(rest);
+      qz[nt][jb][0] = hi | (mid << 16);
+      qz[nt][jb][1] = f_to_bits<T>(rest - bits_to_f<T>(mid));
+    }
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(pj, cached<T, D>(t, true, (j0 + jj) % kTile, lane + 32 * e), o[e]);
+    for (int n = 0; n < 2; ++n) {  // the accumulators' columns are rows 2t and 2t + 1
+      const int src = __shfl_sync(0xffffffffu, e, (2 * t + n) * 4);
+      f[nt][n] = a.scale_log2 * pow2(24 - src);
+      const int rr = row0 + 8 * nt + 2 * t + n;
+      lim[nt][n] = a.causal ? len - c.L + rr % c.L + 1 : len;
     }
   }
-  const float fold = fold_sink(a.sinks, hq, m, l);
-  T* out = row_ptr<T>(a.out, a.lo, b, hq, i);
+  if constexpr (kQSmem) __syncthreads();
+  const int seen = a.causal ? len - c.L + 1 : len;  // every row sees the positions below this
+
+  float o[2 * NG][NT][4];  // O^T, times 2^(k - 24)
+  float zo[NT][NG][2];     // this lane's keys' P·z
+  float m[NT][2], l[NT][2];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) out[lane + 32 * e] = Elem<T>::from_f(l == 0.f ? 0.f : o[e] * fold / l);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? minus_inf() : (m + log2f(l)) * kLn2;
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < 2 * NG; ++j) o[j][nt][0] = o[j][nt][1] = o[j][nt][2] = o[j][nt][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) zo[nt][j][0] = zo[nt][j][1] = 0.f;
+    m[nt][0] = m[nt][1] = minus_inf();
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+  int k = 120;  // P·s enters the MMA times 2^k
+
+  bool ok = true;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int u = warp; u < units; u += kWarps) {
+    ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[warp][s], parity, wc));
+    if (!ok) break;
+    const uint8_t* st = ring + s * C::kUnitBytes;
+    const int key0 = start + u * C::kUnit;
+    const uint32_t tiles = (there >> (s * UT)) & ((1u << UT) - 1);
+    const bool masked = key0 + C::kUnit > min(seen, end) || tiles != (1u << UT) - 1;
+
+    // ---- scores
+    float sc[UT][NT][4];
+#pragma unroll
+    for (int ti = 0; ti < UT; ++ti) {
+      const uint8_t* tile = st + ti * Tl::kBytes;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[ti][nt][0] = sc[ti][nt][1] = sc[ti][nt][2] = sc[ti][nt][3] = 0.f;
+#pragma unroll
+      for (int jb = 0; jb < JB; ++jb) {  // z of group 4·jb + t: (hi, mid) and (lo, nothing)
+        uint32_t z0 = 0, z1 = 0;
+        if (W == 4 || t < W) {
+          const uint32_t* zp = reinterpret_cast<const uint32_t*>(tile + Tl::kKp) + (jb * 16 + g) * W + t;
+          z0 = zp[0] >> 16;
+          z1 = zp[8 * W] >> 16;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[ti][nt][e] *= 0x1p-18f;
+    }
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb) {
+      uint32_t kw[UT][2][W], kp[UT][2][W];
+#pragma unroll
+      for (int ti = 0; ti < UT; ++ti)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint8_t* tile = st + ti * Tl::kBytes;
+          load_words<W>(kw[ti][hf], tile + Tl::kK + ((hf * JB + jb) * 32 + lane) * W * 4);
+          load_words<W>(kp[ti][hf], tile + Tl::kKp + (jb * 16 + g + 8 * hf) * W * 4);
+        }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int j = jb * W + w;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t qq[4];
+          if constexpr (kQSmem) {
+            const uint4 v = qs[(j * NT + nt) * 32 + lane];
+            qq[0] = v.x; qq[1] = v.y; qq[2] = v.z; qq[3] = v.w;
+          } else {
+            qq[0] = qf[j][0]; qq[1] = qf[j][1]; qq[2] = qf[j][2]; qq[3] = qf[j][3];
+          }
+#pragma unroll
+          for (int ti = 0; ti < UT; ++ti) {
+            const uint32_t x0 = kw[ti][0][w], x1 = kw[ti][1][w], y0 = x0 >> 8, y1 = x1 >> 8;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
+            mma<__half>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
+            const float s0 = bits_to_f<T>(kp[ti][0][w] & 0xffffu), s1 = bits_to_f<T>(kp[ti][1][w] & 0xffffu);
+            sc[ti][nt][0] = fmaf(s0, acc[0], sc[ti][nt][0]);
+            sc[ti][nt][1] = fmaf(s0, acc[1], sc[ti][nt][1]);
+            sc[ti][nt][2] = fmaf(s1, acc[2], sc[ti][nt][2]);
+            sc[ti][nt][3] = fmaf(s1, acc[3], sc[ti][nt][3]);
+          }
+        }
+      }
+    }
+
+    // ---- softmax: element e of a tile is key g + 8·(e / 2), column 2t + e % 2
+    bool grew = false;
+    float alpha[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float top = minus_inf();
+#pragma unroll
+        for (int ti = 0; ti < UT; ++ti)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float& x = sc[ti][nt][2 * hf + n];
+            x *= f[nt][n];
+            if (masked) {
+              const int pos = key0 + ti * kTile + g + 8 * hf;
+              if (pos >= min(lim[nt][n], end) || !((tiles >> ti) & 1)) x = minus_inf();
+            }
+            top = fmaxf(top, x);
+          }
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float m_new = fmaxf(m[nt][n], top);
+        alpha[nt][n] = m_new == minus_inf() ? 1.f : ex2(m[nt][n] - m_new);
+        grew = grew || m_new > m[nt][n];
+        m[nt][n] = m_new;
+      }
+    }
+    // The largest value scale of the unit fixes the power of two of P·s.
+    uint32_t vp[UT][2][NG];
+    uint32_t smax = 0;
+#pragma unroll
+    for (int ti = 0; ti < UT; ++ti)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int pos = key0 + ti * kTile + g + 8 * hf;
+        const bool there_key = !masked || (pos < end && ((tiles >> ti) & 1));
+#pragma unroll
+        for (int jb = 0; jb < JB; ++jb) load_words<W>(&vp[ti][hf][jb * W], st + ti * Tl::kBytes + Tl::kVp + (jb * 16 + g + 8 * hf) * W * 4);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          if (!there_key) vp[ti][hf][j] = 0;
+          smax = max(smax, vp[ti][hf][j] & 0xffffu);
+        }
+      }
+    smax = __reduce_max_sync(0xffffffffu, smax);  // scales are not negative: bits order them
+    const int k_new = min(k, min(120, 13 - ((__float_as_int(bits_to_f<T>(smax)) >> 23) - 127)));
+    if (__any_sync(0xffffffffu, grew) || k_new < k) {
+      const float down = k - k_new > 126 ? 0.f : pow2(k_new - k);
+      k = k_new;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float a0 = alpha[nt][0], a1 = alpha[nt][1], d0 = a0 * down, d1 = a1 * down;
+        l[nt][0] *= a0;
+        l[nt][1] *= a1;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          zo[nt][j][0] *= a0;
+          zo[nt][j][1] *= a1;
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * NG; ++j) {
+          o[j][nt][0] *= d0;
+          o[j][nt][1] *= d1;
+          o[j][nt][2] *= d0;
+          o[j][nt][3] *= d1;
+        }
+      }
+    }
+    const float up = pow2(k);
+#pragma unroll
+    for (int ti = 0; ti < UT; ++ti) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[nt][e & 1] == minus_inf() ? 0.f : m[nt][e & 1];
+          sc[ti][nt][e] = ex2(sc[ti][nt][e] - ref);
+          l[nt][e & 1] += sc[ti][nt][e];
+        }
+      // ---- values
+#pragma unroll
+      for (int jb = 0; jb < JB; ++jb) {
+        uint32_t vw[2][W];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) load_words<W>(vw[hf], st + ti * Tl::kBytes + Tl::kV + ((hf * JB + jb) * 32 + lane) * W * 4);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int j = jb * W + w;
+          const float s0 = bits_to_f<T>(vp[ti][0][j] & 0xffffu) * up, s1 = bits_to_f<T>(vp[ti][1][j] & 0xffffu) * up;
+          const float z0 = bits_to_f<T>(vp[ti][0][j] >> 16), z1 = bits_to_f<T>(vp[ti][1][j] >> 16);
+          const uint32_t x0 = vw[0][w], x1 = vw[1][w], y0 = x0 >> 8, y1 = x1 >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float (&p)[4] = sc[ti][nt];
+            if (masked) {  // a hidden key's z may be NaN
+              zo[nt][j][0] += (p[0] == 0.f ? 0.f : p[0] * z0) + (p[2] == 0.f ? 0.f : p[2] * z1);
+              zo[nt][j][1] += (p[1] == 0.f ? 0.f : p[1] * z0) + (p[3] == 0.f ? 0.f : p[3] * z1);
+            } else {
+              zo[nt][j][0] = fmaf(p[0], z0, fmaf(p[2], z1, zo[nt][j][0]));
+              zo[nt][j][1] = fmaf(p[1], z0, fmaf(p[3], z1, zo[nt][j][1]));
+            }
+            const uint32_t b0 = transpose8(pack_h2(p[0] * s0, p[1] * s0)), b1 = transpose8(pack_h2(p[2] * s1, p[3] * s1));
+            mma<__half>(o[2 * j][nt], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u, b0, b1);
+            mma<__half>(o[2 * j + 1][nt], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u, b0, b1);
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage has been read
+    if (issued < units) {
+      issue(issued, s);
+      issued += kWarps;
+    }
+    if (++s == C::kStages) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+  if (!ok) {  // a wait ran out: let this warp's copies in flight end, for as long again
+    const uint64_t t0 = tc::globaltimer();
+    for (int n = s; n < s + C::kStages; ++n)
+      while (!tc::mbar_try_wait(&full[warp][n % C::kStages], parity ^ (n >= C::kStages ? 1u : 0u)) &&
+             tc::globaltimer() - t0 < a.wait_limit_ns) {
+      }
+  }
+  if (__syncthreads_or(!ok)) return;  // also: every warp is done with its ring
+
+  // ---- join the warps: statistics, then 8 rows at a time through shared memory
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int off = 4; off <= 16; off <<= 1) l[nt][n] += __shfl_xor_sync(0xffffffffu, l[nt][n], off);
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) zo[nt][j][n] += __shfl_xor_sync(0xffffffffu, zo[nt][j][n], off);
+      if (g == 0) {
+        stat[warp][8 * nt + 2 * t + n][0] = m[nt][n];
+        stat[warp][8 * nt + 2 * t + n][1] = l[nt][n];
+      }
+    }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");
+  float* red = reinterpret_cast<float*>(smem);  // [warp][8][D + 4]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float wgt[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      float M = minus_inf();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][8 * nt + 2 * t + n][0]);
+      wgt[n] = m[nt][n] == minus_inf() ? 0.f : ex2(m[nt][n] - M);
+    }
+    const float back = pow2(12 - k);  // o·2^(24 - k), in two steps; an odd nibble's also by 1/16
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float z = zo[nt][j][n];
+        float4 v;
+        v.x = (o[2 * j][nt][n] * 4096.f * back + z) * wgt[n];
+        v.y = (o[2 * j][nt][2 + n] * 256.f * back + z) * wgt[n];
+        v.z = (o[2 * j + 1][nt][n] * 4096.f * back + z) * wgt[n];
+        v.w = (o[2 * j + 1][nt][2 + n] * 256.f * back + z) * wgt[n];
+        *reinterpret_cast<float4*>(red + (warp * 8 + 2 * t + n) * (D + 4) + 32 * j + 4 * g) = v;
+      }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 8 * (D / 4); x += kWarps * 32) {
+      const int q = x / (D / 4), d = x % (D / 4) * 4, r = row0 + 8 * nt + q;
+      if (r < R) {
+        float M = minus_inf(), Lsum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][8 * nt + q][0]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = stat[w][8 * nt + q][0];
+          Lsum += mw == minus_inf() ? 0.f : stat[w][8 * nt + q][1] * ex2(mw - M);
+          const float4 y = *reinterpret_cast<const float4*>(red + (w * 8 + q) * (D + 4) + d);
+          v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+        const int hq = h * a.G + r / c.L, i = r % c.L;
+        const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
+        if (splits > 1) {
+          const int64_t at = row * splits + split;
+          *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;
+          if (d == 0) {
+            float* ml = a.workspace + (int64_t)c.B * a.Hq * c.L * splits * D + 2 * at;
+            ml[0] = M;
+            ml[1] = Lsum;
+          }
+        } else {
+          const float fold = fold_sink(a.sinks, hq, M, Lsum), inv = Lsum == 0.f ? 0.f : fold / Lsum;
+          T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
+          *reinterpret_cast<uint2*>(out) = make_uint2(f_to_bits<T>(v.x * inv) | (f_to_bits<T>(v.y * inv) << 16),
+                                                      f_to_bits<T>(v.z * inv) | (f_to_bits<T>(v.w * inv) << 16));
+          if (a.lse && d == 0) a.lse[row] = Lsum == 0.f ? minus_inf() : (M + log2f(Lsum)) * kLn2;
+        }
+      }
+    }
+    __syncthreads();
+  }
 }
 
+// Joins the chunks of one query row: D/4 threads a chunk, several chunks side by side.
+constexpr int kJoinThreads = 128;
+
 template <typename T, int D>
-cudaError_t attn_t(const CacheAttnArgs& a, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.c.B * a.Hq * a.c.L;
-  cache_attn_kernel<T, D><<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a);
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(CacheAttnArgs a, int chunk, int splits, int rows_a_tile) {
+  constexpr int U = D / 4, kSide = kJoinThreads / U;
+  __shared__ float4 part[kSide][U];
+  __shared__ float red[kJoinThreads / 32], sums[kJoinThreads / 32];
+  const CacheArgs& c = a.c;
+  const int64_t row = blockIdx.x;
+  const int i = (int)(row % c.L), hq = (int)(row / c.L % a.Hq), b = (int)(row / c.L / a.Hq);
+  const int len = cache_len(c, b, a.max_len, kKidCacheAttn);
+  const int end = tile_end(a, len, (hq % a.G * c.L + i) / rows_a_tile, rows_a_tile);
+  const int n = (int)(((int64_t)end + chunk - 1) / chunk);  // chunks that have been written
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* ml = a.workspace + (int64_t)c.B * a.Hq * c.L * splits * D + 2 * row * splits;
+  float M = minus_inf(), L = 0.f;
+  for (int x = threadIdx.x; x < n; x += kJoinThreads) M = fmaxf(M, ml[2 * x]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
+  for (int x = threadIdx.x; x < n; x += kJoinThreads)
+    if (ml[2 * x] != minus_inf()) L += ml[2 * x + 1] * ex2(ml[2 * x] - M);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = L;
+  const int side = threadIdx.x / U, d = threadIdx.x % U * 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (side < kSide) {
+#pragma unroll 4
+    for (int x = side; x < n; x += kSide) {
+      const float mx = ml[2 * x], w = mx == minus_inf() ? 0.f : ex2(mx - M);
+      const float4 y = *reinterpret_cast<const float4*>(a.workspace + (row * splits + x) * D + d);
+      v.x = fmaf(w, y.x, v.x);
+      v.y = fmaf(w, y.y, v.y);
+      v.z = fmaf(w, y.z, v.z);
+      v.w = fmaf(w, y.w, v.w);
+    }
+    part[side][d / 4] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x >= U) return;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) L += sums[w];
+  v = part[0][d / 4];
+  for (int x = 1; x < kSide; ++x) {
+    const float4 y = part[x][d / 4];
+    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+  }
+  const float fold = fold_sink(a.sinks, hq, M, L), inv = L == 0.f ? 0.f : fold / L;
+  T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
+  *reinterpret_cast<uint2*>(out) = make_uint2(f_to_bits<T>(v.x * inv) | (f_to_bits<T>(v.y * inv) << 16),
+                                              f_to_bits<T>(v.z * inv) | (f_to_bits<T>(v.w * inv) << 16));
+  if (a.lse && d == 0) a.lse[row] = L == 0.f ? minus_inf() : (M + log2f(L)) * kLn2;
+}
+
+// How a call is cut.
+struct Plan {
+  int nt, row_tiles, chunk, splits;
+};
+
+Plan make_plan(const CacheAttnArgs& a) {
+  Plan p;
+  const int R = a.G * a.c.L, most = a.c.D == 256 ? 2 : 4;
+  p.nt = R <= 8 ? 1 : R <= 16 ? 2 : most;
+  p.row_tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
+  const int step = 256;  // tokens: at least a unit a warp
+  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.nt == 1 ? 2 : 1);
+  const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * p.row_tiles;
+  // One wave of blocks if there are few pairs; otherwise chunks short enough that sequences
+  // of unequal length share the SMs evenly.
+  const int64_t want = pairs >= slots ? 1 : slots / pairs;
+  int64_t chunk = (a.max_len + want - 1) / want;
+  if (chunk > 2048 && pairs * 4 > slots) chunk = 2048;
+  p.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
+  p.splits = (a.max_len + p.chunk - 1) / p.chunk;
+  return p;
+}
+
+template <typename T, int D, int NT>
+cudaError_t attn_nt(const CacheAttnArgs& a, const Plan& p, cudaStream_t s) {
+  auto* kern = cache_attn_kernel<T, D, NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(p.splits, p.row_tiles * a.c.Hkv, a.c.B), kWarps * 32, Cfg<D, NT>::kSmem, s>>>(a, p.chunk, p.splits, p.row_tiles);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t attn_d(const CacheAttnArgs& a, cudaStream_t s) {
-  switch (a.c.D) {
-    case 32: return attn_t<T, 32>(a, s);
-    case 64: return attn_t<T, 64>(a, s);
-    case 96: return attn_t<T, 96>(a, s);
-    case 128: return attn_t<T, 128>(a, s);
-    case 256: return attn_t<T, 256>(a, s);
+template <typename T, int D>
+cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
+  const Plan p = make_plan(a);
+  if (!join) {
+    switch (p.nt) {
+      case 1: return attn_nt<T, D, 1>(a, p, s);
+      case 2: return attn_nt<T, D, 2>(a, p, s);
+      default:
+        if constexpr (D <= 128) return attn_nt<T, D, 4>(a, p, s);
+        return cudaErrorInvalidValue;
+    }
   }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.c.B * a.Hq * a.c.L));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];  // its blocks may be placed while the last chunks are still running
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, a, p.chunk, p.splits, 8 * p.nt);
+}
+
+template <typename T>
+cudaError_t attn_d(const CacheAttnArgs& a, bool join, cudaStream_t s) {
+  switch (a.c.D) {
+    case 32: return attn_t<T, 32>(a, join, s);
+    case 64: return attn_t<T, 64>(a, join, s);
+    case 96: return attn_t<T, 96>(a, join, s);
+    case 128: return attn_t<T, 128>(a, join, s);
+    case 256: return attn_t<T, 256>(a, join, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t attn_any(const CacheAttnArgs& a, int dtype, bool join, cudaStream_t s) {
+  if (dtype == 1) return attn_d<__half>(a, join, s);
+  if (dtype == 2) return attn_d<__nv_bfloat16>(a, join, s);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t cache_attn_workspace(const CacheAttnArgs&) { return 0; }
-
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == 1) return attn_d<__half>(a, s);
-  if (dtype == 2) return attn_d<__nv_bfloat16>(a, s);
-  return cudaErrorInvalidValue;
+size_t cache_attn_workspace(const CacheAttnArgs& a) {
+  const Plan p = make_plan(a);
+  return p.splits == 1 ? 0 : (size_t)a.c.B * a.Hq * a.c.L * p.splits * (a.c.D + 2) * sizeof(float);
 }
+
+int cache_attn_row_tiles(const CacheAttnArgs& a) { return make_plan(a).row_tiles; }
+
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int dtype, cudaStream_t s) { return attn_any(a, dtype, false, s); }
+cudaError_t launch_cache_join(const CacheAttnArgs& a, int dtype, cudaStream_t s) { return attn_any(a, dtype, true, s); }
 
 }  // namespace sdpa
