@@ -48,7 +48,7 @@ struct Cfg {
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -62,6 +62,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+__device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x & 0xffffu))); }
+__device__ __forceinline__ float high_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
@@ -159,10 +161,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
   // Query rows as the B operand: lane (g, t) holds, of row g and each group, elements 8t..8t+7,
   // times a power of two that brings the row's largest to 2^13..2^14 (exact in fp16 down to
   // 2^-27 of that); the odd nibbles' elements are divided by the 16 that their codes carry.
+  // The z term's share has bf16's range to be in the accumulators' units (2^-24) at once; in
+  // fp16 it stays at 2^13 or less and is scaled after its MMA.
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr float kZUp = kHalf ? 0x1p-6f : 0x1p-24f;
   uint32_t qf[kQSmem ? 1 : NG][4];
   uint4* qs = reinterpret_cast<uint4*>(smem + C::kBody);
   uint32_t qz[NT][JB][2];  // group sums of the row, split in three (z term)
-  float f[NT][2];          // per column 2t, 2t+1: scale·log2e·2^(24 - e)
+  float f[NT][2];          // per column 2t, 2t+1: |scale|·log2e·2^(24 - e) > 0
   int lim[NT][2];          // per column: positions below this are visible
   const int R = a.G * c.L, row0 = rt * C::kRows;
 #pragma unroll
@@ -186,7 +192,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
     // 2^e·top in [2^13, 2^14).  A row of zeros (or subnormals) takes 2^100, an infinite one
     // 2^-100 and turns NaN by itself.
     const int e = max(-100, min(100, 13 - ((__float_as_int(top) >> 23) - 127)));
-    const float up = pow2(e);
+    // The scale's sign goes into q, so that the largest score is the largest accumulator; a
+    // scale of zero makes q zero.
+    const float up = a.scale_log2 == 0.f ? 0.f : copysignf(pow2(e), a.scale_log2);
     float sums[JB] = {};
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
@@ -208,8 +216,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
       }
     }
 #pragma unroll
-    for (int jb = 0; jb < JB; ++jb) {  // sums·2^-6 = hi + mid + lo in T (at most 2^13)
-      const float s6 = sums[jb] * 0.015625f;
+    for (int jb = 0; jb < JB; ++jb) {  // sums·kZUp = hi + mid + lo in T
+      const float s6 = sums[jb] * kZUp;
       const uint32_t hi = f_to_bits<T>(s6);
       const float rest = s6 - bits_to_f<T>(hi);
       const uint32_t mid = f_to_bits<T>(rest);
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
 #pragma unroll
     for (int n = 0; n < 2; ++n) {  // the accumulators' columns are rows 2t and 2t + 1
       const int src = __shfl_sync(0xffffffffu, e, (2 * t + n) * 4);
-      f[nt][n] = a.scale_log2 * pow2(24 - src);
+      f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(24 - src), 1e-37f);
       const int rr = row0 + 8 * nt + 2 * t + n;
       lim[nt][n] = a.causal ? len - c.L + rr % c.L + 1 : len;
     }
@@ -241,17 +249,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
   }
   int k = 120;  // P·s enters the MMA times 2^k
 
-  bool ok = true;
-  int s = 0;
-  uint32_t parity = 0;
-  for (int u = warp; u < units; u += kWarps) {
-    ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[warp][s], parity, wc));
-    if (!ok) break;
-    const uint8_t* st = ring + s * C::kUnitBytes;
-    const int key0 = start + u * C::kUnit;
-    const uint32_t tiles = (there >> (s * UT)) & ((1u << UT) - 1);
-    const bool masked = key0 + C::kUnit > min(seen, end) || tiles != (1u << UT) - 1;
-
+  // One unit in shared memory: scores, softmax, values.  Only units that a sequence's or a
+  // row's end cuts, or that lack a tile, take the masked form.
+  auto unit = [&](const uint8_t* st, int key0, uint32_t tiles, auto masked) {
+    constexpr bool kMasked = decltype(masked)::value;
+    auto key_there = [&](int ti, int hf) { return key0 + ti * kTile + g + 8 * hf < end && ((tiles >> ti) & 1); };
     // ---- scores
     float sc[UT][NT][4];
 #pragma unroll
@@ -270,10 +272,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
       }
+      if constexpr (kHalf) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[ti][nt][e] *= 0x1p-18f;
+          for (int e = 0; e < 4; ++e) sc[ti][nt][e] *= 0x1p-18f;
+      }
     }
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb) {
@@ -327,8 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             float& x = sc[ti][nt][2 * hf + n];
-            x *= f[nt][n];
-            if (masked) {
+            if constexpr (kMasked) {
               const int pos = key0 + ti * kTile + g + 8 * hf;
               if (pos >= min(lim[nt][n], end) || !((tiles >> ti) & 1)) x = minus_inf();
             }
@@ -336,29 +339,28 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
           }
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float m_new = fmaxf(m[nt][n], top);
+        const float m_new = fmaxf(m[nt][n], top * f[nt][n]);
         alpha[nt][n] = m_new == minus_inf() ? 1.f : ex2(m[nt][n] - m_new);
         grew = grew || m_new > m[nt][n];
         m[nt][n] = m_new;
       }
     }
-    // The largest value scale of the unit fixes the power of two of P·s.
-    uint32_t vp[UT][2][NG];
+    // The largest value scale of the unit fixes the power of two of P·s: lane (g, t) looks at
+    // group t of rows g and g + 8.
     uint32_t smax = 0;
 #pragma unroll
     for (int ti = 0; ti < UT; ++ti)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int pos = key0 + ti * kTile + g + 8 * hf;
-        const bool there_key = !masked || (pos < end && ((tiles >> ti) & 1));
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int jb = 0; jb < JB; ++jb) load_words<W>(&vp[ti][hf][jb * W], st + ti * Tl::kBytes + Tl::kVp + (jb * 16 + g + 8 * hf) * W * 4);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          if (!there_key) vp[ti][hf][j] = 0;
-          smax = max(smax, vp[ti][hf][j] & 0xffffu);
+        for (int jb = 0; jb < JB; ++jb) {
+          uint32_t w = 0;
+          if (W == 4 || t < W) w = reinterpret_cast<const uint32_t*>(st + ti * Tl::kBytes + Tl::kVp)[(jb * 16 + g + 8 * hf) * W + t];
+          if constexpr (kMasked)
+            if (!key_there(ti, hf)) w = 0;
+          smax = __vmaxu2(smax, w);
         }
-      }
+    smax &= 0xffffu;
     smax = __reduce_max_sync(0xffffffffu, smax);  // scales are not negative: bits order them
     const int k_new = min(k, min(120, 13 - ((__float_as_int(bits_to_f<T>(smax)) >> 23) - 127)));
     if (__any_sync(0xffffffffu, grew) || k_new < k) {
@@ -390,39 +392,76 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1] == minus_inf() ? 0.f : m[nt][e & 1];
-          sc[ti][nt][e] = ex2(sc[ti][nt][e] - ref);
+          const float ref = kMasked && m[nt][e & 1] == minus_inf() ? 0.f : m[nt][e & 1];
+          sc[ti][nt][e] = ex2(fmaf(sc[ti][nt][e], f[nt][e & 1], -ref));
           l[nt][e & 1] += sc[ti][nt][e];
         }
       // ---- values
+      float pu[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pu[nt][e] = sc[ti][nt][e] * up;
 #pragma unroll
       for (int jb = 0; jb < JB; ++jb) {
-        uint32_t vw[2][W];
+        uint32_t vw[2][W], vp[2][W];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) load_words<W>(vw[hf], st + ti * Tl::kBytes + Tl::kV + ((hf * JB + jb) * 32 + lane) * W * 4);
+        for (int hf = 0; hf < 2; ++hf) {
+          load_words<W>(vw[hf], st + ti * Tl::kBytes + Tl::kV + ((hf * JB + jb) * 32 + lane) * W * 4);
+          load_words<W>(vp[hf], st + ti * Tl::kBytes + Tl::kVp + (jb * 16 + g + 8 * hf) * W * 4);
+          if constexpr (kMasked) {
+            if (!key_there(ti, hf)) {
+#pragma unroll
+              for (int w = 0; w < W; ++w) vp[hf][w] = 0;
+            }
+          }
+        }
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const int j = jb * W + w;
-          const float s0 = bits_to_f<T>(vp[ti][0][j] & 0xffffu) * up, s1 = bits_to_f<T>(vp[ti][1][j] & 0xffffu) * up;
-          const float z0 = bits_to_f<T>(vp[ti][0][j] >> 16), z1 = bits_to_f<T>(vp[ti][1][j] >> 16);
+          const float s0 = bits_to_f<T>(vp[0][w] & 0xffffu), s1 = bits_to_f<T>(vp[1][w] & 0xffffu);
+          const float z0 = bits_to_f<T>(vp[0][w] >> 16), z1 = bits_to_f<T>(vp[1][w] >> 16);
           const uint32_t x0 = vw[0][w], x1 = vw[1][w], y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float (&p)[4] = sc[ti][nt];
-            if (masked) {  // a hidden key's z may be NaN
+            if constexpr (kMasked) {  // a hidden key's z may be NaN
               zo[nt][j][0] += (p[0] == 0.f ? 0.f : p[0] * z0) + (p[2] == 0.f ? 0.f : p[2] * z1);
               zo[nt][j][1] += (p[1] == 0.f ? 0.f : p[1] * z0) + (p[3] == 0.f ? 0.f : p[3] * z1);
             } else {
               zo[nt][j][0] = fmaf(p[0], z0, fmaf(p[2], z1, zo[nt][j][0]));
               zo[nt][j][1] = fmaf(p[1], z0, fmaf(p[3], z1, zo[nt][j][1]));
             }
-            const uint32_t b0 = transpose8(pack_h2(p[0] * s0, p[1] * s0)), b1 = transpose8(pack_h2(p[2] * s1, p[3] * s1));
-            mma<__half>(o[2 * j][nt], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u, b0, b1);
-            mma<__half>(o[2 * j + 1][nt], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u, b0, b1);
+            const float q[4] = {pu[nt][0] * s0, pu[nt][1] * s0, pu[nt][2] * s1, pu[nt][3] * s1};
+            const uint32_t h0 = pack_h2(q[0], q[1]), h1 = pack_h2(q[2], q[3]);
+            const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u, a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
+            const uint32_t c0 = y0 & 0x000f000fu, c1 = y0 & 0x00f000f0u, c2 = y1 & 0x000f000fu, c3 = y1 & 0x00f000f0u;
+            uint32_t b0 = transpose8(h0), b1 = transpose8(h1);
+            mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
+            mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
+            if constexpr (kHalf) {  // what the rounding lost: outputs in fp16 would show it
+              b0 = transpose8(pack_h2(q[0] - low_h(h0), q[1] - high_h(h0)));
+              b1 = transpose8(pack_h2(q[2] - low_h(h1), q[3] - high_h(h1)));
+              mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
+              mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
+            }
           }
         }
       }
     }
+  };
+
+  bool ok = true;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int u = warp; u < units; u += kWarps) {
+    ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[warp][s], parity, wc));
+    if (!ok) break;
+    const uint8_t* st = ring + s * C::kUnitBytes;
+    const int key0 = start + u * C::kUnit;
+    const uint32_t tiles = (there >> (s * UT)) & ((1u << UT) - 1);
+    if (key0 + C::kUnit > min(seen, end) || tiles != (1u << UT) - 1) unit(st, key0, tiles, std::true_type());
+    else unit(st, key0, tiles, std::false_type());
     __syncwarp();  // the stage has been read
     if (issued < units) {
       issue(issued, s);
