@@ -37,6 +37,7 @@ struct Cfg {
   static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
   static constexpr int kUnit = UT * kTile;                   // tokens a unit
   static constexpr int kStages = 2;
+  static constexpr int kBlocks = NT == 1 && D <= 128 ? 2 : 1;  // blocks an SM
   static constexpr int kUnitBytes = UT * Tl::kBytes;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
@@ -59,7 +60,7 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 // Transposes an 8 x 8 matrix of 16-bit elements held two a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x & 0xffffu))); }
@@ -67,15 +68,29 @@ __device__ __forceinline__ float high_h(uint32_t x) { return __half2float(__usho
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with an accumulator of zero.
+template <typename T>
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
@@ -108,7 +123,7 @@ __device__ __forceinline__ int tile_end(const CacheAttnArgs& a, int len, int rt,
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kernel(CacheAttnArgs a, int chunk, int splits, int row_tiles) {
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_kernel(CacheAttnArgs a, int chunk, int splits, int row_tiles) {
   using C = Cfg<D, NT>;
   using Tl = Tile<D>;
   constexpr int NG = Tl::NG, W = Tl::W, JB = Tl::JB, UT = C::UT;
@@ -138,25 +153,42 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
 
   uint8_t* ring = smem + warp * (C::kStages * C::kUnitBytes);
   uint32_t there = 0;  // bit s·UT + tile: the tile in stage s was copied
-  // Starts the copies of unit u into stage s (all lanes call it).
-  auto issue = [&](int u, int s) {
-    const int pos = start + u * C::kUnit + lane * kTile;
+  // The tile that this lane copies next: its position, its place in the page table and its
+  // offset in the page, which move on by a fixed step.
+  int pos = start + warp * C::kUnit + lane * kTile;
+  int slot = pos / c.page_size, off = pos % c.page_size;
+  const int step_slots = kWarps * C::kUnit / c.page_size, step_off = kWarps * C::kUnit % c.page_size;
+  const int* table = c.pages + b * c.pages_stride;
+  const int64_t page_bytes = (int64_t)c.Hkv * (c.page_size / kTile) * Tl::kBytes;
+  const uint8_t* head = c.data + (int64_t)h * (c.page_size / kTile) * Tl::kBytes;
+  // Starts the copies of this warp's next unit into stage s (all lanes call it).
+  auto issue = [&](int s) {
     int page = -1;
-    if (lane < UT && pos < end) page = cache_page(c, b, pos, kKidCacheAttn);
+    if (lane < UT && pos < end) {
+      page = table[slot];
+      if ((unsigned)page >= (unsigned)c.num_pages) {
+        report_error(c.err, kDevErrIndex, kKidCacheAttn);
+        page = -1;
+      }
+    }
     const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
     there = (there & ~(((1u << UT) - 1) << (s * UT))) | (ok << (s * UT));
     if (lane == 0) tc::mbar_arrive_expect_tx(&full[warp][s], __popc(ok) * Tl::kBytes);
     __syncwarp();
     if (page >= 0)
-      bulk_copy(ring + s * C::kUnitBytes + lane * Tl::kBytes, cache_tile<D>(c, page, h, pos % c.page_size / kTile), Tl::kBytes, &full[warp][s]);
+      bulk_copy(ring + s * C::kUnitBytes + lane * Tl::kBytes, head + page * page_bytes + off / kTile * Tl::kBytes, Tl::kBytes, &full[warp][s]);
+    pos += kWarps * C::kUnit;
+    slot += step_slots;
+    off += step_off;
+    if (off >= c.page_size) {
+      off -= c.page_size;
+      ++slot;
+    }
   };
   int issued = warp;  // next unit to start
 #pragma unroll
-  for (int s = 0; s < C::kStages; ++s)
-    if (issued < units) {
-      issue(issued, s);
-      issued += kWarps;
-    }
+  for (int s = 0; s < C::kStages; ++s, issued += kWarps)
+    if (issued < units) issue(s);
 
   // Query rows as the B operand: lane (g, t) holds, of row g and each group, elements 8t..8t+7,
   // times a power of two that brings the row's largest to 2^13..2^14 (exact in fp16 down to
@@ -260,8 +292,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
     for (int ti = 0; ti < UT; ++ti) {
       const uint8_t* tile = st + ti * Tl::kBytes;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[ti][nt][0] = sc[ti][nt][1] = sc[ti][nt][2] = sc[ti][nt][3] = 0.f;
-#pragma unroll
       for (int jb = 0; jb < JB; ++jb) {  // z of group 4·jb + t: (hi, mid) and (lo, nothing)
         uint32_t z0 = 0, z1 = 0;
         if (W == 4 || t < W) {
@@ -270,7 +300,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
           z1 = zp[8 * W] >> 16;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (jb == 0) mma0<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
+          else mma<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
+        }
       }
       if constexpr (kHalf) {
 #pragma unroll
@@ -305,8 +338,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
 #pragma unroll
           for (int ti = 0; ti < UT; ++ti) {
             const uint32_t x0 = kw[ti][0][w], x1 = kw[ti][1][w], y0 = x0 >> 8, y1 = x1 >> 8;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
+            float acc[4];
+            mma0<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
             mma<__half>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
             const float s0 = bits_to_f<T>(kp[ti][0][w] & 0xffffu), s1 = bits_to_f<T>(kp[ti][1][w] & 0xffffu);
             sc[ti][nt][0] = fmaf(s0, acc[0], sc[ti][nt][0]);
@@ -463,10 +496,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) cache_attn_kerne
     if (key0 + C::kUnit > min(seen, end) || tiles != (1u << UT) - 1) unit(st, key0, tiles, std::true_type());
     else unit(st, key0, tiles, std::false_type());
     __syncwarp();  // the stage has been read
-    if (issued < units) {
-      issue(issued, s);
-      issued += kWarps;
-    }
+    if (issued < units) issue(s);
+    issued += kWarps;
     if (++s == C::kStages) {
       s = 0;
       parity ^= 1;
@@ -632,7 +663,7 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.nt = R <= 8 ? 1 : R <= 16 ? 2 : most;
   p.row_tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
   const int step = 256;  // tokens: at least a unit a warp
-  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.nt == 1 ? 2 : 1);
+  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.nt == 1 && a.c.D <= 128 ? 2 : 1);
   const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * p.row_tiles;
   // One wave of blocks if there are few pairs; otherwise chunks short enough that sequences
   // of unequal length share the SMs evenly.
