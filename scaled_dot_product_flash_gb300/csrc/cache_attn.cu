@@ -29,19 +29,32 @@
 namespace sdpa {
 namespace {
 
-constexpr int kWarps = 8;
-
-template <int D, int NT>
+// NT: row tiles of 8 rows that a block takes, CW: columns of the transposed products that a
+// lane holds.  CW = 2 is the plain form.  CW = 1 is the form for up to 4 rows, which would leave
+// half of the 8 columns empty: row r is column 2r and the odd columns are zero, so that every
+// lane has one row and half the elements of the softmax and of the scalings.
+#ifndef NW
+#define NW 4
+#define NS 2
+#define NB 3
+#endif
+constexpr int kNarrowWarps = NW, kNarrowStages = NS, kNarrowBlocks = NB;
+template <int D, int NT, int CW>
 struct Cfg {
   using Tl = Tile<D>;
-  static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
+  #ifndef UTN
+#define UTN 2
+#endif
+  static constexpr int UT = CW == 1 && D == 128 ? UTN : D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
   static constexpr int kUnit = UT * kTile;                   // tokens a unit
-  static constexpr int kStages = 2;
-  static constexpr int kBlocks = NT == 1 && D <= 128 ? 2 : 1;  // blocks an SM
+  static constexpr int kWarps = CW == 1 ? kNarrowWarps : 8;
+  static constexpr int kStages = CW == 1 ? kNarrowStages : 2;
+  static constexpr int kBlocks = CW == 1 ? kNarrowBlocks : NT == 1 && D <= 128 ? 2 : 1;  // blocks an SM
   static constexpr int kUnitBytes = UT * Tl::kBytes;
-  static constexpr int kRows = 8 * NT;
+  static constexpr int kSlab = 4 * CW;       // rows of a row tile
+  static constexpr int kRows = kSlab * NT;
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
-  static constexpr int kMerge = kWarps * 8 * (D + 4) * 4;  // 8 rows of every warp's output
+  static constexpr int kMerge = kWarps * kSlab * (D + 4) * 4;  // a slab of rows of every warp's output
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQ = NT > 1 ? NT * (D / kGroup) * 32 * 16 : 0;  // q fragments
   static constexpr int kSmem = kBody + kQ;
@@ -122,9 +135,10 @@ __device__ __forceinline__ int tile_end(const CacheAttnArgs& a, int len, int rt,
   return max(0, len - a.c.L + last + 1);
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_kernel(CacheAttnArgs a, int chunk, int splits, int row_tiles) {
-  using C = Cfg<D, NT>;
+template <typename T, int D, int NT, int CW>
+__global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::kBlocks) cache_attn_kernel(CacheAttnArgs a, int chunk, int splits, int row_tiles) {
+  using C = Cfg<D, NT, CW>;
+  constexpr int kWarps = C::kWarps;
   using Tl = Tile<D>;
   constexpr int NG = Tl::NG, W = Tl::W, JB = Tl::JB, UT = C::UT;
   constexpr bool kQSmem = NT > 1;
@@ -200,12 +214,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
   uint32_t qf[kQSmem ? 1 : NG][4];
   uint4* qs = reinterpret_cast<uint4*>(smem + C::kBody);
   uint32_t qz[NT][JB][2];  // group sums of the row, split in three (z term)
-  float f[NT][2];          // per column 2t, 2t+1: |scale|·log2e·2^(24 - e) > 0
-  int lim[NT][2];          // per column: positions below this are visible
+  float f[NT][CW];         // per row of this lane's columns: |scale|·log2e·2^(24 - e) > 0
+  int lim[NT][CW];         // the same: positions below this are visible
   const int R = a.G * c.L, row0 = rt * C::kRows;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = row0 + 8 * nt + g;
+    const int r = CW == 2 ? row0 + 8 * nt + g : g % 2 == 0 ? row0 + g / 2 : R;  // R: no row
     float x[NG][8];
     float top = 0.f;
 #pragma unroll
@@ -257,10 +271,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
       qz[nt][jb][1] = f_to_bits<T>(rest - bits_to_f<T>(mid));
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {  // the accumulators' columns are rows 2t and 2t + 1
+    for (int n = 0; n < CW; ++n) {  // the accumulators' columns are 2t and 2t + 1
       const int src = __shfl_sync(0xffffffffu, e, (2 * t + n) * 4);
       f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(24 - src), 1e-37f);
-      const int rr = row0 + 8 * nt + 2 * t + n;
+      const int rr = row0 + C::kSlab * nt + CW * t + n;
       lim[nt][n] = a.causal ? len - c.L + rr % c.L + 1 : len;
     }
   }
@@ -268,18 +282,22 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
   const int seen = a.causal ? len - c.L + 1 : len;  // every row sees the positions below this
 
   float o[2 * NG][NT][4];  // O^T, times 2^(k - 24)
-  float zo[NT][NG][2];     // this lane's keys' P·z
-  float m[NT][2], l[NT][2];
+  float zo[NT][NG][CW];    // this lane's keys' P·z
+  float m[NT][CW], l[NT][CW], high[NT][CW];  // reference, sum, score that calls for a new reference
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int j = 0; j < 2 * NG; ++j) o[j][nt][0] = o[j][nt][1] = o[j][nt][2] = o[j][nt][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) zo[nt][j][0] = zo[nt][j][1] = 0.f;
-    m[nt][0] = m[nt][1] = minus_inf();
-    l[nt][0] = l[nt][1] = 0.f;
+    for (int n = 0; n < CW; ++n) {
+#pragma unroll
+      for (int j = 0; j < NG; ++j) zo[nt][j][n] = 0.f;
+      m[nt][n] = high[nt][n] = minus_inf();
+      l[nt][n] = 0.f;
+    }
   }
-  int k = 120;  // P·s enters the MMA times 2^k
+  int k = kHalf ? 21 : 120;  // P·s enters the MMA times 2^k, at most 2^8·2^7
+  uint32_t slimit = 1;       // scales whose bits reach this call for a smaller k
 
   // One unit in shared memory: scores, softmax, values.  Only units that a sequence's or a
   // row's end cuts, or that lack a tile, take the masked form.
@@ -287,10 +305,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
     constexpr bool kMasked = decltype(masked)::value;
     auto key_there = [&](int ti, int hf) { return key0 + ti * kTile + g + 8 * hf < end && ((tiles >> ti) & 1); };
     // ---- scores
-    float sc[UT][NT][4];
+    float sc[UT][NT][2][CW];  // [.][.][half][n]: key g + 8·half, this lane's column n
 #pragma unroll
     for (int ti = 0; ti < UT; ++ti) {
       const uint8_t* tile = st + ti * Tl::kBytes;
+      float acc[NT][4];
 #pragma unroll
       for (int jb = 0; jb < JB; ++jb) {  // z of group 4·jb + t: (hi, mid) and (lo, nothing)
         uint32_t z0 = 0, z1 = 0;
@@ -301,16 +320,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (jb == 0) mma0<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
-          else mma<T>(sc[ti][nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
+          if (jb == 0) mma0<T>(acc[nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
+          else mma<T>(acc[nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
         }
       }
-      if constexpr (kHalf) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[ti][nt][e] *= 0x1p-18f;
-      }
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int n = 0; n < CW; ++n) sc[ti][nt][hf][n] = kHalf ? acc[nt][2 * hf + n] * 0x1p-18f : acc[nt][2 * hf + n];
     }
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb) {
@@ -341,46 +360,40 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
             float acc[4];
             mma0<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
             mma<__half>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
-            const float s0 = bits_to_f<T>(kp[ti][0][w] & 0xffffu), s1 = bits_to_f<T>(kp[ti][1][w] & 0xffffu);
-            sc[ti][nt][0] = fmaf(s0, acc[0], sc[ti][nt][0]);
-            sc[ti][nt][1] = fmaf(s0, acc[1], sc[ti][nt][1]);
-            sc[ti][nt][2] = fmaf(s1, acc[2], sc[ti][nt][2]);
-            sc[ti][nt][3] = fmaf(s1, acc[3], sc[ti][nt][3]);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float s = bits_to_f<T>(kp[ti][hf][w] & 0xffffu);
+#pragma unroll
+              for (int n = 0; n < CW; ++n) sc[ti][nt][hf][n] = fmaf(s, acc[2 * hf + n], sc[ti][nt][hf][n]);
+            }
           }
         }
       }
     }
 
-    // ---- softmax: element e of a tile is key g + 8·(e / 2), column 2t + e % 2
-    bool grew = false;
-    float alpha[NT][2];
+    // ---- softmax.  The reference m of a row need not be its running maximum: it stays until
+    // some score is more than 2^8 above it (P <= 2^8 then), and so does the power of two of the
+    // value scales until one is over 2^7 times too large.  One vote covers both.
+    bool over = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < CW; ++n) {
         float top = minus_inf();
 #pragma unroll
         for (int ti = 0; ti < UT; ++ti)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float& x = sc[ti][nt][2 * hf + n];
+            float& x = sc[ti][nt][hf][n];
             if constexpr (kMasked) {
               const int pos = key0 + ti * kTile + g + 8 * hf;
               if (pos >= min(lim[nt][n], end) || !((tiles >> ti) & 1)) x = minus_inf();
             }
             top = fmaxf(top, x);
           }
-#pragma unroll
-        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float m_new = fmaxf(m[nt][n], top * f[nt][n]);
-        alpha[nt][n] = m_new == minus_inf() ? 1.f : ex2(m[nt][n] - m_new);
-        grew = grew || m_new > m[nt][n];
-        m[nt][n] = m_new;
+        over = over || top > high[nt][n];
       }
-    }
-    // The largest value scale of the unit fixes the power of two of P·s: lane (g, t) looks at
-    // group t of rows g and g + 8.
-    uint32_t smax = 0;
+    uint32_t smax = 0;  // lane (g, t) looks at group t of rows g and g + 8
 #pragma unroll
     for (int ti = 0; ti < UT; ++ti)
 #pragma unroll
@@ -393,48 +406,53 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
             if (!key_there(ti, hf)) w = 0;
           smax = __vmaxu2(smax, w);
         }
-    smax &= 0xffffu;
-    smax = __reduce_max_sync(0xffffffffu, smax);  // scales are not negative: bits order them
-    const int k_new = min(k, min(120, 13 - ((__float_as_int(bits_to_f<T>(smax)) >> 23) - 127)));
-    if (__any_sync(0xffffffffu, grew) || k_new < k) {
+    smax &= 0xffffu;  // scales are not negative: their bits order them
+    if (__any_sync(0xffffffffu, over || smax >= slimit)) {
+      smax = __reduce_max_sync(0xffffffffu, smax);
+      const int k_new = min(k, 5 - ((__float_as_int(bits_to_f<T>(smax)) >> 23) - 127));
       const float down = k - k_new > 126 ? 0.f : pow2(k_new - k);
       k = k_new;
+      slimit = f_to_bits<T>(min(7 - k, 127) < 16 || !kHalf ? pow2(min(7 - k, 127)) : 65504.f);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float a0 = alpha[nt][0], a1 = alpha[nt][1], d0 = a0 * down, d1 = a1 * down;
-        l[nt][0] *= a0;
-        l[nt][1] *= a1;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          zo[nt][j][0] *= a0;
-          zo[nt][j][1] *= a1;
+        for (int n = 0; n < CW; ++n) {
+          float top = minus_inf();
+#pragma unroll
+          for (int ti = 0; ti < UT; ++ti) top = fmaxf(top, fmaxf(sc[ti][nt][0][n], sc[ti][nt][1][n]));
+#pragma unroll
+          for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const float m_new = fmaxf(m[nt][n], top * f[nt][n]);
+          const float al = m_new == minus_inf() ? 1.f : ex2(m[nt][n] - m_new), both = al * down;
+          m[nt][n] = m_new;
+          high[nt][n] = (m_new + 8.f) / f[nt][n];
+          l[nt][n] *= al;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) zo[nt][j][n] *= al;
+#pragma unroll
+          for (int j = 0; j < 2 * NG; ++j) {
+            o[j][nt][n] *= both;
+            o[j][nt][2 + n] *= both;
+          }
         }
-#pragma unroll
-        for (int j = 0; j < 2 * NG; ++j) {
-          o[j][nt][0] *= d0;
-          o[j][nt][1] *= d1;
-          o[j][nt][2] *= d0;
-          o[j][nt][3] *= d1;
-        }
-      }
     }
     const float up = pow2(k);
 #pragma unroll
     for (int ti = 0; ti < UT; ++ti) {
+      float pu[NT][2][CW];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = kMasked && m[nt][e & 1] == minus_inf() ? 0.f : m[nt][e & 1];
-          sc[ti][nt][e] = ex2(fmaf(sc[ti][nt][e], f[nt][e & 1], -ref));
-          l[nt][e & 1] += sc[ti][nt][e];
-        }
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int n = 0; n < CW; ++n) {
+            const float ref = kMasked && m[nt][n] == minus_inf() ? 0.f : m[nt][n];
+            const float p = ex2(fmaf(sc[ti][nt][hf][n], f[nt][n], -ref));
+            sc[ti][nt][hf][n] = p;
+            l[nt][n] += p;
+            pu[nt][hf][n] = p * up;
+          }
       // ---- values
-      float pu[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pu[nt][e] = sc[ti][nt][e] * up;
 #pragma unroll
       for (int jb = 0; jb < JB; ++jb) {
         uint32_t vw[2][W], vp[2][W];
@@ -452,29 +470,32 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const int j = jb * W + w;
-          const float s0 = bits_to_f<T>(vp[0][w] & 0xffffu), s1 = bits_to_f<T>(vp[1][w] & 0xffffu);
-          const float z0 = bits_to_f<T>(vp[0][w] >> 16), z1 = bits_to_f<T>(vp[1][w] >> 16);
           const uint32_t x0 = vw[0][w], x1 = vw[1][w], y0 = x0 >> 8, y1 = x1 >> 8;
+          const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u, a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
+          const uint32_t c0 = y0 & 0x000f000fu, c1 = y0 & 0x00f000f0u, c2 = y1 & 0x000f000fu, c3 = y1 & 0x00f000f0u;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float (&p)[4] = sc[ti][nt];
-            if constexpr (kMasked) {  // a hidden key's z may be NaN
-              zo[nt][j][0] += (p[0] == 0.f ? 0.f : p[0] * z0) + (p[2] == 0.f ? 0.f : p[2] * z1);
-              zo[nt][j][1] += (p[1] == 0.f ? 0.f : p[1] * z0) + (p[3] == 0.f ? 0.f : p[3] * z1);
-            } else {
-              zo[nt][j][0] = fmaf(p[0], z0, fmaf(p[2], z1, zo[nt][j][0]));
-              zo[nt][j][1] = fmaf(p[1], z0, fmaf(p[3], z1, zo[nt][j][1]));
+            float q[2][2];
+            uint32_t hi[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float s = bits_to_f<T>(vp[hf][w] & 0xffffu), z = bits_to_f<T>(vp[hf][w] >> 16);
+              q[hf][1] = 0.f;
+#pragma unroll
+              for (int n = 0; n < CW; ++n) {
+                const float p = sc[ti][nt][hf][n];
+                q[hf][n] = pu[nt][hf][n] * s;
+                if constexpr (kMasked) zo[nt][j][n] += p == 0.f ? 0.f : p * z;  // a hidden key's z may be NaN
+                else zo[nt][j][n] = fmaf(p, z, zo[nt][j][n]);
+              }
+              hi[hf] = pack_h2(q[hf][0], q[hf][1]);
             }
-            const float q[4] = {pu[nt][0] * s0, pu[nt][1] * s0, pu[nt][2] * s1, pu[nt][3] * s1};
-            const uint32_t h0 = pack_h2(q[0], q[1]), h1 = pack_h2(q[2], q[3]);
-            const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u, a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
-            const uint32_t c0 = y0 & 0x000f000fu, c1 = y0 & 0x00f000f0u, c2 = y1 & 0x000f000fu, c3 = y1 & 0x00f000f0u;
-            uint32_t b0 = transpose8(h0), b1 = transpose8(h1);
+            uint32_t b0 = transpose8(hi[0]), b1 = transpose8(hi[1]);
             mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
             mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
             if constexpr (kHalf) {  // what the rounding lost: outputs in fp16 would show it
-              b0 = transpose8(pack_h2(q[0] - low_h(h0), q[1] - high_h(h0)));
-              b1 = transpose8(pack_h2(q[2] - low_h(h1), q[3] - high_h(h1)));
+              b0 = transpose8(pack_h2(q[0][0] - low_h(hi[0]), q[0][1] - high_h(hi[0])));
+              b1 = transpose8(pack_h2(q[1][0] - low_h(hi[1]), q[1][1] - high_h(hi[1])));
               mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
               mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
             }
@@ -516,7 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < CW; ++n) {
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) l[nt][n] += __shfl_xor_sync(0xffffffffu, l[nt][n], off);
 #pragma unroll
@@ -524,49 +545,49 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks) cache_attn_k
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) zo[nt][j][n] += __shfl_xor_sync(0xffffffffu, zo[nt][j][n], off);
       if (g == 0) {
-        stat[warp][8 * nt + 2 * t + n][0] = m[nt][n];
-        stat[warp][8 * nt + 2 * t + n][1] = l[nt][n];
+        stat[warp][C::kSlab * nt + CW * t + n][0] = m[nt][n];
+        stat[warp][C::kSlab * nt + CW * t + n][1] = l[nt][n];
       }
     }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
-  float* red = reinterpret_cast<float*>(smem);  // [warp][8][D + 4]
+  float* red = reinterpret_cast<float*>(smem);  // [warp][kSlab][D + 4]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float wgt[2];
+    float wgt[CW];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < CW; ++n) {
       float M = minus_inf();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][8 * nt + 2 * t + n][0]);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][C::kSlab * nt + CW * t + n][0]);
       wgt[n] = m[nt][n] == minus_inf() ? 0.f : ex2(m[nt][n] - M);
     }
     const float back = pow2(12 - k);  // o·2^(24 - k), in two steps; an odd nibble's also by 1/16
 #pragma unroll
     for (int j = 0; j < NG; ++j)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < CW; ++n) {
         const float z = zo[nt][j][n];
         float4 v;
         v.x = (o[2 * j][nt][n] * 4096.f * back + z) * wgt[n];
         v.y = (o[2 * j][nt][2 + n] * 256.f * back + z) * wgt[n];
         v.z = (o[2 * j + 1][nt][n] * 4096.f * back + z) * wgt[n];
         v.w = (o[2 * j + 1][nt][2 + n] * 256.f * back + z) * wgt[n];
-        *reinterpret_cast<float4*>(red + (warp * 8 + 2 * t + n) * (D + 4) + 32 * j + 4 * g) = v;
+        *reinterpret_cast<float4*>(red + (warp * C::kSlab + CW * t + n) * (D + 4) + 32 * j + 4 * g) = v;
       }
     __syncthreads();
-    for (int x = threadIdx.x; x < 8 * (D / 4); x += kWarps * 32) {
-      const int q = x / (D / 4), d = x % (D / 4) * 4, r = row0 + 8 * nt + q;
+    for (int x = threadIdx.x; x < C::kSlab * (D / 4); x += kWarps * 32) {
+      const int q = x / (D / 4), d = x % (D / 4) * 4, r = row0 + C::kSlab * nt + q;
       if (r < R) {
         float M = minus_inf(), Lsum = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][8 * nt + q][0]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][C::kSlab * nt + q][0]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = stat[w][8 * nt + q][0];
-          Lsum += mw == minus_inf() ? 0.f : stat[w][8 * nt + q][1] * ex2(mw - M);
-          const float4 y = *reinterpret_cast<const float4*>(red + (w * 8 + q) * (D + 4) + d);
+          const float mw = stat[w][C::kSlab * nt + q][0];
+          Lsum += mw == minus_inf() ? 0.f : stat[w][C::kSlab * nt + q][1] * ex2(mw - M);
+          const float4 y = *reinterpret_cast<const float4*>(red + (w * C::kSlab + q) * (D + 4) + d);
           v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
         }
         const int hq = h * a.G + r / c.L, i = r % c.L;
@@ -654,16 +675,18 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(CacheAttnArgs 
 
 // How a call is cut.
 struct Plan {
-  int nt, row_tiles, chunk, splits;
+  int cw, nt, row_tiles, chunk, splits, rows;
 };
 
 Plan make_plan(const CacheAttnArgs& a) {
   Plan p;
   const int R = a.G * a.c.L, most = a.c.D == 256 ? 2 : 4;
+  p.cw = R <= 4 ? 1 : 2;
   p.nt = R <= 8 ? 1 : R <= 16 ? 2 : most;
-  p.row_tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
+  p.rows = 4 * p.cw * p.nt;
+  p.row_tiles = (R + p.rows - 1) / p.rows;
   const int step = 256;  // tokens: at least a unit a warp
-  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.nt == 1 && a.c.D <= 128 ? 2 : 1);
+  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.cw == 1 ? kNarrowBlocks : p.nt == 1 && a.c.D <= 128 ? 2 : 1);
   const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * p.row_tiles;
   // One wave of blocks if there are few pairs; otherwise chunks short enough that sequences
   // of unequal length share the SMs evenly.
@@ -675,12 +698,13 @@ Plan make_plan(const CacheAttnArgs& a) {
   return p;
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int CW>
 cudaError_t attn_nt(const CacheAttnArgs& a, const Plan& p, cudaStream_t s) {
-  auto* kern = cache_attn_kernel<T, D, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::kSmem);
+  using C = Cfg<D, NT, CW>;
+  auto* kern = cache_attn_kernel<T, D, NT, CW>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(p.splits, p.row_tiles * a.c.Hkv, a.c.B), kWarps * 32, Cfg<D, NT>::kSmem, s>>>(a, p.chunk, p.splits, p.row_tiles);
+  kern<<<dim3(p.splits, p.row_tiles * a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(a, p.chunk, p.splits, p.row_tiles);
   return cudaGetLastError();
 }
 
@@ -688,11 +712,12 @@ template <typename T, int D>
 cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
   const Plan p = make_plan(a);
   if (!join) {
+    if (p.cw == 1) return attn_nt<T, D, 1, 1>(a, p, s);
     switch (p.nt) {
-      case 1: return attn_nt<T, D, 1>(a, p, s);
-      case 2: return attn_nt<T, D, 2>(a, p, s);
+      case 1: return attn_nt<T, D, 1, 2>(a, p, s);
+      case 2: return attn_nt<T, D, 2, 2>(a, p, s);
       default:
-        if constexpr (D <= 128) return attn_nt<T, D, 4>(a, p, s);
+        if constexpr (D <= 128) return attn_nt<T, D, 4, 2>(a, p, s);
         return cudaErrorInvalidValue;
     }
   }
@@ -705,7 +730,7 @@ cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, a, p.chunk, p.splits, 8 * p.nt);
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, a, p.chunk, p.splits, p.rows);
 }
 
 template <typename T>
