@@ -221,23 +221,28 @@ def sdpa_cache_page_bytes(page_size, Hkv, D, dtype) -> int:
     return load().sdpa_cache_page_bytes(page_size, Hkv, D, dtype)
 
 
+def _struct(cache):
+    """A ``Cache`` as a pointer, or the bytes of one as they are."""
+    return cache if type(cache) is bytes else ctypes.byref(cache)
+
+
 def sdpa_cache_write(cache, k, v, layouts, counts, B, L, stream):
-    """cache: a ``Cache``; layouts: Int64x6 of k and v."""
-    return load().sdpa_cache_write(ctypes.byref(cache), k, v, layouts, counts, B, L, stream)
+    """cache: a ``Cache``, or its bytes; layouts: Int64x6 of k and v, or their bytes."""
+    return load().sdpa_cache_write(_struct(cache), k, v, layouts, counts, B, L, stream)
 
 
 def sdpa_cache_read(cache, k, v, layouts, B, L, stream):
-    return load().sdpa_cache_read(ctypes.byref(cache), k, v, layouts, B, L, stream)
+    return load().sdpa_cache_read(_struct(cache), k, v, layouts, B, L, stream)
 
 
 def sdpa_cache_attn_workspace_size(cache, B, Hq, Lq, max_len) -> int:
-    return load().sdpa_cache_attn_workspace_size(ctypes.byref(cache), B, Hq, Lq, max_len)
+    return load().sdpa_cache_attn_workspace_size(_struct(cache), B, Hq, Lq, max_len)
 
 
 def sdpa_cache_attn(cache, q, out, lse, sinks, layouts, B, Hq, Lq, scale, is_causal, max_len,
                     workspace, workspace_bytes, stream):
-    """cache: a ``Cache``; layouts: Int64x6 of q and out."""
-    return load().sdpa_cache_attn(ctypes.byref(cache), q, out, lse, sinks, layouts, B, Hq, Lq,
+    """cache: a ``Cache``, or its bytes; layouts: Int64x6 of q and out, or their bytes."""
+    return load().sdpa_cache_attn(_struct(cache), q, out, lse, sinks, layouts, B, Hq, Lq,
                                   scale, is_causal, max_len, workspace, workspace_bytes, stream)
 
 

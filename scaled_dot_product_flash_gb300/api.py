@@ -7,6 +7,7 @@ a non-OK status is raised as ``SdpaError``.  All arithmetic runs in the library.
 from __future__ import annotations
 
 import math
+import struct
 
 import torch
 
@@ -214,14 +215,29 @@ def attention_backward(q, k, v, out, dout, lse, scale=None, is_causal=False, wor
 # ---- rotary embedding
 
 
-def _same_device(q, **others):
-    """q must be on the current device (its context runs the kernels), the others beside it."""
-    if q.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {q.device}, not on the current device: "
-                         "select it with torch.cuda.device")
-    for name, t in others.items():
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} must be on {q.device}")
+# These calls are short on the device, so what a call costs on the host counts: sizes and
+# strides go over as packed bytes, and the current stream's handle is asked for directly.
+_pack3, _pack6, _pack12 = (struct.Struct(f"{n}q").pack for n in (3, 6, 12))
+_pack_cache = struct.Struct("@PiiiiiPqiP").pack  # sdpa_cache_t
+
+
+def _here(*tensors):
+    """Handle of the current stream; every tensor must be on the current device, whose context
+    runs the kernels."""
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"a tensor is on {t.device}, not on the current device, cuda:{d}: "
+                             "select its device with torch.cuda.device")
+    return torch._C._cuda_getCurrentRawStream(d)
+
+
+def _rows_ok(name, t, dtype):
+    """A [B, H, L, D] CUDA tensor of dtype with contiguous rows."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D [B, H, L, D] tensor")
+    if t.dtype is not dtype or not t.is_cuda or t.stride(3) != 1:
+        _check(name, t, dtype)
 
 
 def _dense(t):
@@ -245,11 +261,12 @@ def _positions(positions, B, L):
     """(axes, strides) of positions [L], [B, L] or [axes, B, L]; B may be 1 for all batches."""
     if positions.dtype not in (torch.int32, torch.int64):
         raise ValueError("positions must be int32 or int64")
-    shape, strides = (1,) * (3 - positions.dim()) + tuple(positions.shape), positions.stride()
+    shape, strides = tuple(positions.shape), positions.stride()
+    if len(shape) < 3:
+        shape, strides = (1,) * (3 - len(shape)) + shape, (0,) * (3 - len(shape)) + strides
     if len(shape) != 3 or shape[1] not in (1, B) or shape[2] != L or shape[0] < 1:
         raise ValueError(f"positions {tuple(positions.shape)} must be [L], [B, L] or [axes, B, L] "
                          f"with L = {L} and B = {B} or 1")
-    strides = (0,) * (3 - len(strides)) + strides
     return shape[0], [0 if n == 1 else s for n, s in zip(shape, strides)]
 
 
@@ -257,46 +274,49 @@ def _rotary(q, k, positions, inv_freq, axes, adjacent, inverse, q_out, k_out, st
     if stream is not None and stream != torch.cuda.current_stream():
         with torch.cuda.stream(stream):  # outputs then belong to that stream
             return _rotary(q, k, positions, inv_freq, axes, adjacent, inverse, q_out, k_out, None)
-    _check("q", q)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, H, L, D]")
+    dtype = q.dtype
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"q has dtype {dtype}, expected fp32, fp16 or bf16")
+    _rows_ok("q", q, dtype)
     B, Hq, L, D = q.shape
-    if k is not None:
-        _check("k", k, q.dtype)
-        if k.dim() != 4 or k.shape[0] != B or k.shape[2] != L or k.shape[3] != D:
-            raise ValueError("q and k disagree in batch, rows or head dim")
-    if q.dtype not in DTYPE_CODE:
-        raise ValueError(f"q has dtype {q.dtype}, expected fp32, fp16 or bf16")
-    _same_device(q, k=k, positions=positions, inv_freq=inv_freq, axes=axes, q_out=q_out, k_out=k_out)
     naxes, at = _positions(positions, B, L)
-    _check("inv_freq", inv_freq, torch.float32)
-    if inv_freq.dim() != 1 or not 2 <= 2 * inv_freq.numel() <= D:
-        raise ValueError("inv_freq must be 1-D, one frequency a pair, at most D/2")
-    if axes is not None:
-        _check("axes", axes, torch.int32)
-        if axes.shape != inv_freq.shape:
-            raise ValueError("axes must have one axis for each of inv_freq's pairs")
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    _check("q_out", q_out, q.dtype)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    strides = (*_dense(q), 0, 0, 0, *_dense(q_out), 0, 0, 0)
+    pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous() or not 2 <= 2 * pairs <= D:
+        raise ValueError("inv_freq must be a contiguous 1-D fp32 tensor, one frequency a pair, at "
+                         "most D/2")
+    if axes is not None and (axes.dtype is not torch.int32 or axes.shape != inv_freq.shape
+                             or not axes.is_contiguous()):
+        raise ValueError("axes must be a contiguous int32 tensor, one axis for each of inv_freq's "
+                         "pairs")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _rows_ok("q_out", q_out, dtype)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    Hkv, ks, kos = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        _check("k_out", k_out, q.dtype)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        strides = (*strides[:3], *_dense(k), *strides[6:9], *_dense(k_out))
+        _rows_ok("k", k, dtype)
+        Hkv = k.shape[1]
+        if k.shape[0] != B or k.shape[2] != L or k.shape[3] != D:
+            raise ValueError("q and k disagree in batch, rows or head dim")
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        else:
+            _rows_ok("k_out", k_out, dtype)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
+        ks, kos = _dense(k), _dense(k_out)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     st = _lib.sdpa_rotary(
         q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
         None if k is None else k_out.data_ptr(), positions.data_ptr(),
-        64 if positions.dtype == torch.int64 else 32, _lib.Int64x3(*at), inv_freq.data_ptr(),
-        None if axes is None else axes.data_ptr(), naxes, B, Hq, 0 if k is None else k.shape[1], L,
-        D, 2 * inv_freq.numel(),
+        64 if positions.dtype is torch.int64 else 32, _pack3(*at), inv_freq.data_ptr(),
+        None if axes is None else axes.data_ptr(), naxes, B, Hq, Hkv, L, D, 2 * pairs,
         (_lib.ROTARY_ADJACENT if adjacent else 0) | (_lib.ROTARY_INVERSE if inverse else 0),
-        DTYPE_CODE[q.dtype], _lib.Int64x12(*strides), _stream(None))
+        DTYPE_CODE[dtype], _pack12(*_dense(q), *ks, *_dense(q_out), *kos),
+        _here(q, k, positions, inv_freq, axes, q_out, k_out))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_rotary")
     return q_out, k_out
@@ -339,29 +359,28 @@ def cache_empty(num_pages, num_kv_heads, page_size, head_dim, dtype=torch.bfloat
 
 
 def _cache(cache, pages, lens, B):
-    """The library's view of a cache with one call's page table [B, n] and lengths [B]."""
-    if not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 10:
+    """sdpa_cache_t, packed: a cache with one call's page table [B, n] and lengths [B]."""
+    dtype = cache.dtype
+    if cache.dim() != 4 or not cache.is_cuda or not cache.is_contiguous() or cache.shape[3] % 10:
         raise ValueError("cache must be a contiguous CUDA tensor made by cache_empty")
-    if cache.dtype not in (torch.float16, torch.bfloat16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError("cache must be fp16 or bf16")
-    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != B or pages.stride(1) != 1:
+    if pages.dtype is not torch.int32 or pages.dim() != 2 or pages.shape[0] != B or pages.stride(1) != 1:
         raise ValueError(f"pages must be an int32 [{B}, n] tensor with contiguous rows")
-    if lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
         raise ValueError(f"lens must be a contiguous int32 [{B}] tensor")
     n, H, tiles, width = cache.shape
-    width_p = pages.shape[1]
-    return _lib.Cache(cache.data_ptr(), n, 16 * tiles, H, width // 10, DTYPE_CODE[cache.dtype],
-                      pages.data_ptr(), pages.stride(0) if B > 1 else width_p, width_p,
-                      lens.data_ptr())
+    entries = pages.shape[1]
+    return _pack_cache(cache.data_ptr(), n, 16 * tiles, H, width // 10, DTYPE_CODE[dtype],
+                       pages.data_ptr(), pages.stride(0) if B > 1 else entries, entries,
+                       lens.data_ptr())
 
 
-def _cache_rows(name, t, cache, B=None, L=None):
+def _cache_rows(name, t, cache, B, L):
     """Checks a [B, Hkv, L, D] tensor of rows of the cache."""
-    _check(name, t, cache.dtype)
-    if t.dim() != 4 or t.shape[1] != cache.shape[1] or 10 * t.shape[3] != cache.shape[3]:
-        raise ValueError(f"{name} must be [B, Hkv, L, D] of the cache's heads and head dim")
-    if B is not None and (t.shape[0], t.shape[2]) != (B, L):
-        raise ValueError(f"{name} must have {B} sequences of {L} rows")
+    _rows_ok(name, t, cache.dtype)
+    if t.shape != (B, cache.shape[1], L, cache.shape[3] // 10):
+        raise ValueError(f"{name} must be [{B}, Hkv, {L}, D] of the cache's heads and head dim")
 
 
 def cache_write(cache, k, v, pages, lens, counts=None, stream=None):
@@ -376,16 +395,17 @@ def cache_write(cache, k, v, pages, lens, counts=None, stream=None):
     if stream is not None and stream != torch.cuda.current_stream():
         with torch.cuda.stream(stream):
             return cache_write(cache, k, v, pages, lens, counts)
-    _cache_rows("k", k, cache)
+    c = _cache(cache, pages, lens, k.shape[0])
+    _rows_ok("k", k, cache.dtype)
     B, L = k.shape[0], k.shape[2]
+    _cache_rows("k", k, cache, B, L)
     _cache_rows("v", v, cache, B, L)
-    c = _cache(cache, pages, lens, B)
-    if counts is not None and (counts.dtype != torch.int32 or counts.shape != (B,)
+    if counts is not None and (counts.dtype is not torch.int32 or counts.shape != (B,)
                                or not counts.is_contiguous()):
         raise ValueError(f"counts must be a contiguous int32 [{B}] tensor")
-    _same_device(k, cache=cache, v=v, pages=pages, lens=lens, counts=counts)
-    st = _lib.sdpa_cache_write(c, k.data_ptr(), v.data_ptr(), _lib.Int64x6(*_dense(k), *_dense(v)),
-                               None if counts is None else counts.data_ptr(), B, L, _stream(None))
+    st = _lib.sdpa_cache_write(c, k.data_ptr(), v.data_ptr(), _pack6(*_dense(k), *_dense(v)),
+                               None if counts is None else counts.data_ptr(), B, L,
+                               _here(cache, k, v, pages, lens, counts))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_cache_write")
 
@@ -399,13 +419,16 @@ def cache_read(cache, pages, lens, rows, k=None, v=None, stream=None):
     B = lens.shape[0]
     c = _cache(cache, pages, lens, B)
     shape = (B, cache.shape[1], rows, cache.shape[3] // 10)
-    k = torch.empty(shape, dtype=cache.dtype, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=cache.dtype, device=cache.device) if v is None else v
-    _cache_rows("k", k, cache, B, rows)
-    _cache_rows("v", v, cache, B, rows)
-    _same_device(cache, k=k, v=v, pages=pages, lens=lens)
-    st = _lib.sdpa_cache_read(c, k.data_ptr(), v.data_ptr(), _lib.Int64x6(*_dense(k), *_dense(v)),
-                              B, rows, _stream(None))
+    if k is None:
+        k = cache.new_empty(shape)
+    else:
+        _cache_rows("k", k, cache, B, rows)
+    if v is None:
+        v = cache.new_empty(shape)
+    else:
+        _cache_rows("v", v, cache, B, rows)
+    st = _lib.sdpa_cache_read(c, k.data_ptr(), v.data_ptr(), _pack6(*_dense(k), *_dense(v)), B, rows,
+                              _here(cache, pages, lens, k, v))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_cache_read")
     return k, v
@@ -426,38 +449,36 @@ def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
         with torch.cuda.stream(stream):
             return cache_attention(q, cache, pages, lens, scale, is_causal, need_lse, out, lse,
                                    sinks, max_len, workspace)
-    _check("q", q, cache.dtype)
-    if q.dim() != 4 or 10 * q.shape[3] != cache.shape[-1]:
-        raise ValueError("q must be [B, Hq, L, D] of the cache's head dim")
+    _rows_ok("q", q, cache.dtype)
     B, Hq, L, D = q.shape
     c = _cache(cache, pages, lens, B)
-    out = torch.empty_like(q) if out is None else out
-    _check("out", out, q.dtype)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if need_lse and lse is None:
-        lse = torch.empty((B, Hq, L), device=q.device, dtype=torch.float32)
+    if 10 * D != cache.shape[3]:
+        raise ValueError("q must be [B, Hq, L, D] of the cache's head dim")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _rows_ok("out", out, q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if not need_lse:
         lse = None
-    elif lse.shape != (B, Hq, L) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    elif lse is None:
+        lse = torch.empty((B, Hq, L), device=q.device, dtype=torch.float32)
+    elif lse.shape != (B, Hq, L) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [B, Hq, L] tensor")
     if sinks is not None:
         _check_sinks("sinks", sinks, Hq)
-    _same_device(q, cache=cache, pages=pages, lens=lens, out=out, lse=lse, sinks=sinks,
-                 workspace=workspace)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     max_len = 0 if max_len is None else int(max_len)
     need = _lib.sdpa_cache_attn_workspace_size(c, B, Hq, L, max_len)
     if workspace is None and need:
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-    st = _lib.sdpa_cache_attn(c, q.data_ptr(), out.data_ptr(),
-                              None if lse is None else lse.data_ptr(),
-                              None if sinks is None else sinks.data_ptr(),
-                              _lib.Int64x6(*_dense(q), *_dense(out)), B, Hq, L, scale,
-                              _causal(is_causal), max_len,
-                              None if workspace is None else workspace.data_ptr(),
-                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                              _stream(None))
+    st = _lib.sdpa_cache_attn(
+        c, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if sinks is None else sinks.data_ptr(), _pack6(*_dense(q), *_dense(out)), B, Hq, L,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _causal(is_causal), max_len,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _here(q, cache, pages, lens, out, lse, sinks, workspace))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_cache_attn")
     return out, lse

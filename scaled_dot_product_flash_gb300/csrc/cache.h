@@ -73,16 +73,8 @@ struct Tile {
   static constexpr int W = NG < 4 ? NG : 4;
   static constexpr int JB = NG / W;
   static constexpr int kK = 0, kV = 8 * D, kKp = 16 * D, kVp = 18 * D, kBytes = 20 * D;
-  // 32-bit word that holds elements 32j + 8t .. + 7 of key row r.
-  static __host__ __device__ constexpr int k_word(int r, int t, int j) {
-    return (((r / 8 * JB + j / W) * 8 + r % 8) * 4 + t) * W + j % W;
-  }
-  // Half-word that holds elements 32j + 4g .. + 3 of value row r.
-  static __host__ __device__ constexpr int v_half(int r, int g, int j) {
-    return 2 * ((((r / 8 * JB + j / W) * 8 + g) * 4 + r % 8 / 2) * W + j % W) + r % 2;
-  }
-  // Word (s in its low half, z in its high half) of group j of row r, from kKp or kVp.
-  static __host__ __device__ constexpr int param(int r, int j) { return (j / W * 16 + r) * W + j % W; }
+  // Lane 4g + t of a warp reads the K and V codes as pieces [row half][jb][lane] of W words, and
+  // the parameters of row r as piece [jb][r] of W words (s in the low half, z in the high one).
 };
 
 // Tokens of sequence b that a call may touch: lens[b] within 0..most, reported otherwise.
@@ -118,5 +110,21 @@ template <>
 __device__ __forceinline__ uint32_t f_to_bits<__half>(float x) { return __half_as_ushort(__float2half_rn(x)); }
 template <>
 __device__ __forceinline__ uint32_t f_to_bits<__nv_bfloat16>(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+
+// Two values rounded to 16-bit elements, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 }  // namespace sdpa

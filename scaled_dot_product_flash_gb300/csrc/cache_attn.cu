@@ -23,6 +23,8 @@
 //    the probabilities take the scale, P·s in fp16 (normalised by a power of two that follows
 //    the largest scale, rounded once, 2^-11 relative); P·z is summed in fp32 FMAs.
 //    So scores are exact up to fp32 sums, and P·s is the only rounding to fewer bits.
+#include <atomic>
+
 #include "cache.h"
 #include "tc_common.cuh"
 
@@ -56,19 +58,16 @@ struct Cfg {
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
   static constexpr int kMerge = kWarps * kSlab * (D + 4) * 4;  // a slab of rows of every warp's output
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kQ = NT > 1 ? NT * (D / kGroup) * 32 * 16 : 0;  // q fragments
-  static constexpr int kSmem = kBody + kQ;
+  static constexpr int kQ = kBody;                              // q fragments: [group][NT][lane] of 16 bytes
+  static constexpr int kSums = kQ + NT * Tl::NG * 32 * 16;      // q's group sums, fp32 [row][group]
+  static constexpr int kExps = kSums + kRows * Tl::NG * 4;      // q's exponents, int [row]
+  static constexpr int kSmem = kExps + kRows * 4;
 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 // Transposes an 8 x 8 matrix of 16-bit elements held two a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -159,38 +158,39 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   const int start = (int)first, end = (int)min((int64_t)end_all, first + chunk);
   const int units = end > start ? (end - start + C::kUnit - 1) / C::kUnit : 0;
 
-  if (lane < C::kStages) tc::mbar_init(&full[warp][lane], 1);
+  // ---- the first copies
+  if (lane < C::kStages) {
+    tc::mbar_init(&full[warp][lane], 1);
+    tc::fence_mbar_init();
+  }
   if (threadIdx.x == 0) abort_flag = 0;
-  tc::fence_mbar_init();
-  __syncthreads();
+  __syncwarp();
   const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidCacheAttn};
-
   uint8_t* ring = smem + warp * (C::kStages * C::kUnitBytes);
-  uint32_t there = 0;  // bit s·UT + tile: the tile in stage s was copied
-  // The tile that this lane copies next: its position, its place in the page table and its
-  // offset in the page, which move on by a fixed step.
-  int pos = start + warp * C::kUnit + lane * kTile;
-  int slot = pos / c.page_size, off = pos % c.page_size;
-  const int step_slots = kWarps * C::kUnit / c.page_size, step_off = kWarps * C::kUnit % c.page_size;
   const int* table = c.pages + b * c.pages_stride;
   const int64_t page_bytes = (int64_t)c.Hkv * (c.page_size / kTile) * Tl::kBytes;
   const uint8_t* head = c.data + (int64_t)h * (c.page_size / kTile) * Tl::kBytes;
-  // Starts the copies of this warp's next unit into stage s (all lanes call it).
-  auto issue = [&](int s) {
-    int page = -1;
-    if (lane < UT && pos < end) {
-      page = table[slot];
-      if ((unsigned)page >= (unsigned)c.num_pages) {
-        report_error(c.err, kDevErrIndex, kKidCacheAttn);
-        page = -1;
-      }
-    }
-    const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
-    there = (there & ~(((1u << UT) - 1) << (s * UT))) | (ok << (s * UT));
-    if (lane == 0) tc::mbar_arrive_expect_tx(&full[warp][s], __popc(ok) * Tl::kBytes);
-    __syncwarp();
-    if (page >= 0)
-      bulk_copy(ring + s * C::kUnitBytes + lane * Tl::kBytes, head + page * page_bytes + off / kTile * Tl::kBytes, Tl::kBytes, &full[warp][s]);
+  // Page of a tile at position pos (entry `slot` of the table), or -1: past the end, or bad.
+  auto page_at = [&](int pos, int slot) {
+    if (pos >= end) return -1;
+    const int page = table[slot];
+    if ((unsigned)page < (unsigned)c.num_pages) return page;
+    report_error(c.err, kDevErrIndex, kKidCacheAttn);
+    return -1;
+  };
+  // Lane st·UT + i starts with tile i of this warp's unit for stage st.  Later lane i copies tile
+  // i of every unit: it keeps that tile's position, its place in the table and its offset in
+  // the page, which move on by a fixed step, and has its page looked up one unit ahead.
+  int pos = start + (warp + lane / UT * kWarps) * C::kUnit + lane % UT * kTile;
+  int slot = pos / c.page_size, off = pos % c.page_size;
+  int page = lane < C::kStages * UT ? page_at(pos, slot) : -1;
+  uint32_t there = __ballot_sync(0xffffffffu, page >= 0);  // bit st·UT + i: tile i of stage st is copied
+  if (lane < C::kStages && warp + lane * kWarps < units)
+    tc::mbar_arrive_expect_tx(&full[warp][lane], __popc((there >> (lane * UT)) & ((1u << UT) - 1)) * Tl::kBytes);
+  __syncwarp();
+  if (page >= 0) bulk_copy(ring + lane * Tl::kBytes, head + page * page_bytes + off / kTile * Tl::kBytes, Tl::kBytes, &full[warp][lane / UT]);
+  const int step_slots = kWarps * C::kUnit / c.page_size, step_off = kWarps * C::kUnit % c.page_size;
+  auto advance = [&] {
     pos += kWarps * C::kUnit;
     slot += step_slots;
     off += step_off;
@@ -199,86 +199,97 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       ++slot;
     }
   };
-  int issued = warp;  // next unit to start
 #pragma unroll
-  for (int s = 0; s < C::kStages; ++s, issued += kWarps)
-    if (issued < units) issue(s);
+  for (int n = 0; n < C::kStages; ++n) advance();
+  page = lane < UT ? page_at(pos, slot) : -1;
+  // Starts the copies of this warp's next unit into stage s (all lanes call it).
+  auto issue = [&](int s) {
+    const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+    there = (there & ~(((1u << UT) - 1) << (s * UT))) | (ok << (s * UT));
+    if (lane == 0) tc::mbar_arrive_expect_tx(&full[warp][s], __popc(ok) * Tl::kBytes);
+    __syncwarp();
+    if (page >= 0)
+      bulk_copy(ring + s * C::kUnitBytes + lane * Tl::kBytes, head + page * page_bytes + off / kTile * Tl::kBytes, Tl::kBytes, &full[warp][s]);
+    advance();
+    page = lane < UT ? page_at(pos, slot) : -1;
+  };
+  int issued = warp + C::kStages * kWarps;  // next unit to start
 
-  // Query rows as the B operand: lane (g, t) holds, of row g and each group, elements 8t..8t+7,
-  // times a power of two that brings the row's largest to 2^13..2^14 (exact in fp16 down to
-  // 2^-27 of that); the odd nibbles' elements are divided by the 16 that their codes carry.
+  // ---- query rows as the B operand, through shared memory.  A row is multiplied by the power of
+  // two that brings its largest element to 2^13..2^14 (exact in fp16 down to 2^-27 of that), and by
+  // the sign of the scale, so that the largest score is the largest accumulator (0 for a scale of
+  // zero).  Lane (g, t) of a fragment has row g's elements 8t..8t+7 of a group, those of odd
+  // nibbles divided by the 16 that their codes carry.
+  uint16_t* const q_frag = reinterpret_cast<uint16_t*>(smem + C::kQ);
+  float* const q_sum = reinterpret_cast<float*>(smem + C::kSums);
+  int* const q_exp = reinterpret_cast<int*>(smem + C::kExps);
+  const int R = a.G * c.L, row0 = rt * C::kRows;
+  for (int rr = warp; rr < C::kRows; rr += kWarps) {
+    const int r = row0 + rr;
+    float x[NG], top = 0.f;
+    const T* q = r < R ? row_ptr<T>(a.q, a.lq, b, h * a.G + r / c.L, r % c.L) + lane : nullptr;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) x[j] = q ? Elem<T>::to_f(q[32 * j]) : 0.f;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) top = fmaxf(top, fabsf(x[j]));
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    // A row of zeros (or subnormals) takes 2^100; one with an infinity 2^-100, and turns NaN by itself.
+    const int e = max(-100, min(100, 13 - ((__float_as_int(top) >> 23) - 127)));
+    const float up = a.scale_log2 == 0.f ? 0.f : copysignf(pow2(e), a.scale_log2);
+    const int nt = CW == 2 ? rr / 8 : 0, g_row = CW == 2 ? rr % 8 : 2 * rr;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      x[j] *= up;
+      const int n = lane % 8;  // element 8·(lane / 8) + n of the group
+      const float v = n & 1 ? x[j] * 0.0625f : x[j];
+      q_frag[((j * NT + nt) * 32 + g_row * 4 + lane / 8) * 8 + n % 4 * 2 + n / 4] = (uint16_t)f_to_bits<__half>(v);
+    }
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) x[j] += __shfl_xor_sync(0xffffffffu, x[j], off);
+      if (lane == j) q_sum[rr * NG + j] = x[j];
+    }
+    if (lane == 0) q_exp[rr] = e;
+  }
+  __syncthreads();
   // The z term's share has bf16's range to be in the accumulators' units (2^-24) at once; in
   // fp16 it stays at 2^13 or less and is scaled after its MMA.
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr float kZUp = kHalf ? 0x1p-6f : 0x1p-24f;
+  const uint4* qs = reinterpret_cast<const uint4*>(smem + C::kQ);
+  const bool row_here = CW == 2 || g % 2 == 0;  // odd columns of the narrow form are zero
   uint32_t qf[kQSmem ? 1 : NG][4];
-  uint4* qs = reinterpret_cast<uint4*>(smem + C::kBody);
+  if constexpr (!kQSmem) {
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row_here) v = qs[j * 32 + lane];
+      qf[j][0] = v.x; qf[j][1] = v.y; qf[j][2] = v.z; qf[j][3] = v.w;
+    }
+  }
   uint32_t qz[NT][JB][2];  // group sums of the row, split in three (z term)
   float f[NT][CW];         // per row of this lane's columns: |scale|·log2e·2^(24 - e) > 0
   int lim[NT][CW];         // the same: positions below this are visible
-  const int R = a.G * c.L, row0 = rt * C::kRows;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = CW == 2 ? row0 + 8 * nt + g : g % 2 == 0 ? row0 + g / 2 : R;  // R: no row
-    float x[NG][8];
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (r < R) w = *reinterpret_cast<const uint4*>(row_ptr<T>(a.q, a.lq, b, h * a.G + r / c.L, r % c.L) + 32 * j + 8 * t);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[j][e] = bits_to_f<T>((ws[e / 2] >> (16 * (e & 1))) & 0xffffu);
-        top = fmaxf(top, fabsf(x[j][e]));
-      }
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^e·top in [2^13, 2^14).  A row of zeros (or subnormals) takes 2^100, an infinite one
-    // 2^-100 and turns NaN by itself.
-    const int e = max(-100, min(100, 13 - ((__float_as_int(top) >> 23) - 127)));
-    // The scale's sign goes into q, so that the largest score is the largest accumulator; a
-    // scale of zero makes q zero.
-    const float up = a.scale_log2 == 0.f ? 0.f : copysignf(pow2(e), a.scale_log2);
-    float sums[JB] = {};
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        x[j][n] *= up;
-        sum += x[j][n];
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (j % 4 == t) sums[j / 4] = sum;
-      const uint32_t f0 = pack_h2(x[j][0], x[j][4]), f1 = pack_h2(x[j][1] * 0.0625f, x[j][5] * 0.0625f);
-      const uint32_t f2 = pack_h2(x[j][2], x[j][6]), f3 = pack_h2(x[j][3] * 0.0625f, x[j][7] * 0.0625f);
-      if constexpr (kQSmem) {
-        if (warp == 0) qs[(j * NT + nt) * 32 + lane] = make_uint4(f0, f1, f2, f3);
-      } else {
-        qf[j][0] = f0; qf[j][1] = f1; qf[j][2] = f2; qf[j][3] = f3;
-      }
-    }
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb) {  // sums·kZUp = hi + mid + lo in T
-      const float s6 = sums[jb] * kZUp;
-      const uint32_t hi = f_to_bits<T>(s6);
-      const float rest = s6 - bits_to_f<T>(hi);
+      float sum = 0.f;
+      if (row_here && (W == 4 || t < W)) sum = q_sum[(CW == 2 ? 8 * nt + g : g / 2) * NG + 4 * jb + t] * kZUp;
+      const uint32_t hi = f_to_bits<T>(sum);
+      const float rest = sum - bits_to_f<T>(hi);
       const uint32_t mid = f_to_bits<T>(rest);
       qz[nt][jb][0] = hi | (mid << 16);
       qz[nt][jb][1] = f_to_bits<T>(rest - bits_to_f<T>(mid));
     }
 #pragma unroll
     for (int n = 0; n < CW; ++n) {  // the accumulators' columns are 2t and 2t + 1
-      const int src = __shfl_sync(0xffffffffu, e, (2 * t + n) * 4);
-      f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(24 - src), 1e-37f);
-      const int rr = row0 + C::kSlab * nt + CW * t + n;
-      lim[nt][n] = a.causal ? len - c.L + rr % c.L + 1 : len;
+      const int rr = C::kSlab * nt + CW * t + n;
+      f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(24 - q_exp[rr]), 1e-37f);
+      lim[nt][n] = a.causal ? len - c.L + (row0 + rr) % c.L + 1 : len;
     }
   }
-  if constexpr (kQSmem) __syncthreads();
   const int seen = a.causal ? len - c.L + 1 : len;  // every row sees the positions below this
 
   float o[2 * NG][NT][4];  // O^T, times 2^(k - 24)
@@ -488,14 +499,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
                 if constexpr (kMasked) zo[nt][j][n] += p == 0.f ? 0.f : p * z;  // a hidden key's z may be NaN
                 else zo[nt][j][n] = fmaf(p, z, zo[nt][j][n]);
               }
-              hi[hf] = pack_h2(q[hf][0], q[hf][1]);
+              hi[hf] = pack2<__half>(q[hf][0], q[hf][1]);
             }
             uint32_t b0 = transpose8(hi[0]), b1 = transpose8(hi[1]);
             mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
             mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
             if constexpr (kHalf) {  // what the rounding lost: outputs in fp16 would show it
-              b0 = transpose8(pack_h2(q[0][0] - low_h(hi[0]), q[0][1] - high_h(hi[0])));
-              b1 = transpose8(pack_h2(q[1][0] - low_h(hi[1]), q[1][1] - high_h(hi[1])));
+              b0 = transpose8(pack2<__half>(q[0][0] - low_h(hi[0]), q[0][1] - high_h(hi[0])));
+              b1 = transpose8(pack2<__half>(q[1][0] - low_h(hi[1]), q[1][1] - high_h(hi[1])));
               mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
               mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
             }
@@ -603,8 +614,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         } else {
           const float fold = fold_sink(a.sinks, hq, M, Lsum), inv = Lsum == 0.f ? 0.f : fold / Lsum;
           T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
-          *reinterpret_cast<uint2*>(out) = make_uint2(f_to_bits<T>(v.x * inv) | (f_to_bits<T>(v.y * inv) << 16),
-                                                      f_to_bits<T>(v.z * inv) | (f_to_bits<T>(v.w * inv) << 16));
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
           if (a.lse && d == 0) a.lse[row] = Lsum == 0.f ? minus_inf() : (M + log2f(Lsum)) * kLn2;
         }
       }
@@ -668,19 +678,21 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(CacheAttnArgs 
   }
   const float fold = fold_sink(a.sinks, hq, M, L), inv = L == 0.f ? 0.f : fold / L;
   T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
-  *reinterpret_cast<uint2*>(out) = make_uint2(f_to_bits<T>(v.x * inv) | (f_to_bits<T>(v.y * inv) << 16),
-                                              f_to_bits<T>(v.z * inv) | (f_to_bits<T>(v.w * inv) << 16));
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
   if (a.lse && d == 0) a.lse[row] = L == 0.f ? minus_inf() : (M + log2f(L)) * kLn2;
 }
 
 // How a call is cut.
+#ifndef NTM
+#define NTM 2
+#endif
 struct Plan {
   int cw, nt, row_tiles, chunk, splits, rows;
 };
 
 Plan make_plan(const CacheAttnArgs& a) {
   Plan p;
-  const int R = a.G * a.c.L, most = a.c.D == 256 ? 2 : 4;
+  const int R = a.G * a.c.L, most = a.c.D == 256 ? 2 : NTM;
   p.cw = R <= 4 ? 1 : 2;
   p.nt = R <= 8 ? 1 : R <= 16 ? 2 : most;
   p.rows = 4 * p.cw * p.nt;
@@ -688,11 +700,19 @@ Plan make_plan(const CacheAttnArgs& a) {
   const int step = 256;  // tokens: at least a unit a warp
   const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.cw == 1 ? kNarrowBlocks : p.nt == 1 && a.c.D <= 128 ? 2 : 1);
   const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * p.row_tiles;
-  // One wave of blocks if there are few pairs; otherwise chunks short enough that sequences
-  // of unequal length share the SMs evenly.
-  const int64_t want = pairs >= slots ? 1 : slots / pairs;
+#ifndef CW_
+#define CW_ 1
+#endif
+#ifndef CM_
+#define CM_ 2048
+#endif
+#ifndef CN_
+#define CN_ 512
+#endif
+  const int64_t want = max((int64_t)1, CW_ * slots / pairs);
   int64_t chunk = (a.max_len + want - 1) / want;
-  if (chunk > 2048 && pairs * 4 > slots) chunk = 2048;
+  if (pairs * 4 > slots) chunk = min(chunk, (int64_t)CM_);
+  chunk = max(chunk, (int64_t)CN_);
   p.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
   p.splits = (a.max_len + p.chunk - 1) / p.chunk;
   return p;
@@ -702,8 +722,17 @@ template <typename T, int D, int NT, int CW>
 cudaError_t attn_nt(const CacheAttnArgs& a, const Plan& p, cudaStream_t s) {
   using C = Cfg<D, NT, CW>;
   auto* kern = cache_attn_kernel<T, D, NT, CW>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  // The shared-memory limit is set once on each device.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   kern<<<dim3(p.splits, p.row_tiles * a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(a, p.chunk, p.splits, p.row_tiles);
   return cudaGetLastError();
 }

@@ -4,12 +4,13 @@
 // Pair p of a row turns by the angle position·inv_freq[p].  Far positions make that angle
 // thousands of turns, of which only the fraction counts, so it is computed modulo one turn in
 // 64-bit integers: inv_freq/2π as a fraction of 2^64 (a 24-bit mantissa times 2^64/2π,
-// shifted), times the position, wraps by itself.  No fp64 and no range reduction is left;
-// sincospif takes the signed top 32 bits.
+// shifted), times the position, wraps by itself.  No fp64 and no range reduction is left: the
+// top two bits are the quadrant, the rest is an angle within π/4 of it.
 //
-// Bound: HBM (each element read and written once; a sine and a cosine a pair and token,
-// shared by the heads).  A thread keeps the sines and cosines of VP pairs of one token in
-// registers and runs over a range of heads with 16-byte loads and stores.
+// Bound: HBM (each element read and written once).  A block takes a few tokens: its threads
+// compute their sines and cosines once, into shared memory, while the first heads' loads are
+// on their way; then a thread keeps those of VP pairs of one token in registers and turns that
+// token's heads hg, hg + HG, ... in 16-byte pieces.
 #include "cache.h"
 
 namespace sdpa {
@@ -32,75 +33,137 @@ __device__ __forceinline__ uint64_t turns_per_step(float f) {
   return (bits >> 31) ? 0 - r : r;
 }
 
+// Cosine and sine of a phase in units of 2^-32 turns.  x in [-π/4, π/4] is the distance from
+// the nearest quarter turn; Taylor's series to x^8 and x^9 leave 2.4e-8 and 2e-9 there.
+__device__ __forceinline__ float2 cos_sin(uint32_t phase) {
+  const uint32_t quarter = (phase + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(phase - (quarter << 30)) * 1.4629180792671596e-9f;  // 2π / 2^32
+  const float y = x * x;
+  const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+  return make_float2(((quarter + 1) & 2) ? -a : a, (quarter & 2) ? -b : b);
+}
+
 template <typename T, int N>
 struct __align__(N * sizeof(T)) Vec {
   T v[N];
 };
 
-// VP pairs a thread: PAIRED vectors of VP elements at p and p + rot/2, or one of 2·VP
-// adjacent ones.  VP = 1 is the form for any rot.
+__device__ __forceinline__ void turn(float& u, float& w, float c, float s) {
+  const float a = u * c - w * s;
+  w = w * c + u * s;
+  u = a;
+}
+
+// Turns VP pairs: x[e], y[e], or (adjacent) x[2e], x[2e + 1].  16-bit elements are unpacked and
+// packed two at a time.
 template <typename T, bool ADJ, int VP>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int slots, int tail, int rows_per_block, int heads) {
-  constexpr int NV = ADJ ? 2 * VP : VP;  // elements a vector
-  using V = Vec<T, NV>;
-  const int all = slots + tail;
-  const int lrow = threadIdx.x / all, slot = threadIdx.x % all;
-  const int64_t row = (int64_t)blockIdx.x * rows_per_block + lrow;
-  if (lrow >= rows_per_block || row >= (int64_t)a.B * a.L) return;
-  const int b = (int)(row / a.L), i = (int)(row % a.L);
-  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.Hq + a.Hkv);
-  if (slot >= slots) {  // elements past rot are copied
-    const int d = a.rot + (slot - slots) * NV;
-    for (int h = h0; h < h1; ++h) {
-      const bool is_q = h < a.Hq;
-      const T* src = is_q ? row_ptr<T>(a.q, a.lq, b, h, i) : row_ptr<T>(a.k, a.lk, b, h - a.Hq, i);
-      T* dst = is_q ? row_ptr<T>(a.q_out, a.lqo, b, h, i) : row_ptr<T>(a.k_out, a.lko, b, h - a.Hq, i);
-      if (dst != src) *reinterpret_cast<V*>(dst + d) = *reinterpret_cast<const V*>(src + d);
-    }
-    return;
-  }
-  const int p0 = slot * VP, half = a.rot / 2;
-  float cs[VP], sn[VP];
+__device__ __forceinline__ void turn_pairs(Vec<T, ADJ ? 2 * VP : VP>& x, Vec<T, ADJ ? 2 * VP : VP>& y, const float (&cs)[VP], const float (&sn)[VP]) {
+  if constexpr (sizeof(T) == 2 && (ADJ || VP % 2 == 0)) {
+    uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+    uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
-  for (int e = 0; e < VP; ++e) {
-    int axis = a.axes ? a.axes[p0 + e] : 0;
+    for (int e = 0; e < (ADJ ? VP : VP / 2); ++e) {
+      float a = bits_to_f<T>(xw[e] & 0xffffu), b = bits_to_f<T>(xw[e] >> 16);
+      if constexpr (ADJ) {
+        turn(a, b, cs[e], sn[e]);
+      } else {
+        float c = bits_to_f<T>(yw[e] & 0xffffu), d = bits_to_f<T>(yw[e] >> 16);
+        turn(a, c, cs[2 * e], sn[2 * e]);
+        turn(b, d, cs[2 * e + 1], sn[2 * e + 1]);
+        yw[e] = pack2<T>(c, d);
+      }
+      xw[e] = pack2<T>(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VP; ++e) {
+      T& u = ADJ ? x.v[2 * e] : x.v[e];
+      T& w = ADJ ? x.v[2 * e + 1] : y.v[e];
+      float a = Elem<T>::to_f(u), b = Elem<T>::to_f(w);
+      turn(a, b, cs[e], sn[e]);
+      u = Elem<T>::from_f(a);
+      w = Elem<T>::from_f(b);
+    }
+  }
+}
+
+// VP pairs a thread: vectors of VP elements at p and p + rot/2, or one of 2·VP adjacent ones.
+// VP = 1 is the form for any rot.
+template <typename T, bool ADJ, int VP>
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int slots, int tail, int tokens, int groups) {
+  constexpr int NV = ADJ ? 2 * VP : VP;  // elements a vector
+  constexpr int kBatch = sizeof(T) == 4 ? 4 : 2;  // heads whose loads a thread has in flight
+  using V = Vec<T, NV>;
+  extern __shared__ __align__(16) float tables[];  // cosines, then sines: [tokens][rot / 2]
+  const int half = a.rot / 2, all = slots + tail, H = a.Hq + a.Hkv;
+  const unsigned row0 = blockIdx.x * tokens, rows = (unsigned)a.B * a.L;  // fewer than 2^31
+  const int slot = threadIdx.x % all, token = threadIdx.x / all % tokens, group = threadIdx.x / all / tokens;
+  const unsigned row = row0 + token;
+  const bool here = group < groups && row < rows;
+  const int b = here ? row / (unsigned)a.L : 0, i = here ? row - b * a.L : 0;
+  // Row i of batch b: where its first head is, for each of the four tensors.
+  const T* q = row_ptr<T>(a.q, a.lq, b, 0, i);
+  const T* k = row_ptr<T>(a.k, a.lk, b, 0, i);
+  T* q_out = row_ptr<T>(a.q_out, a.lqo, b, 0, i);
+  T* k_out = row_ptr<T>(a.k_out, a.lko, b, 0, i);
+  const int at0 = slot < slots ? slot * NV : a.rot + (slot - slots) * NV;  // this thread's elements
+  V x[kBatch], y[kBatch];
+  const int first = blockIdx.y * groups + group, step = gridDim.y * groups;
+  auto load = [&](int hb) {  // heads hb, hb + step, ...: their loads are in flight together
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int h = hb + n * step;
+      if (h >= H) continue;
+      const T* src = (h < a.Hq ? q + h * a.lq.sh : k + (h - a.Hq) * a.lk.sh) + at0;
+      x[n] = *reinterpret_cast<const V*>(src);
+      if (!ADJ && slot < slots) y[n] = *reinterpret_cast<const V*>(src + half);
+    }
+  };
+  if (here) load(first);
+  const int pair = threadIdx.x % half, stride = kThreads / half;  // a pair, and every stride-th token
+  if (threadIdx.x < stride * half) {
+    int axis = a.axes ? a.axes[pair] : 0;
     if ((unsigned)axis >= (unsigned)a.naxes) {
       report_error(a.err, kDevErrIndex, kKidRotary);
       axis = 0;
     }
-    const int64_t at = axis * a.pos_axis + b * a.pos_batch + i * a.pos_row;
-    const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.positions)[at] : static_cast<const int32_t*>(a.positions)[at];
-    const float f = a.inv_freq[p0 + e];
-    const uint64_t phase = turns_per_step(f) * (uint64_t)pos;
-    const float x = (float)(int32_t)(uint32_t)(phase >> 32) * 0x1p-31f;  // half turns in [-1, 1]
-    sincospif(x, &sn[e], &cs[e]);
-    if (!isfinite(f)) cs[e] = sn[e] = __int_as_float(0x7fffffff);
-    if (a.inverse) sn[e] = -sn[e];
+    const float f = a.inv_freq[pair];
+    const uint64_t step_phase = turns_per_step(f);
+    for (int tk = threadIdx.x / half; tk < tokens && row0 + tk < rows; tk += stride) {
+      const unsigned r = row0 + tk, rb = r / (unsigned)a.L;
+      const int64_t at = axis * a.pos_axis + rb * a.pos_batch + (r - rb * a.L) * a.pos_row;
+      const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.positions)[at] : static_cast<const int32_t*>(a.positions)[at];
+      float2 cs = cos_sin((uint32_t)((step_phase * (uint64_t)pos) >> 32));
+      if (!isfinite(f)) cs.x = cs.y = __int_as_float(0x7fffffff);
+      tables[tk * half + pair] = cs.x;
+      tables[(tokens + tk) * half + pair] = a.inverse ? -cs.y : cs.y;
+    }
   }
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const bool is_q = h < a.Hq;
-    const T* src = is_q ? row_ptr<T>(a.q, a.lq, b, h, i) : row_ptr<T>(a.k, a.lk, b, h - a.Hq, i);
-    T* dst = is_q ? row_ptr<T>(a.q_out, a.lqo, b, h, i) : row_ptr<T>(a.k_out, a.lko, b, h - a.Hq, i);
-    if (ADJ) {
-      V x = *reinterpret_cast<const V*>(src + 2 * p0);
+  __syncthreads();
+  if (!here) return;
+  float cs[VP], sn[VP];
 #pragma unroll
-      for (int e = 0; e < VP; ++e) {
-        const float u = Elem<T>::to_f(x.v[2 * e]), w = Elem<T>::to_f(x.v[2 * e + 1]);
-        x.v[2 * e] = Elem<T>::from_f(u * cs[e] - w * sn[e]);
-        x.v[2 * e + 1] = Elem<T>::from_f(w * cs[e] + u * sn[e]);
-      }
-      *reinterpret_cast<V*>(dst + 2 * p0) = x;
-    } else {
-      V x = *reinterpret_cast<const V*>(src + p0), y = *reinterpret_cast<const V*>(src + p0 + half);
+  for (int e = 0; e < VP; ++e) {
+    const int p = token * half + (slot < slots ? slot * VP : 0) + e;
+    cs[e] = tables[p];
+    sn[e] = tables[tokens * half + p];
+  }
+  for (int hb = first; hb < H; hb += kBatch * step) {
+    if (hb != first) load(hb);
 #pragma unroll
-      for (int e = 0; e < VP; ++e) {
-        const float u = Elem<T>::to_f(x.v[e]), w = Elem<T>::to_f(y.v[e]);
-        x.v[e] = Elem<T>::from_f(u * cs[e] - w * sn[e]);
-        y.v[e] = Elem<T>::from_f(w * cs[e] + u * sn[e]);
+    for (int n = 0; n < kBatch; ++n) {
+      const int h = hb + n * step;
+      if (h >= H) continue;
+      T* dst = (h < a.Hq ? q_out + h * a.lqo.sh : k_out + (h - a.Hq) * a.lko.sh) + at0;
+      if (slot >= slots) {  // elements past rot are copied
+        *reinterpret_cast<V*>(dst) = x[n];
+        continue;
       }
-      *reinterpret_cast<V*>(dst + p0) = x;
-      *reinterpret_cast<V*>(dst + p0 + half) = y;
+      turn_pairs<T, ADJ, VP>(x[n], y[n], cs, sn);
+      *reinterpret_cast<V*>(dst) = x[n];
+      if (!ADJ) *reinterpret_cast<V*>(dst + half) = y[n];
     }
   }
 }
@@ -108,15 +171,17 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int slot
 template <typename T, bool ADJ, int VP>
 cudaError_t rotary_t(const RotaryArgs& a, cudaStream_t s) {
   constexpr int NV = ADJ ? 2 * VP : VP;
-  const int slots = a.rot / 2 / VP, tail = (a.D - a.rot) / NV;
-  const int rows = kThreads / (slots + tail);
-  const int64_t blocks = ((int64_t)a.B * a.L + rows - 1) / rows;
-  const int H = a.Hq + a.Hkv;
-  // Heads are split over blocks until there are some 8 blocks an SM.
-  const int64_t want = 8 * (int64_t)(a.num_sms > 0 ? a.num_sms : 1);
-  const int splits = (int)min((int64_t)H, max((int64_t)1, (want + blocks - 1) / blocks));
-  const int heads = (H + splits - 1) / splits;
-  rotary_kernel<T, ADJ, VP><<<dim3((unsigned)blocks, (H + heads - 1) / heads), kThreads, 0, s>>>(a, slots, tail, rows, heads);
+  const int slots = a.rot / 2 / VP, tail = (a.D - a.rot) / NV, all = slots + tail, H = a.Hq + a.Hkv;
+  const int64_t rows = (int64_t)a.B * a.L, sms = a.num_sms > 0 ? a.num_sms : 1;
+  // As many tokens a block as share its threads' sines well, fewer while that leaves SMs idle;
+  // the threads that are left split the heads, and blocks split them too if there are still
+  // few.
+  int tokens = max(1, min(32, kThreads / all));
+  while (tokens > 1 && (rows + tokens - 1) / tokens < 3 * sms) tokens /= 2;
+  const int groups = max(1, min(H, kThreads / (all * tokens)));
+  const int64_t blocks = (rows + tokens - 1) / tokens;
+  const int splits = (int)max((int64_t)1, min((int64_t)((H + groups - 1) / groups), 2 * sms / blocks));
+  rotary_kernel<T, ADJ, VP><<<dim3((unsigned)blocks, splits), kThreads, tokens * a.rot * sizeof(float), s>>>(a, slots, tail, tokens, groups);
   return cudaGetLastError();
 }
 
