@@ -232,20 +232,21 @@ def _here(*tensors):
     return torch._C._cuda_getCurrentRawStream(d)
 
 
-def _rows_ok(name, t, dtype):
-    """A [B, H, L, D] CUDA tensor of dtype with contiguous rows."""
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be a 4-D [B, H, L, D] tensor")
-    if t.dtype is not dtype or not t.is_cuda or t.stride(3) != 1:
-        _check(name, t, dtype)
-
-
-def _dense(t):
-    """(batch, head, row) strides of a [B, H, L, D] tensor; those of size-1 dimensions, which
-    torch leaves undefined, are replaced by D."""
-    B, H, L, D = t.shape
-    b, h, r, _ = t.stride()
-    return (b if B > 1 else D, h if H > 1 else D, r if L > 1 else D)
+def _rows(name, t, dtype, want=None):
+    """Shape and (batch, head, row) strides of a [B, H, L, D] tensor of dtype with contiguous
+    rows (and of shape `want`).  Strides of size-1 dimensions, which torch leaves undefined, are
+    replaced by D."""
+    shape = t.shape
+    if len(shape) != 4 or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a 4-D [B, H, L, D] CUDA tensor of {dtype}, not "
+                         f"{tuple(shape)} of {t.dtype} on {t.device}")
+    if want is not None and shape != want:
+        raise ValueError(f"{name} must have shape {tuple(want)}, not {tuple(shape)}")
+    b, h, r, e = t.stride()
+    B, H, L, D = shape
+    if e != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride 1 along D)")
+    return shape, (b if B > 1 else D, h if H > 1 else D, r if L > 1 else D)
 
 
 def rotary_axes(sections, device="cuda"):
@@ -277,8 +278,8 @@ def _rotary(q, k, positions, inv_freq, axes, adjacent, inverse, q_out, k_out, st
     dtype = q.dtype
     if dtype not in DTYPE_CODE:
         raise ValueError(f"q has dtype {dtype}, expected fp32, fp16 or bf16")
-    _rows_ok("q", q, dtype)
-    B, Hq, L, D = q.shape
+    shape, qs = _rows("q", q, dtype)
+    B, Hq, L, D = shape
     naxes, at = _positions(positions, B, L)
     pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
     if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous() or not 2 <= 2 * pairs <= D:
@@ -290,32 +291,25 @@ def _rotary(q, k, positions, inv_freq, axes, adjacent, inverse, q_out, k_out, st
                          "pairs")
     if q_out is None:
         q_out = torch.empty_like(q)
-    else:
-        _rows_ok("q_out", q_out, dtype)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    Hkv, ks, kos = 0, (0, 0, 0), (0, 0, 0)
+    _, qos = _rows("q_out", q_out, dtype, shape)
+    Hkv, ks, kos, k_ptr, k_out_ptr = 0, (0, 0, 0), (0, 0, 0), None, None
     if k is not None:
-        _rows_ok("k", k, dtype)
-        Hkv = k.shape[1]
-        if k.shape[0] != B or k.shape[2] != L or k.shape[3] != D:
+        k_shape, ks = _rows("k", k, dtype)
+        Hkv = k_shape[1]
+        if k_shape[0] != B or k_shape[2] != L or k_shape[3] != D:
             raise ValueError("q and k disagree in batch, rows or head dim")
         if k_out is None:
             k_out = torch.empty_like(k)
-        else:
-            _rows_ok("k_out", k_out, dtype)
-            if k_out.shape != k.shape:
-                raise ValueError("k_out must have k's shape")
-        ks, kos = _dense(k), _dense(k_out)
+        _, kos = _rows("k_out", k_out, dtype, k_shape)
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out needs k")
     st = _lib.sdpa_rotary(
-        q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-        None if k is None else k_out.data_ptr(), positions.data_ptr(),
+        q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, positions.data_ptr(),
         64 if positions.dtype is torch.int64 else 32, _pack3(*at), inv_freq.data_ptr(),
         None if axes is None else axes.data_ptr(), naxes, B, Hq, Hkv, L, D, 2 * pairs,
         (_lib.ROTARY_ADJACENT if adjacent else 0) | (_lib.ROTARY_INVERSE if inverse else 0),
-        DTYPE_CODE[dtype], _pack12(*_dense(q), *ks, *_dense(q_out), *kos),
+        DTYPE_CODE[dtype], _pack12(*qs, *ks, *qos, *kos),
         _here(q, k, positions, inv_freq, axes, q_out, k_out))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_rotary")
@@ -376,13 +370,6 @@ def _cache(cache, pages, lens, B):
                        lens.data_ptr())
 
 
-def _cache_rows(name, t, cache, B, L):
-    """Checks a [B, Hkv, L, D] tensor of rows of the cache."""
-    _rows_ok(name, t, cache.dtype)
-    if t.shape != (B, cache.shape[1], L, cache.shape[3] // 10):
-        raise ValueError(f"{name} must be [{B}, Hkv, {L}, D] of the cache's heads and head dim")
-
-
 def cache_write(cache, k, v, pages, lens, counts=None, stream=None):
     """Quantises the rows of k and v [B,Hkv,L,D] into the cache, in place.
 
@@ -395,15 +382,16 @@ def cache_write(cache, k, v, pages, lens, counts=None, stream=None):
     if stream is not None and stream != torch.cuda.current_stream():
         with torch.cuda.stream(stream):
             return cache_write(cache, k, v, pages, lens, counts)
-    c = _cache(cache, pages, lens, k.shape[0])
-    _rows_ok("k", k, cache.dtype)
-    B, L = k.shape[0], k.shape[2]
-    _cache_rows("k", k, cache, B, L)
-    _cache_rows("v", v, cache, B, L)
+    shape, ks = _rows("k", k, cache.dtype)
+    _, vs = _rows("v", v, cache.dtype, shape)
+    B, H, L, D = shape
+    c = _cache(cache, pages, lens, B)
+    if H != cache.shape[1] or 10 * D != cache.shape[3]:
+        raise ValueError("k and v must be [B, Hkv, L, D] of the cache's heads and head dim")
     if counts is not None and (counts.dtype is not torch.int32 or counts.shape != (B,)
                                or not counts.is_contiguous()):
         raise ValueError(f"counts must be a contiguous int32 [{B}] tensor")
-    st = _lib.sdpa_cache_write(c, k.data_ptr(), v.data_ptr(), _pack6(*_dense(k), *_dense(v)),
+    st = _lib.sdpa_cache_write(c, k.data_ptr(), v.data_ptr(), _pack6(*ks, *vs),
                                None if counts is None else counts.data_ptr(), B, L,
                                _here(cache, k, v, pages, lens, counts))
     if st != _lib.OK:
@@ -416,18 +404,16 @@ def cache_read(cache, pages, lens, rows, k=None, v=None, stream=None):
     if stream is not None and stream != torch.cuda.current_stream():
         with torch.cuda.stream(stream):
             return cache_read(cache, pages, lens, rows, k, v)
-    B = lens.shape[0]
+    B = lens.numel()
     c = _cache(cache, pages, lens, B)
-    shape = (B, cache.shape[1], rows, cache.shape[3] // 10)
+    shape, dtype = (B, cache.shape[1], rows, cache.shape[3] // 10), cache.dtype
     if k is None:
-        k = cache.new_empty(shape)
-    else:
-        _cache_rows("k", k, cache, B, rows)
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
     if v is None:
-        v = cache.new_empty(shape)
-    else:
-        _cache_rows("v", v, cache, B, rows)
-    st = _lib.sdpa_cache_read(c, k.data_ptr(), v.data_ptr(), _pack6(*_dense(k), *_dense(v)), B, rows,
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+    _, ks = _rows("k", k, dtype, shape)
+    _, vs = _rows("v", v, dtype, shape)
+    st = _lib.sdpa_cache_read(c, k.data_ptr(), v.data_ptr(), _pack6(*ks, *vs), B, rows,
                               _here(cache, pages, lens, k, v))
     if st != _lib.OK:
         raise _lib.SdpaError(st, "sdpa_cache_read")
@@ -449,17 +435,15 @@ def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
         with torch.cuda.stream(stream):
             return cache_attention(q, cache, pages, lens, scale, is_causal, need_lse, out, lse,
                                    sinks, max_len, workspace)
-    _rows_ok("q", q, cache.dtype)
-    B, Hq, L, D = q.shape
+    dtype = cache.dtype
+    shape, qs = _rows("q", q, dtype)
+    B, Hq, L, D = shape
     c = _cache(cache, pages, lens, B)
     if 10 * D != cache.shape[3]:
         raise ValueError("q must be [B, Hq, L, D] of the cache's head dim")
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _rows_ok("out", out, q.dtype)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
+    _, os = _rows("out", out, dtype, shape)
     if not need_lse:
         lse = None
     elif lse is None:
@@ -474,7 +458,7 @@ def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
     st = _lib.sdpa_cache_attn(
         c, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if sinks is None else sinks.data_ptr(), _pack6(*_dense(q), *_dense(out)), B, Hq, L,
+        None if sinks is None else sinks.data_ptr(), _pack6(*qs, *os), B, Hq, L,
         1.0 / math.sqrt(D) if scale is None else float(scale), _causal(is_causal), max_len,
         None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
