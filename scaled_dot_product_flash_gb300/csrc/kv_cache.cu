@@ -34,70 +34,87 @@ __device__ __forceinline__ void unpack8(float (&x)[8], const uint4& w) {
   }
 }
 
+// Minimum and maximum that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Quotients rounded correctly from a reciprocal rounded correctly, one residual step (Markstein
+// 1990): a few instructions instead of a division's, for values whose residual does not underflow.
+__device__ __forceinline__ float quotient(float a, float d, float inv) {
+  const float q = __fmul_rn(a, inv);
+  return fmaf(fmaf(-q, d, a), inv, q);
+}
+
 // Codes, scale and zero of a group of 32 elements held by the 4 lanes of a quad, 8 each.
 // Returns this lane's 8 codes (nibble n = x[n]) and the parameter word (s | z << 16).
 template <typename T>
 __device__ __forceinline__ uint32_t quantise(const uint4& in, uint32_t& param) {
   constexpr float kInf = __builtin_huge_valf();
+  // Scales from here on are normal numbers of T, so that no quotient exceeds 15.5, and far from
+  // fp32's smallest.  Others take the form below that divides and clamps.
+  constexpr float kPlain = std::is_same<T, __half>::value ? 0x1p-14f : 0x1p-100f;
   float x[8];
   unpack8<T>(x, in);
   float lo = x[0], hi = x[0];
-  bool fine = fabsf(x[0]) < kInf;
 #pragma unroll
   for (int e = 1; e < 8; ++e) {
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-    fine = fine && fabsf(x[e]) < kInf;
+    lo = min_nan(lo, x[e]);
+    hi = max_nan(hi, x[e]);
   }
-  if (!fine) hi = kInf;
 #pragma unroll
   for (int off = 1; off <= 2; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
   const float range = __fsub_rn(hi, lo);
-  if (!(range < kInf)) {
+  if (!(range < kInf)) {  // an element that is not finite, or too wide a range
     param = f_to_bits<T>(__int_as_float(0x7fffffff)) << 16;
     return 0;
   }
-  const uint32_t sb = f_to_bits<T>(__fdiv_rn(range, 15.f));
+  const uint32_t sb = f_to_bits<T>(range > 0x1p-100f ? quotient(range, 15.f, 1.f / 15.f) : __fdiv_rn(range, 15.f));
   param = sb | (f_to_bits<T>(lo) << 16);
   const float s = bits_to_f<T>(sb);
-  // The quotient rounded correctly from the reciprocal rounded correctly, one residual step
-  // (Markstein 1990), so that ties fall as the definition has them.  Scales near the end of
-  // fp32's range, where that would underflow, divide.
   float c[8];
-  if (s > 0x1p-100f) {
+  if (s >= kPlain) {
     const float inv = __frcp_rn(s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float d = __fsub_rn(x[e], lo), q = __fmul_rn(d, inv);
-      c[e] = fmaf(fmaf(-q, s, d), inv, q);
-    }
+    for (int e = 0; e < 8; ++e) c[e] = quotient(__fsub_rn(x[e], lo), s, inv);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = s > 0.f ? __fdiv_rn(__fsub_rn(x[e], lo), s) : 0.f;
+    for (int e = 0; e < 8; ++e) c[e] = s > 0.f ? fminf(__fdiv_rn(__fsub_rn(x[e], lo), s), 15.f) : 0.f;
   }
-  constexpr float kRound = 12582912.f;  // 1.5·2^23: adding it rounds to an integer, ties to even
+  // Adding 1.5·2^23 rounds to an integer, ties to even, in the low mantissa bits; the bits above
+  // them are the same eight times over and leave with one constant, modulo 2^32.
+  constexpr uint32_t kMagic = 0x4b400000u;
+  uint32_t word = 0u - kMagic * 0x11111111u;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = __fsub_rn(__fadd_rn(fminf(c[e], 15.f), kRound), kRound);
-  // Four codes a half-word, exact in fp32; 2^23 puts that integer in the low mantissa bits.
-  float w[2];
-#pragma unroll
-  for (int n = 0; n < 2; ++n) w[n] = fmaf(c[4 * n + 3], 4096.f, fmaf(c[4 * n + 2], 256.f, fmaf(c[4 * n + 1], 16.f, c[4 * n]))) + 8388608.f;
-  return __byte_perm(__float_as_uint(w[0]), __float_as_uint(w[1]), 0x5410);
+  for (int e = 0; e < 8; ++e) word += __float_as_uint(__fadd_rn(c[e], 12582912.f)) * (1u << (4 * e));
+  return word;
 }
 
-// The 8 values that a word of codes stands for.
+// The 8 values that a word of codes stands for.  A nibble under the exponent of 1024 is
+// 1024 + code in fp16 (1024 + 16·code, one nibble higher), two of them a word.
 template <typename T>
 __device__ __forceinline__ uint4 values8(uint32_t code, uint32_t param) {
-  const float s = bits_to_f<T>(param & 0xffffu), z = bits_to_f<T>(param >> 16);
-  uint32_t w[4];
+  const float s = bits_to_f<T>(param & 0xffffu), z = bits_to_f<T>(param >> 16), s16 = s * 0.0625f;
+  float x[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    w[e] = pack2<T>(fmaf(s, (float)((code >> (8 * e)) & 15u), z), fmaf(s, (float)((code >> (8 * e + 4)) & 15u), z));
+  for (int n = 0; n < 4; ++n) {  // nibbles n and n + 4
+    const uint32_t w = n < 2 ? code : code >> 8;
+    const uint32_t bits = n % 2 ? (w & 0x00f000f0u) | 0x64006400u : (w & 0x000f000fu) | 0x64006400u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&bits), __half2half2(__float2half_rn(1024.f)));
+    x[n] = fmaf(n % 2 ? s16 : s, __low2float(h), z);
+    x[n + 4] = fmaf(n % 2 ? s16 : s, __high2float(h), z);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
 }
 
 template <int W>
@@ -131,20 +148,18 @@ struct Place {
   int v, hf;            // 0: keys, 1: values; half of the tile's rows
   bool any;             // whether the warp has work
 };
+// The grid is (tiles, heads, sequences).
 __device__ __forceinline__ Place place_of(const CacheArgs& c, unsigned kid) {
-  const int tiles = tiles_of(c.L);
-  int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  const int w = blockIdx.x * kWarps + threadIdx.x / 32;
   Place p;
-  p.any = w < (int64_t)c.B * c.Hkv * tiles * 4;
+  p.b = blockIdx.z;
+  p.h = blockIdx.y;
+  p.v = w & 1;
+  p.hf = w >> 1 & 1;
+  p.any = w >> 2 < tiles_of(c.L);
   if (!p.any) return p;
-  p.v = (int)(w & 1);
-  p.hf = (int)(w >> 1 & 1);
-  w >>= 2;
-  const int tile = (int)(w % tiles);
-  p.h = (int)(w / tiles % c.Hkv);
-  p.b = (int)(w / tiles / c.Hkv);
   p.len = cache_len(c, p.b, c.pages_per_seq * c.page_size, kid);
-  p.pos0 = (((p.len - c.L) >> 4) + tile) * kTile;  // >> rounds down
+  p.pos0 = (((p.len - c.L) >> 4) + (w >> 2)) * kTile;  // >> rounds down
   p.any = p.pos0 < p.len;
   return p;
 }
@@ -232,7 +247,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(CacheArgs c) {
 
 template <typename T, int D>
 cudaError_t launch_t(const CacheArgs& c, bool write, cudaStream_t s) {
-  const unsigned blocks = (unsigned)(((int64_t)c.B * c.Hkv * tiles_of(c.L) * 4 + kWarps - 1) / kWarps);
+  const dim3 blocks((unsigned)((tiles_of(c.L) * 4u + kWarps - 1) / kWarps), c.Hkv, c.B);
   if (write) cache_write_kernel<T, D><<<blocks, kWarps * 32, 0, s>>>(c);
   else cache_read_kernel<T, D><<<blocks, kWarps * 32, 0, s>>>(c);
   return cudaGetLastError();
