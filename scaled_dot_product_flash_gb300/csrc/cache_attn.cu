@@ -35,23 +35,17 @@ namespace {
 // lane holds.  CW = 2 is the plain form.  CW = 1 is the form for up to 4 rows, which would leave
 // half of the 8 columns empty: row r is column 2r and the odd columns are zero, so that every
 // lane has one row and half the elements of the softmax and of the scalings.
-#ifndef NW
-#define NW 4
-#define NS 2
-#define NB 3
-#endif
-constexpr int kNarrowWarps = NW, kNarrowStages = NS, kNarrowBlocks = NB;
 template <int D, int NT, int CW>
 struct Cfg {
   using Tl = Tile<D>;
-  #ifndef UTN
-#define UTN 2
-#endif
-  static constexpr int UT = CW == 1 && D == 128 ? UTN : D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
+    static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
   static constexpr int kUnit = UT * kTile;                   // tokens a unit
-  static constexpr int kWarps = CW == 1 ? kNarrowWarps : 8;
-  static constexpr int kStages = CW == 1 ? kNarrowStages : 2;
-  static constexpr int kBlocks = CW == 1 ? kNarrowBlocks : NT == 1 && D <= 128 ? 2 : 1;  // blocks an SM
+  // Warps a block, and blocks an SM.  The narrow form ran best on 12 warps of up to 168 registers
+  // an SM (131072 tokens, D = 128: 37.4 us; 8 warps of 222 registers 36.2, but 49.4 with chunks
+  // that keep fewer blocks busy; 16 warps of 128 registers, which spill, 41.0; 20 of 96, 54.1).
+  static constexpr int kWarps = CW == 1 ? 4 : 8;
+  static constexpr int kBlocks = CW == 1 ? 3 : NT == 1 && D <= 128 ? 2 : 1;
+  static constexpr int kStages = 2;  // a third one changed nothing (37.5 us)
   static constexpr int kUnitBytes = UT * Tl::kBytes;
   static constexpr int kSlab = 4 * CW;       // rows of a row tile
   static constexpr int kRows = kSlab * NT;
@@ -147,21 +141,27 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   __shared__ int abort_flag;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int split = blockIdx.x, rt = blockIdx.y % row_tiles, h = blockIdx.y / row_tiles, b = blockIdx.z;
+  const int split = blockIdx.x, b = blockIdx.z, h = row_tiles == 1 ? blockIdx.y : blockIdx.y / row_tiles, rt = blockIdx.y - h * row_tiles;
   // This warp's query rows, on their way while the length and the pages are looked up.
   const int R = a.G * c.L, row0 = rt * C::kRows;
   constexpr int kMine = (C::kRows + kWarps - 1) / kWarps;
   T q_in[kMine][NG];
 #pragma unroll
   for (int n = 0; n < kMine; ++n) {
-    const int rr = warp + n * kWarps, r = row0 + rr;
-    const T* q = rr < C::kRows && r < R ? row_ptr<T>(a.q, a.lq, b, h * a.G + r / c.L, r % c.L) + lane : nullptr;
+    const int rr = warp + n * kWarps, r = row0 + rr, head = c.L == 1 ? r : r / c.L;
+    const T* q = rr < C::kRows && r < R ? row_ptr<T>(a.q, a.lq, b, h * a.G + head, r - head * c.L) + lane : nullptr;
 #pragma unroll
     for (int j = 0; j < NG; ++j) q_in[n][j] = q ? q[32 * j] : Elem<T>::from_f(0.f);
   }
+  // Lane st·UT + i looks at tile i of this warp's unit for stage st; the entry is read beside the
+  // length, which says whether it counts.
+  const int* table = c.pages + b * c.pages_stride;
+  const int64_t first = (int64_t)split * chunk;
+  int pos = (int)first + (warp + lane / UT * kWarps) * C::kUnit + lane % UT * kTile;
+  int slot = (unsigned)pos / (unsigned)c.page_size, off = pos - slot * c.page_size;
+  const int entry = lane < C::kStages * UT && slot < c.pages_per_seq ? table[slot] : -1;
   const int len = cache_len(c, b, a.max_len, kKidCacheAttn);
   const int end_all = tile_end(a, len, rt, C::kRows);
-  const int64_t first = (int64_t)split * chunk;
   if (first >= end_all && splits > 1) {
     asm volatile("griddepcontrol.launch_dependents;");
     return;
@@ -178,23 +178,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   __syncwarp();
   const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidCacheAttn};
   uint8_t* ring = smem + warp * (C::kStages * C::kUnitBytes);
-  const int* table = c.pages + b * c.pages_stride;
   const int64_t page_bytes = (int64_t)c.Hkv * (c.page_size / kTile) * Tl::kBytes;
   const uint8_t* head = c.data + (int64_t)h * (c.page_size / kTile) * Tl::kBytes;
-  // Page of a tile at position pos (entry `slot` of the table), or -1: past the end, or bad.
-  auto page_at = [&](int pos, int slot) {
+  // The page of a tile at position pos: -1 if the tile is past the end, or the page bad.
+  auto checked = [&](int page, int pos) {
     if (pos >= end) return -1;
-    const int page = table[slot];
     if ((unsigned)page < (unsigned)c.num_pages) return page;
     report_error(c.err, kDevErrIndex, kKidCacheAttn);
     return -1;
   };
-  // Lane st·UT + i starts with tile i of this warp's unit for stage st.  Later lane i copies tile
-  // i of every unit: it keeps that tile's position, its place in the table and its offset in
-  // the page, which move on by a fixed step, and has its page looked up one unit ahead.
-  int pos = start + (warp + lane / UT * kWarps) * C::kUnit + lane % UT * kTile;
-  int slot = pos / c.page_size, off = pos % c.page_size;
-  int page = lane < C::kStages * UT ? page_at(pos, slot) : -1;
+  // The lanes that looked a page up start with its tile.  Later lane i copies tile i of every unit:
+  // it keeps that tile's position, its place in the table and its offset in the page, which move
+  // on by a fixed step, and has its page looked up one unit ahead.
+  int page = lane < C::kStages * UT ? checked(entry, pos) : -1;
   uint32_t there = __ballot_sync(0xffffffffu, page >= 0);  // bit st·UT + i: tile i of stage st is copied
   if (lane < C::kStages && warp + lane * kWarps < units)
     tc::mbar_arrive_expect_tx(&full[warp][lane], __popc((there >> (lane * UT)) & ((1u << UT) - 1)) * Tl::kBytes);
@@ -212,7 +208,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   };
 #pragma unroll
   for (int n = 0; n < C::kStages; ++n) advance();
-  page = lane < UT ? page_at(pos, slot) : -1;
+  page = lane < UT && pos < end ? checked(table[slot], pos) : -1;
   // Starts the copies of this warp's next unit into stage s (all lanes call it).
   auto issue = [&](int s) {
     const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
@@ -222,7 +218,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     if (page >= 0)
       bulk_copy(ring + s * C::kUnitBytes + lane * Tl::kBytes, head + page * page_bytes + off / kTile * Tl::kBytes, Tl::kBytes, &full[warp][s]);
     advance();
-    page = lane < UT ? page_at(pos, slot) : -1;
+    page = lane < UT && pos < end ? checked(table[slot], pos) : -1;
   };
   int issued = warp + C::kStages * kWarps;  // next unit to start
 
@@ -704,21 +700,12 @@ Plan make_plan(const CacheAttnArgs& a) {
   p.rows = 4 * p.cw * p.nt;
   p.row_tiles = (R + p.rows - 1) / p.rows;
   const int step = 256;  // tokens: at least a unit a warp
-  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.cw == 1 ? kNarrowBlocks : p.nt == 1 && a.c.D <= 128 ? 2 : 1);
+  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.cw == 1 ? 3 : p.nt == 1 && a.c.D <= 128 ? 2 : 1);
   const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * p.row_tiles;
-#ifndef CW_
-#define CW_ 1
-#endif
-#ifndef CM_
-#define CM_ 1536
-#endif
-#ifndef CN_
-#define CN_ 512
-#endif
-  const int64_t want = max((int64_t)1, CW_ * slots / pairs);
+  const int64_t want = max((int64_t)1, slots / pairs);
   int64_t chunk = (a.max_len + want - 1) / want;
-  if (pairs * 4 > slots) chunk = min(chunk, (int64_t)CM_);
-  chunk = max(chunk, (int64_t)CN_);
+  if (pairs * 4 > slots) chunk = min(chunk, (int64_t)1536);
+  chunk = max(chunk, (int64_t)512);
   p.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
   p.splits = (a.max_len + p.chunk - 1) / p.chunk;
   return p;
@@ -757,9 +744,6 @@ cudaError_t join_t(const CacheAttnArgs& a, const Plan& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D, kThreads>, a, p.chunk, p.splits, p.rows);
 }
 
-#ifndef JTS
-#define JTS 128
-#endif
 template <typename T, int D>
 cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
   const Plan p = make_plan(a);
@@ -772,7 +756,7 @@ cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
   }
   // A row of few chunks is joined by two warps; with many, 16 warps read them side by side
   // (131072 tokens in 57 chunks: 36.6 us a call with 4 warps, 34.1 with 16; 6 chunks: 41.9, 46.2).
-  return p.splits > 16 ? join_t<T, D, 512>(a, p, s) : join_t<T, D, JTS>(a, p, s);
+  return p.splits > 16 ? join_t<T, D, 512>(a, p, s) : join_t<T, D, 128>(a, p, s);
 }
 
 template <typename T>
