@@ -357,7 +357,7 @@ int sdpa_cache_read(const sdpa_cache_t* cache, void* k, void* v, const sdpa_layo
 /*
  * Attention of q [B,Hq,Lq,D] over the cached keys and values, as sdpa_fwd_sinks defines it
  * (scale, sinks, lse, grouped heads), for any Lq >= 1; meant for few rows a KV head
- * (Hq/Hkv·Lq): each 32 of them (16 at D = 256) read the cache once.  layouts[0] and [1] are
+ * (Hq/Hkv·Lq): each 16 of them read the cache once.  layouts[0] and [1] are
  * those of q and out.  is_causal: SDPA_CAUSAL_NONE (every query sees all lens[b] tokens) or
  * SDPA_CAUSAL_BOTTOM_RIGHT (query i sees positions up to lens[b] − Lq + i, its own);
  * SDPA_CAUSAL_TOP_LEFT is SDPA_ERR_UNSUPPORTED.  A row that sees nothing gets out = 0 and
