@@ -49,6 +49,9 @@
  *    return SDPA_ERR_INVALID_ARG or SDPA_ERR_UNSUPPORTED; a failed launch returns
  *    SDPA_ERR_CUDA.  Kernels never trap: a wait that runs out of its iteration limit sets
  *    the device error word and the kernel returns; sdpa_poll_status reports it.
+ *  - Beside the attention the library has the rotary embedding of q and k (sdpa_rotary) and a
+ *    paged cache of keys and values in 4 bits (sdpa_cache_*), each with its own rules below;
+ *    what those read from device memory (pages, lengths, axes) is checked by the kernels.
  *  - Supported: dtype in {SDPA_F32, SDPA_F16, SDPA_BF16}; D in {32, 64, 96, 128, 256}
  *    (fp16/bf16 run on tensor cores at every D, fp32 on the CUDA-core tiled kernels);
  *    B, Hq, Hkv, Lq, Lkv >= 1; Hq % Hkv == 0; Hq, B <= 65535; scale finite (0 allowed).
@@ -284,7 +287,7 @@ int sdpa_bwd_noalloc(const void* q, const void* k, const void* v, const void* ou
  *   (axis, batch, row) in position_strides; a stride of 0 broadcasts.  inv_freq [rot/2] fp32,
  *   axes [rot/2] int32 or NULL (axis 0 for all).  Each may overlap inputs, not outputs.
  *   1 <= naxes, rot even, 2 <= rot <= D.
- * Angles are exact to 2^-32 turns plus |position·inv_freq|·2^-64 turns: they are computed
+ * Angles are exact to 2^-32 turns plus |position|·(1 + |inv_freq|)·2^-64 turns: they are computed
  * modulo one turn in integers, however far the position.  Rotations run in fp32 and are
  * rounded once.  An axis outside 0..naxes-1 is read as axis 0 and reported by
  * sdpa_poll_status (SDPA_ERR_DEVICE_INDEX).  A frequency that is not finite gives NaN.

@@ -4,9 +4,12 @@ The computation lives in ``libsdpa.so`` (hand-written CUDA for sm_103a behind a 
 declared in ``include/sdpa.h``).  This package is its thin Python binding:
 
 * ``_lib``: ctypes entry points under the C names (``sdpa_fwd``, ``sdpa_bwd``, ...).
-* ``api``: tensor-level calls that allocate outputs with PyTorch and pass raw pointers.
-* ``autograd``: ``SDPAFunction`` (torch autograd over the forward and fused backward) and a
-  ``scaled_dot_product_attention`` drop-in for the cases the kernels cover.
+* ``api``: tensor-level calls that allocate outputs with PyTorch and pass raw pointers:
+  attention forward and backward, rotary positions, and a 4-bit paged cache of keys and
+  values (write, read back, attention over it).
+* ``autograd``: ``SDPAFunction`` (torch autograd over the forward and fused backward), a
+  ``scaled_dot_product_attention`` drop-in for the cases the kernels cover, and
+  ``rotary_embedding``.
 * ``inputs``: seeded synthetic inputs.
 * ``build``: nvcc build of the library.
 """

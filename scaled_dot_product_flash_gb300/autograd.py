@@ -15,6 +15,9 @@ D in {32, 64, 96, 128, 256}, optional top-left causal mask or ``attn_mask`` (boo
 the key; floating: added to the scores; no gradient flows into it), any finite scale,
 optional per-head attention-sink logits (``sinks``, differentiable).  Dropout and other
 head layouts raise ``NotImplementedError``.
+
+``rotary_embedding`` turns queries and keys by their positions before the attention; its
+gradient is the same kernel with the angles negated.
 """
 from __future__ import annotations
 
