@@ -321,8 +321,9 @@ int sdpa_rotary(const void* q, const void* k, void* q_out, void* k_out, const vo
  *    after the call's own, row i of L is position lens[b] − L + i.  Rows of negative position
  *    are padding, on the left.
  *  - dtype is SDPA_F16 or SDPA_BF16 (others: SDPA_ERR_UNSUPPORTED), D one of the supported
- *    head dims, page_size a multiple of 16, at most 2^16, pages_per_seq·page_size at most
- *    2^30; every call on a cache uses one dtype.  data is 16-byte aligned; pages and lens are 4-byte aligned.
+ *    head dims, page_size a multiple of 16, at most 2^16, pages_per_seq·page_size and
+ *    B·Hkv·L at most 2^30; every call on a cache uses one dtype.  data is 16-byte aligned;
+ *    pages and lens are 4-byte aligned.
  *  - A page outside 0..num_pages−1, where a position needs it, or a length below 0 or above
  *    pages_per_seq·page_size is reported by sdpa_poll_status (SDPA_ERR_DEVICE_INDEX) and never
  *    read or written through: such tokens are not written, read as 0 and are hidden from

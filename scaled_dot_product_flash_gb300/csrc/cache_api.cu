@@ -29,7 +29,7 @@ int check_cache(const sdpa_cache_t* cache, int B, int L, CacheArgs* c) {
   if (cache->dtype != SDPA_F16 && cache->dtype != SDPA_BF16) return SDPA_ERR_UNSUPPORTED;
   if (!head_dim_ok(cache->D) || cache->page_size > 65536 || B > 65535 || cache->Hkv > 65535) return SDPA_ERR_UNSUPPORTED;
   // Positions (and a little past them) are 32-bit, offsets in bytes 64-bit.
-  if ((double)cache->pages_per_seq * cache->page_size > 1073741824.0 || (double)B * cache->Hkv * L > 2147483647.0) return SDPA_ERR_UNSUPPORTED;
+  if ((double)cache->pages_per_seq * cache->page_size > 1073741824.0 || (double)B * cache->Hkv * L > 1073741824.0) return SDPA_ERR_UNSUPPORTED;
   if (cache->pages_stride > ((int64_t)1 << 40)) return SDPA_ERR_INVALID_ARG;
   std::memset(c, 0, sizeof(*c));
   c->data = static_cast<uint8_t*>(cache->data);

@@ -48,8 +48,8 @@ namespace {
 template <int D, int NT, int CW>
 struct Cfg {
   using Tl = Tile<D>;
-    static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
-  static constexpr int kUnit = UT * kTile;                   // tokens a unit
+  static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
+  static constexpr int kUnit = UT * kTile;                    // tokens a unit
   // Warps a block, and blocks an SM.  The narrow form ran best on 12 warps of up to 168 registers
   // an SM (131072 tokens, D = 128: 37.4 us; 8 warps of 222 registers 36.2, but 49.4 with chunks
   // that keep fewer blocks busy; 16 warps of 128 registers, which spill, 41.0; 20 of 96, 54.1).
@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
     for (int j = 0; j < NG; ++j) top = fmaxf(top, fabsf(x[j]));
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    // A row of zeros (or subnormals) takes 2^100; one with an infinity 2^-100, and turns NaN by itself.
-    const int e = max(-100, min(100, 13 - ((__float_as_int(top) >> 23) - 127)));
+    // A row of zeros (or subnormals) takes 2^126; one with an infinity 2^-115, and turns NaN by itself.
+    const int e = min(126, 13 - ((__float_as_int(top) >> 23) - 127));
     const float up = a.scale_log2 == 0.f ? 0.f : copysignf(pow2(e), a.scale_log2);
     const int nt = CW == 2 ? rr / 8 : 0, g_row = CW == 2 ? rr % 8 : 2 * rr;
 #pragma unroll
@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
     for (int n = 0; n < CW; ++n) {  // the accumulators' columns are 2t and 2t + 1
       const int rr = C::kSlab * nt + CW * t + n;
-      f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(24 - q_exp[rr]), 1e-37f);
+      const int e = 24 - q_exp[rr], e0 = e / 2;  // -102..139: in two steps
+      f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(e0) * pow2(e - e0), 1e-37f);
       lim[nt][n] = a.causal ? len - c.L + (row0 + rr) % c.L + 1 : len;
     }
   }
@@ -590,17 +591,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][C::kSlab * nt + CW * t + n][0]);
       wgt[n] = m[nt][n] == minus_inf() ? 0.f : ex2(m[nt][n] - M);
     }
-    const float back = pow2(12 - k);  // o·2^(24 - k), in two steps; an odd nibble's also by 1/16
+    // o·2^(24 - k), in two steps since k goes down to -122; an odd nibble's also by 1/16.
+    const int half_back = (24 - k) / 2;
+    const float back0 = pow2(half_back), back1 = pow2(24 - k - half_back), odd1 = back1 * 0.0625f;
 #pragma unroll
     for (int j = 0; j < NG; ++j)
 #pragma unroll
       for (int n = 0; n < CW; ++n) {
         const float z = zo[nt][j][n];
         float4 v;
-        v.x = (o[2 * j][nt][n] * 4096.f * back + z) * wgt[n];
-        v.y = (o[2 * j][nt][2 + n] * 256.f * back + z) * wgt[n];
-        v.z = (o[2 * j + 1][nt][n] * 4096.f * back + z) * wgt[n];
-        v.w = (o[2 * j + 1][nt][2 + n] * 256.f * back + z) * wgt[n];
+        v.x = (o[2 * j][nt][n] * back0 * back1 + z) * wgt[n];
+        v.y = (o[2 * j][nt][2 + n] * back0 * odd1 + z) * wgt[n];
+        v.z = (o[2 * j + 1][nt][n] * back0 * back1 + z) * wgt[n];
+        v.w = (o[2 * j + 1][nt][2 + n] * back0 * odd1 + z) * wgt[n];
         *reinterpret_cast<float4*>(red + (warp * C::kSlab + CW * t + n) * (D + 4) + 32 * j + 4 * g) = v;
       }
     __syncthreads();

@@ -161,7 +161,7 @@ def test_scales(dtype, scale):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype,sizes", [("bf16", (1e-20, 1e20)), ("bf16", (1e-3, 1e3)), ("f16", (1e-4, 500.0))])
+@pytest.mark.parametrize("dtype,sizes", [("bf16", (1e-20, 1e20)), ("bf16", (1e-3, 1e3)), ("bf16", (1e36, 3e-33)), ("f16", (1e-4, 500.0))])
 def test_values_of_any_size(dtype, sizes):
     """Queries and values far from 1, and values whose scale changes by token and by group (the
     keys stay plain, scaled against the queries' size)."""
@@ -426,3 +426,54 @@ def test_a_training_step():
     assert np.abs(as_f64(out.detach()) - o).max() <= 1e-5
     for x, want in zip(leaves, (dq, dk, dv)):
         assert np.abs(as_f64(x.grad) - want).max() <= 1e-4
+
+
+@pytest.mark.gpu
+def test_many_short_sequences():
+    """More sequences than blocks in a wave, some empty, three rows a KV head."""
+    rng = np.random.default_rng(32)
+    lens = [int(x) for x in rng.integers(0, 40, 500)]
+    cache, table, ks, vs, low = fill(rng, lens, 1, 32, 16, "bf16")
+    q = draw_rows(rng, (500, 3, 1, 32), "bf16")
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True)
+    api.poll_status()
+    check(out, lse, q, ks, vs, low, 1 / math.sqrt(32), True, None, "bf16")
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls of different shapes on two streams, each with its own memory, as each gives alone."""
+    rng = np.random.default_rng(33)
+    jobs = []
+    for D, lens, H, L in ((128, [4000, 100], 2, 1), (64, [900], 1, 5)):
+        cache, table, *_ = fill(rng, lens, H, D, 32, "f16")
+        q = draw_rows(rng, (len(lens), 4 * H, L, D), "f16").cuda()
+        args = (q, cache, table.cuda(), ints(lens).cuda())
+        jobs.append((args, api.cache_attention(*args)[0], api.cache_read(*args[1:], 50), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        for args, _, _, stream in jobs:
+            got.append((api.cache_attention(*args, stream=stream)[0], api.cache_read(*args[1:], 50, stream=stream)))
+    torch.cuda.synchronize()
+    api.poll_status()
+    for n, (out, (k, v)) in enumerate(got):
+        _, want, (wk, wv), _ = jobs[n % 2]
+        assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv)
+
+
+@pytest.mark.gpu
+def test_a_growing_sequence_keeps_its_tokens():
+    """Tokens written one call at a time, across tile and page ends, against one call for all."""
+    rng = np.random.default_rng(34)
+    B, H, D, page, n = 2, 2, 96, 16, 37
+    table = ints([[3, 0, 5], [1, 4, 2]]).cuda()
+    k, v = (draw_rows(rng, (B, H, n, D), "f16").cuda() for _ in range(2))
+    once, grown = dirty_cache(6, H, page, D, "f16"), dirty_cache(6, H, page, D, "f16")
+    api.cache_write(once, k, v, table, ints([n, n]).cuda())
+    at = 0
+    for rows in (1, 1, 14, 2, 15, 3, 1):
+        api.cache_write(grown, k[:, :, at:at + rows], v[:, :, at:at + rows], table, ints([at + rows] * B).cuda())
+        at += rows
+    api.poll_status()
+    assert at == n and torch.equal(once.view(torch.uint8), grown.view(torch.uint8))
