@@ -11,10 +11,10 @@
 // compute their sines and cosines once, into shared memory, while the first heads' loads are
 // on their way; then a thread keeps those of VP pairs of one token in registers and turns that
 // token's heads hg, hg + HG, ... in 16-byte pieces.
-// Measured (bf16, B = 2, 32 + 8 heads, L = 4096, D = 128; 168 MB): 31.6 us a call from a graph,
-// 5.3 TB/s, 0.78 of the copy rate; waiting on loads (long scoreboard 10 of 16 cycles a warp and
+// Measured (bf16, B = 2, 32 + 8 heads, L = 4096, D = 128; 168 MB): 31.0 us a call from a graph,
+// 5.4 TB/s, 0.80 of the copy rate; waiting on loads (long scoreboard 8.8 of 14 cycles a warp and
 // instruction).  With the sines computed by every thread for 8 heads (64-bit divisions, CUDA's
-// sincospif) it took 35 to 50 us; fp32 (B = 8, 8 + 8 heads, L = 577, D = 64) 8.4 us, 4.5 TB/s.
+// sincospif) it took 35 to 50 us; fp32 (B = 8, 8 + 8 heads, L = 577, D = 64) 7.5 us, 5.0 TB/s.
 #include "cache.h"
 
 namespace sdpa {
@@ -98,9 +98,10 @@ __device__ __forceinline__ void turn_pairs(Vec<T, ADJ ? 2 * VP : VP>& x, Vec<T, 
 template <typename T, bool ADJ, int VP>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int slots, int tail, int tokens, int groups) {
   constexpr int NV = ADJ ? 2 * VP : VP;  // elements a vector
-  // Heads whose loads a thread has in flight: 16-bit types 2 (64.2 us for two calls, 4: 69.5),
-  // fp32 4 (16.5 us, 2: 19.1).
-  constexpr int kBatch = sizeof(T) == 4 ? 4 : 2;
+  // Heads of a batch; the next batch is loaded while one is turned.  16-bit types 1 (62.0 us for
+  // two calls; 2, which needs 80 registers, 73.7; without the batch ahead 2 took 63.2), fp32 2
+  // (15.0 us; 1: 15.7; 4 without the batch ahead 16.8).
+  constexpr int kBatch = sizeof(T) == 4 ? 2 : 1;
   using V = Vec<T, NV>;
   extern __shared__ __align__(16) float tables[];  // cosines, then sines: [tokens][rot / 2]
   const int half = a.rot / 2, all = slots + tail, H = a.Hq + a.Hkv;
@@ -115,9 +116,9 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int s
   T* q_out = row_ptr<T>(a.q_out, a.lqo, b, 0, i);
   T* k_out = row_ptr<T>(a.k_out, a.lko, b, 0, i);
   const int at0 = slot < slots ? slot * NV : a.rot + (slot - slots) * NV;  // this thread's elements
-  V x[kBatch], y[kBatch];
-  const int first = blockIdx.y * groups + group, step = gridDim.y * groups;
-  auto load = [&](int hb) {  // heads hb, hb + step, ...: their loads are in flight together
+  const int step = gridDim.y * groups;
+  V x[2][kBatch], y[2][kBatch];
+  auto load = [&](int hb, V (&x)[kBatch], V (&y)[kBatch]) {  // heads hb, hb + step, ...: their loads are in flight together
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
       const int h = hb + n * step;
@@ -127,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int s
       if (!ADJ && slot < slots) y[n] = *reinterpret_cast<const V*>(src + half);
     }
   };
-  if (here) load(first);
+  const int first = blockIdx.y * groups + group;
+  if (here) load(first, x[0], y[0]);
   const int pair = threadIdx.x % half, stride = kThreads / half;  // a pair, and every stride-th token
   if (threadIdx.x < stride * half) {
     int axis = a.axes ? a.axes[pair] : 0;
@@ -156,8 +158,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int s
     cs[e] = tables[p];
     sn[e] = tables[tokens * half + p];
   }
-  for (int hb = first; hb < H; hb += kBatch * step) {
-    if (hb != first) load(hb);
+  auto finish = [&](int hb, V (&x)[kBatch], V (&y)[kBatch]) {
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
       const int h = hb + n * step;
@@ -171,6 +172,13 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int s
       *reinterpret_cast<V*>(dst) = x[n];
       if (!ADJ) *reinterpret_cast<V*>(dst + half) = y[n];
     }
+  };
+  const int ahead = kBatch * step;
+  for (int hb = first; hb < H; hb += 2 * ahead) {
+    if (hb + ahead < H) load(hb + ahead, x[1], y[1]);
+    finish(hb, x[0], y[0]);
+    if (hb + 2 * ahead < H) load(hb + 2 * ahead, x[0], y[0]);
+    if (hb + ahead < H) finish(hb + ahead, x[1], y[1]);
   }
 }
 
