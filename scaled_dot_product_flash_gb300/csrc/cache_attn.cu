@@ -616,8 +616,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][C::kSlab * nt + q][0]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = stat[w][C::kSlab * nt + q][0];
-          Lsum += mw == minus_inf() ? 0.f : stat[w][C::kSlab * nt + q][1] * ex2(mw - M);
+          // A warp without a maximum has seen nothing, or nothing but NaN: its sum is 0 or NaN.
+          const float mw = stat[w][C::kSlab * nt + q][0], lw = stat[w][C::kSlab * nt + q][1];
+          Lsum += mw == minus_inf() ? lw : lw * ex2(mw - M);
           const float4 y = *reinterpret_cast<const float4*>(red + (w * C::kSlab + q) * (D + 4) + d);
           v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
         }
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(CacheAttnArgs 
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
   for (int x = threadIdx.x; x < n; x += kJoinThreads)
-    if (ml[2 * x] != minus_inf()) L += ml[2 * x + 1] * ex2(ml[2 * x] - M);
+    L += ml[2 * x] == minus_inf() ? ml[2 * x + 1] : ml[2 * x + 1] * ex2(ml[2 * x] - M);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
   if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = L;

@@ -477,3 +477,24 @@ def test_a_growing_sequence_keeps_its_tokens():
         at += rows
     api.poll_status()
     assert at == n and torch.equal(once.view(torch.uint8), grown.view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G", [(32, 4), (128, 1), (128, 8), (64, 16)])
+def test_a_nan_key_reaches_out_and_lse(D, G):
+    """The newest token's key holds a NaN: the rows that see it are NaN in out and lse, alone in
+    its unit, as the only token, or beside finite ones of the same unit; the others are not."""
+    rng = np.random.default_rng(35)
+    unit = 64 if D <= 64 else 32
+    lens, H, L = [1, unit + 1, 3 * unit + 5, 700, 0], 2, 2
+    cache, table, ks, vs, low = fill(rng, lens, H, D, 32, "bf16")
+    q = draw_rows(rng, (len(lens), G * H, L, D), "bf16").cuda()
+    args = (q, cache, table.cuda(), ints(lens).cuda())
+    bad = torch.full((len(lens), H, 1, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    api.cache_write(cache, bad, bad, *args[2:])
+    out, lse = api.cache_attention(*args, need_lse=True)
+    api.poll_status()
+    for b, n in enumerate(lens):
+        assert bool(out[b, :, 1].isnan().all()) == (n > 0) and bool(lse[b, :, 1].isnan().all()) == (n > 0), n
+    before = [[x[:, :max(0, n - 1)] for x, n in zip(xs, lens)] for xs in (ks, vs, low)]
+    check(out[:, :, :1], lse[:, :, :1], q[:, :, :1], *before, 1 / math.sqrt(D), True, None, "bf16")
