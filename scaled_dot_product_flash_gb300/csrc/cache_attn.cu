@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       l[nt][n] = 0.f;
     }
   }
-  int k = kHalf ? 21 : 120;  // P·s enters the MMA times 2^k, at most 2^8·2^7
+  int k = kHalf ? 21 : 118;  // P·s enters the MMA times 2^k, at most 2^8·2^7 (and P·2^k is finite)
   uint32_t slimit = 1;       // scales whose bits reach this call for a smaller k
 
   // One unit in shared memory: scores, softmax, values.  Only units that a sequence's or a

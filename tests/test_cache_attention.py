@@ -498,3 +498,28 @@ def test_a_nan_key_reaches_out_and_lse(D, G):
         assert bool(out[b, :, 1].isnan().all()) == (n > 0) and bool(lse[b, :, 1].isnan().all()) == (n > 0), n
     before = [[x[:, :max(0, n - 1)] for x, n in zip(xs, lens)] for xs in (ks, vs, low)]
     check(out[:, :, :1], lse[:, :, :1], q[:, :, :1], *before, 1 / math.sqrt(D), True, None, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("B,H,G", [(1, 1, 1), (40, 8, 8)])
+def test_constant_values_under_rising_scores(B, H, G, dtype):
+    """Values whose groups are constant (scale 0), and scores that rise by 8 in base 2, as far as
+    a row's reference may lag, from one unit of a warp to its next: every output is the constant."""
+    D, page, rise = 32, 64, 256 if G <= 4 else 512                     # 4 or 8 warps of units of 64
+    n = 2 * rise
+    k = torch.zeros(B, H, n, D, dtype=TYPES[dtype])
+    k[..., 1] = 15.0                                                   # scale 1, zero 0: exact codes
+    k[:, :, rise:, 0] = 8.0
+    v = torch.full_like(k, 1.5)
+    table = torch.arange(B * n // page, dtype=torch.int32).view(B, n // page).cuda()
+    lens = ints([n] * B).cuda()
+    cache = dirty_cache(B * n // page, H, page, D, dtype)
+    api.cache_write(cache, k.cuda(), v.cuda(), table, lens)
+    q = torch.zeros(B, H * G, 1, D, dtype=TYPES[dtype], device="cuda")
+    q[..., 0] = 1.0
+    out, lse = api.cache_attention(q, cache, table, lens, scale=math.log(2), need_lse=True)
+    api.poll_status()
+    want = math.log(rise * (1 + 2.0**8))
+    assert bool((out == 1.5).all())                                    # 2^-16·1.5 is less than half a step
+    assert np.abs(as_f64(lse) - want).max() <= 2.0**-16 * want
