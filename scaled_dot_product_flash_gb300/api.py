@@ -456,6 +456,8 @@ def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
     need = _lib.sdpa_cache_attn_workspace_size(c, B, Hq, L, max_len)
     if workspace is None and need:
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    elif workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     st = _lib.sdpa_cache_attn(
         c, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if sinks is None else sinks.data_ptr(), _pack6(*qs, *os), B, Hq, L,

@@ -523,3 +523,13 @@ def test_constant_values_under_rising_scores(B, H, G, dtype):
     want = math.log(rise * (1 + 2.0**8))
     assert bool((out == 1.5).all())                                    # 2^-16·1.5 is less than half a step
     assert np.abs(as_f64(lse) - want).max() <= 2.0**-16 * want
+
+
+@pytest.mark.gpu
+def test_a_strided_workspace_is_refused():
+    cache = api.cache_empty(300, 1, 16, 64)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.arange(300, dtype=torch.int32, device="cuda").view(1, 300), ints([0]).cuda()
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 16), torch.empty(1 << 18, device="cuda")[::4]):
+        with pytest.raises(ValueError):
+            api.cache_attention(q, cache, table, lens, workspace=ws)
