@@ -726,7 +726,14 @@ Plan make_plan(const CacheAttnArgs& a) {
   const int64_t want = max((int64_t)1, slots / pairs);
   int64_t chunk = (a.max_len + want - 1) / want;
   if (pairs * 4 > slots) chunk = min(chunk, (int64_t)1536);
-  chunk = max(chunk, (int64_t)512);
+  // A second chunk costs the join, some 1.5 us, whatever it saves: none while one block's warps read
+  // the sequence in less.  One call of 8 KV heads, whole against chunks of 256: D = 128, 512 tokens,
+  // 5.8 us, 6.8, 1024 tokens 8.6, 6.9; D = 64, 1024 tokens 6.2, 6.4; D = 256, 512 tokens 10.8, 9.0;
+  // 32 rows (D = 64) 512 tokens 7.1, 7.6, 1024 tokens 9.2, 7.6.  Longer ones: chunks of at least
+  // 256 (1024 to 4096 tokens, D = 128: 6.9 to 7.7 us; of 512 8.2 to 8.5, of 128 6.6 to 7.7, but 11.0
+  // instead of 9.9 for 8 sequences).
+  const int whole = min(1024, (p.nt == 1 ? 65536 : 32768) / a.c.D);
+  chunk = a.max_len <= whole ? a.max_len : max(chunk, (int64_t)step);
   p.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
   p.splits = (a.max_len + p.chunk - 1) / p.chunk;
   return p;
@@ -775,7 +782,7 @@ cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
       default: return attn_nt<T, D, 2, 2>(a, p, s);
     }
   }
-  // A row of few chunks is joined by two warps; with many, 16 warps read them side by side
+  // A row of few chunks is joined by four warps; with many, 16 warps read them side by side
   // (131072 tokens in 57 chunks: 36.6 us a call with 4 warps, 34.1 with 16; 6 chunks: 41.9, 46.2).
   return p.splits > 16 ? join_t<T, D, 512>(a, p, s) : join_t<T, D, 128>(a, p, s);
 }
