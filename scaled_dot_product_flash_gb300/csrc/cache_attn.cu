@@ -16,6 +16,10 @@
 //    or, one nibble higher, 16·code·2^-24, which the tensor cores multiply exactly: one AND
 //    gives two operands (5 instructions for 8 codes).  The factors 16 and 2^-24 are undone in
 //    q, in the output and in fp32 scales.
+//    Sums over such small operands keep fewer low bits, the fewer the lower the nibble.  With 11
+//    bits of q it shows: at one token fp16 scores are off by 8.7e-7 rms, with every key nibble
+//    moved to the higher place (2 shifts more a word) by 0.9e-7.  fp16 keys are read so; bf16,
+//    3.3e-7 and 0.6e-7, keeps the fewer instructions (32 sequences 41.5 us, moved 42.8).
 //  - The product is transposed, S^T = K·Q^T and O^T = V^T·P^T (m16n8k16), so that the cache is
 //    the 16-row operand and 8 query rows fill the other one.
 //  - Scales stay outside the products: S = sum_j s_j·(c_j·q_j) + sum_j z_j·sum(q_j) over the
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   constexpr int kWarps = C::kWarps;
   using Tl = Tile<D>;
   constexpr int NG = Tl::NG, W = Tl::W, JB = Tl::JB, UT = C::UT;
-  constexpr bool kQSmem = NT > 1;
+  constexpr bool kQSmem = NT > 1, kHalf = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][C::kStages];
   __shared__ float stat[kWarps][C::kRows][2];
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   // two that brings its largest element to 2^13..2^14 (exact in fp16 down to 2^-27 of that), and by
   // the sign of the scale, so that the largest score is the largest accumulator (0 for a scale of
   // zero).  Lane (g, t) of a fragment has row g's elements 8t..8t+7 of a group, those of odd
-  // nibbles divided by the 16 that their codes carry.
+  // nibbles divided by the 16 that their codes carry (in fp16 all codes carry it).
   uint16_t* const q_frag = reinterpret_cast<uint16_t*>(smem + C::kQ);
   float* const q_sum = reinterpret_cast<float*>(smem + C::kSums);
   int* const q_exp = reinterpret_cast<int*>(smem + C::kExps);
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     for (int j = 0; j < NG; ++j) {
       x[j] *= up;
       const int n = lane % 8;  // element 8·(lane / 8) + n of the group
-      const float v = n & 1 ? x[j] * 0.0625f : x[j];
+      const float v = !kHalf && (n & 1) ? x[j] * 0.0625f : x[j];
       q_frag[((j * NT + nt) * 32 + g_row * 4 + lane / 8) * 8 + n % 4 * 2 + n / 4] = (uint16_t)f_to_bits<__half>(v);
     }
 #pragma unroll
@@ -270,9 +274,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     if (lane == 0) q_exp[rr] = e;
   }
   __syncthreads();
-  // The z term's share has bf16's range to be in the accumulators' units (2^-24) at once; in
-  // fp16 it stays at 2^13 or less and is scaled after its MMA.
-  constexpr bool kHalf = std::is_same<T, __half>::value;
+  // The z term's share has bf16's range to be in the accumulators' units (2^-24; 2^-20 in fp16,
+  // from the codes' 16) at once; in fp16 it stays at 2^13 or less and is scaled after its MMA.
+  constexpr int kUp = kHalf ? 20 : 24;
   constexpr float kZUp = kHalf ? 0x1p-6f : 0x1p-24f;
   const uint4* qs = reinterpret_cast<const uint4*>(smem + C::kQ);
   const bool row_here = CW == 2 || g % 2 == 0;  // odd columns of the narrow form are zero
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     }
   }
   uint32_t qz[NT][JB][2];  // group sums of the row, split in three (z term)
-  float f[NT][CW];         // per row of this lane's columns: |scale|·log2e·2^(24 - e) > 0
+  float f[NT][CW];         // per row of this lane's columns: |scale|·log2e·2^(kUp - e) > 0
   int lim[NT][CW];         // the same: positions below this are visible
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
     for (int n = 0; n < CW; ++n) {  // the accumulators' columns are 2t and 2t + 1
       const int rr = C::kSlab * nt + CW * t + n;
-      const int e = 24 - q_exp[rr], e0 = e / 2;  // -102..139: in two steps
+      const int e = kUp - q_exp[rr], e0 = e / 2;  // -102..139: in two steps
       f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(e0) * pow2(e - e0), 1e-37f);
       lim[nt][n] = a.causal ? len - c.L + (row0 + rr) % c.L + 1 : len;
     }
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int n = 0; n < CW; ++n) sc[ti][nt][hf][n] = kHalf ? acc[nt][2 * hf + n] * 0x1p-18f : acc[nt][2 * hf + n];
+          for (int n = 0; n < CW; ++n) sc[ti][nt][hf][n] = kHalf ? acc[nt][2 * hf + n] * 0x1p-14f : acc[nt][2 * hf + n];
     }
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb) {
@@ -387,8 +391,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           for (int ti = 0; ti < UT; ++ti) {
             const uint32_t x0 = kw[ti][0][w], x1 = kw[ti][1][w], y0 = x0 >> 8, y1 = x1 >> 8;
             float acc[4];
-            mma0<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
-            mma<__half>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
+            if constexpr (kHalf) {
+              mma0<__half>(acc, x0 << 4 & 0x00f000f0u, x1 << 4 & 0x00f000f0u, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
+              mma<__half>(acc, x0 >> 4 & 0x00f000f0u, x1 >> 4 & 0x00f000f0u, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
+            } else {
+              mma0<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
+              mma<__half>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
+            }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const float s = bits_to_f<T>(kp[ti][hf][w] & 0xffffu);

@@ -533,3 +533,21 @@ def test_a_strided_workspace_is_refused():
     for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 16), torch.empty(1 << 18, device="cuda")[::4]):
         with pytest.raises(ValueError):
             api.cache_attention(q, cache, table, lens, workspace=ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,G,L", [(32, 4, 1), (96, 1, 3), (128, 4, 1), (256, 16, 1)])
+def test_scores_keep_fp32_precision(D, G, L, dtype):
+    """lse of sequences of one token is the score itself.  D/32 groups, each a sum of 32 products
+    and a z term about twice as large as what is left of them: fp32 sums are off by some 2^-24 of
+    those terms' root sum, 2^-24·3·sqrt(D) against a score of sqrt(D)·|q||k|, and bf16 may be 4 times
+    that (its codes' lower nibbles are summed with up to 4 bits fewer): rms relative errors of
+    2^-22 and 2^-20."""
+    rng = np.random.default_rng(36)
+    B, H = 16, 8
+    cache, table, ks, vs, low = fill(rng, [1] * B, H, D, 16, dtype)
+    q = draw_rows(rng, (B, G * H, L, D), dtype)
+    _, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([1] * B).cuda(), need_lse=True, is_causal=False)
+    _, want = ref.cached_attention(as_f64(q), ks, vs, 1 / math.sqrt(D), False, None)
+    assert np.linalg.norm(as_f64(lse) - want) <= (2.0**-22 if dtype == "f16" else 2.0**-20) * np.linalg.norm(want)
