@@ -353,7 +353,8 @@ int sdpa_cache_write(const sdpa_cache_t* cache, const void* k, const void* v,
 /*
  * Reads the last L rows of each sequence back into k and v [B,Hkv,L,D] (every row is
  * written: 0 where the position is negative), layouts as in sdpa_cache_write.  Values are
- * z + s·c in fp32, rounded once.
+ * z + s·c in fp32, rounded once; an element within s/2 of dtype's largest number may so become
+ * an infinity (attention over the cache reads it in fp32).
  */
 int sdpa_cache_read(const sdpa_cache_t* cache, void* k, void* v, const sdpa_layout_t* layouts, int B,
                     int L, void* stream);
