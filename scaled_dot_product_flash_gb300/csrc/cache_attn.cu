@@ -80,7 +80,7 @@ __device__ __forceinline__ float ex2(float x) {
 // Transposes an 8 x 8 matrix of 16-bit elements held two a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x & 0xffffu))); }
@@ -336,7 +336,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   // row's end cuts, or that lack a tile, take the masked form.
   auto unit = [&](const uint8_t* st, int key0, uint32_t tiles, auto masked) {
     constexpr bool kMasked = decltype(masked)::value;
-    auto key_there = [&](int ti, int hf) { return key0 + ti * kTile + g + 8 * hf < end && ((tiles >> ti) & 1); };
+    // All ones where key g + 8·hf of tile ti is there, and where this lane's row sees it.  What
+    // differs from lane to lane is arithmetic on such words, not a branch: the MMAs and transposes
+    // need the whole warp at once, and a compiler may copy what follows a branch into its arms.
+    auto key_there = [&](int ti, int hf) { return (uint32_t)((key0 + ti * kTile + g + 8 * hf - end) >> 31) & (0u - ((tiles >> ti) & 1)); };
+    auto seen_by = [&](int ti, int hf, int nt, int n) { return (uint32_t)((key0 + ti * kTile + g + 8 * hf - lim[nt][n]) >> 31); };
+    const int tw = W == 4 ? t : min(t, W - 1);  // lanes beyond the groups repeat the last one
     // ---- scores
     float sc[UT][NT][2][CW];  // [.][.][half][n]: key g + 8·half, this lane's column n
 #pragma unroll
@@ -345,12 +350,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       float acc[NT][4];
 #pragma unroll
       for (int jb = 0; jb < JB; ++jb) {  // z of group 4·jb + t: (hi, mid) and (lo, nothing)
-        uint32_t z0 = 0, z1 = 0;
-        if (W == 4 || t < W) {
-          const uint32_t* zp = reinterpret_cast<const uint32_t*>(tile + Tl::kKp) + (jb * 16 + g) * W + t;
-          z0 = zp[0] >> 16;
-          z1 = zp[8 * W] >> 16;
-        }
+        const uint32_t* zp = reinterpret_cast<const uint32_t*>(tile + Tl::kKp) + (jb * 16 + g) * W + tw;
+        const uint32_t group_here = W == 4 ? ~0u : (uint32_t)((t - W) >> 31);
+        const uint32_t z0 = zp[0] >> 16 & group_here, z1 = zp[8 * W] >> 16 & group_here;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if (jb == 0) mma0<T>(acc[nt], z0 * 0x10001u, z1 * 0x10001u, z0, z1, qz[nt][jb][0], qz[nt][jb][1]);
@@ -424,8 +426,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           for (int hf = 0; hf < 2; ++hf) {
             float& x = sc[ti][nt][hf][n];
             if constexpr (kMasked) {
-              const int pos = key0 + ti * kTile + g + 8 * hf;
-              if (pos >= min(lim[nt][n], end) || !((tiles >> ti) & 1)) x = minus_inf();
+              const uint32_t here = key_there(ti, hf) & seen_by(ti, hf, nt, n);
+              x = __uint_as_float((__float_as_uint(x) & here) | (0xff800000u & ~here));
             }
             top = fmaxf(top, x);
           }
@@ -438,10 +440,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int jb = 0; jb < JB; ++jb) {
-          uint32_t w = 0;
-          if (W == 4 || t < W) w = reinterpret_cast<const uint32_t*>(st + ti * Tl::kBytes + Tl::kVp)[(jb * 16 + g + 8 * hf) * W + t];
-          if constexpr (kMasked)
-            if (!key_there(ti, hf)) w = 0;
+          uint32_t w = reinterpret_cast<const uint32_t*>(st + ti * Tl::kBytes + Tl::kVp)[(jb * 16 + g + 8 * hf) * W + tw];
+          if constexpr (kMasked) w &= key_there(ti, hf);
           smax = __vmaxu2(smax, w);
         }
     smax &= 0xffffu;  // scales are not negative: their bits order them
@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         }
     }
     const float up = pow2(k);
+    __syncwarp();
 #pragma unroll
     for (int ti = 0; ti < UT; ++ti) {
       float pu[NT][2][CW];
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int n = 0; n < CW; ++n) {
-            const float ref = kMasked && m[nt][n] == minus_inf() ? 0.f : m[nt][n];
+            const float ref = kMasked ? fmaxf(m[nt][n], -3.4e38f) : m[nt][n];  // -inf while nothing was seen: P = 0
             const float p = ex2(fmaf(sc[ti][nt][hf][n], f[nt][n], -ref));
             sc[ti][nt][hf][n] = p;
             l[nt][n] += p;
@@ -499,10 +500,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           load_words<W>(vw[hf], st + ti * Tl::kBytes + Tl::kV + ((hf * JB + jb) * 32 + lane) * W * 4);
           load_words<W>(vp[hf], st + ti * Tl::kBytes + Tl::kVp + (jb * 16 + g + 8 * hf) * W * 4);
           if constexpr (kMasked) {
-            if (!key_there(ti, hf)) {
 #pragma unroll
-              for (int w = 0; w < W; ++w) vp[hf][w] = 0;
-            }
+            for (int w = 0; w < W; ++w) vp[hf][w] &= key_there(ti, hf);
           }
         }
 #pragma unroll
@@ -523,7 +522,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
               for (int n = 0; n < CW; ++n) {
                 const float p = sc[ti][nt][hf][n];
                 q[hf][n] = pu[nt][hf][n] * s;
-                if constexpr (kMasked) zo[nt][j][n] += p == 0.f ? 0.f : p * z;  // a hidden key's z may be NaN
+                // A hidden key's z may be NaN: without a weight it counts as 0.
+                if constexpr (kMasked) zo[nt][j][n] = fmaf(p, __uint_as_float(__float_as_uint(z) & (uint32_t)(-__float_as_int(p) >> 31)), zo[nt][j][n]);
                 else zo[nt][j][n] = fmaf(p, z, zo[nt][j][n]);
               }
               hi[hf] = pack2<__half>(q[hf][0], q[hf][1]);

@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(CacheArgs c) {
     if (v == 0) {
       if (written(r)) store_words<W>(words, code);
     } else {
+      __syncwarp();  // the transposes need the whole warp, whose lanes' groups took different branches
 #pragma unroll
       for (int w = 0; w < W; ++w) code[w] = transpose8(code[w]);
       const bool low = written(2 * t + 8 * hf), high = written(2 * t + 1 + 8 * hf);
@@ -241,13 +242,19 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(CacheArgs c) {
     }
   }
   T* dst = row_ptr<T>(v ? c.v : c.k, v ? c.lv : c.lk, p.b, p.h, i) + 8 * t;
+  if (v) {  // before the stores, which only some lanes make
+    __syncwarp();
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb)
+#pragma unroll
+      for (int w = 0; w < W; ++w) code[jb][w] = transpose8(code[jb][w]);
+  }
+  __syncwarp();
+  if (i < 0 || i >= c.L) return;
 #pragma unroll
   for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const uint32_t x = v ? transpose8(code[jb][w]) : code[jb][w];
-      if (i >= 0 && i < c.L) *reinterpret_cast<uint4*>(dst + 32 * (jb * W + w)) = values8<T>(x, param[jb][w]);
-    }
+    for (int w = 0; w < W; ++w) *reinterpret_cast<uint4*>(dst + 32 * (jb * W + w)) = values8<T>(code[jb][w], param[jb][w]);
 }
 
 template <typename T, int D>

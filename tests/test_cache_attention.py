@@ -551,3 +551,18 @@ def test_scores_keep_fp32_precision(D, G, L, dtype):
     _, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([1] * B).cuda(), need_lse=True, is_causal=False)
     _, want = ref.cached_attention(as_f64(q), ks, vs, 1 / math.sqrt(D), False, None)
     assert np.linalg.norm(as_f64(lse) - want) <= (2.0**-22 if dtype == "f16" else 2.0**-20) * np.linalg.norm(want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G,L", [(32, 2, 1), (64, 4, 1), (96, 1, 2), (128, 4, 1), (256, 1, 1), (64, 8, 1), (128, 5, 1), (256, 2, 4), (96, 4, 4), (128, 8, 2)])
+def test_lengths_that_end_anywhere(D, G, L, dtype):
+    """Every length from 0 to two units and a little: ends inside tiles, halves and units of every
+    form, where the lanes of a warp differ in what they see."""
+    rng = np.random.default_rng(43)
+    lens = list(range(0, 70 if D > 64 else 132, 1 if D > 64 else 3))
+    cache, table, ks, vs, low = fill(rng, lens, 1, D, 16, dtype)
+    q = draw_rows(rng, (len(lens), G, L, D), dtype)
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True)
+    api.poll_status()
+    check(out, lse, q, ks, vs, low, 1 / math.sqrt(D), True, None, dtype)
