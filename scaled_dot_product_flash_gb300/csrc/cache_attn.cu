@@ -25,10 +25,12 @@
 //  - Scales stay outside the products: S = sum_j s_j·(c_j·q_j) + sum_j z_j·sum(q_j) over the
 //    groups j, the first in fp32 FMAs over one accumulator a group, the second as one MMA in
 //    the element type whose q sums are split in three so that nothing is lost.  For the values
-//    the probabilities take the scale, P·s in fp16 (normalised by a power of two that follows
-//    the largest scale, rounded once, 2^-11 relative); P·z is summed in fp32 FMAs.
-//    So scores are exact up to fp32 sums, and P·s is the only rounding to fewer bits; fp16
-//    outputs would show it, so there its remainder goes through a second MMA.
+//    the probabilities take the scale; P·s (normalised by a power of two that follows the
+//    largest scale) enters as two fp16 numbers, its leading 11 bits and what they leave, 2^-21
+//    relative in all.  One fp16 number would be cheaper (32 sequences 41.5 us) but is off by
+//    2^-11 of s·c, several 2^-12 of an output where s·c and z nearly cancel, so that a tenth of
+//    the bf16 outputs were rounded the other way.  P·z is summed in fp32 FMAs.  So nothing is
+//    rounded to fewer bits than fp32 sums show but the output.
 //
 // Measured (bf16, 32 query and 8 KV heads, D = 128, a call replayed from a graph): one sequence of
 // 131072 tokens 33.8 us, 168 MB, 5.0 TB/s (kernel alone 33.0 us under ncu with a cold L2, 65% of
@@ -47,8 +49,9 @@ namespace {
 
 // NT: row tiles of 8 rows that a block takes, CW: columns of the transposed products that a
 // lane holds.  CW = 2 is the plain form.  CW = 1 is the form for up to 4 rows, which would leave
-// half of the 8 columns empty: row r is column 2r and the odd columns are zero, so that every
-// lane has one row and half the elements of the softmax and of the scalings.
+// half of the 8 columns empty: row r is column 2r, so that every lane has one row and half the
+// elements of the softmax and of the scalings.  Its odd columns are zero in the scores; in the
+// values they take the remainders of P·s, which need a second MMA in the plain form.
 template <int D, int NT, int CW>
 struct Cfg {
   using Tl = Tile<D>;
@@ -83,8 +86,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x & 0xffffu))); }
-__device__ __forceinline__ float high_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
@@ -471,6 +472,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           for (int j = 0; j < 2 * NG; ++j) {
             o[j][nt][n] *= both;
             o[j][nt][2 + n] *= both;
+            if constexpr (CW == 1) {
+              o[j][nt][1] *= both;
+              o[j][nt][3] *= both;
+            }
           }
         }
     }
@@ -512,30 +517,29 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           const uint32_t c0 = y0 & 0x000f000fu, c1 = y0 & 0x00f000f0u, c2 = y1 & 0x000f000fu, c3 = y1 & 0x00f000f0u;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float q[2][2];
-            uint32_t hi[2];
+            float top[2][CW], rest[2][CW];  // P·s: its leading 11 bits, and the rest
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const float s = bits_to_f<T>(vp[hf][w] & 0xffffu), z = bits_to_f<T>(vp[hf][w] >> 16);
-              q[hf][1] = 0.f;
 #pragma unroll
               for (int n = 0; n < CW; ++n) {
-                const float p = sc[ti][nt][hf][n];
-                q[hf][n] = pu[nt][hf][n] * s;
+                const float p = sc[ti][nt][hf][n], q = pu[nt][hf][n] * s;
+                top[hf][n] = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
+                rest[hf][n] = q - top[hf][n];
                 // A hidden key's z may be NaN: without a weight it counts as 0.
                 if constexpr (kMasked) zo[nt][j][n] = fmaf(p, __uint_as_float(__float_as_uint(z) & (uint32_t)(-__float_as_int(p) >> 31)), zo[nt][j][n]);
                 else zo[nt][j][n] = fmaf(p, z, zo[nt][j][n]);
               }
-              hi[hf] = pack2<__half>(q[hf][0], q[hf][1]);
             }
-            uint32_t b0 = transpose8(hi[0]), b1 = transpose8(hi[1]);
+            const uint32_t b0 = transpose8(pack2<__half>(top[0][0], CW == 1 ? rest[0][0] : top[0][CW - 1]));
+            const uint32_t b1 = transpose8(pack2<__half>(top[1][0], CW == 1 ? rest[1][0] : top[1][CW - 1]));
             mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
             mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
-            if constexpr (kHalf) {  // what the rounding lost: outputs in fp16 would show it
-              b0 = transpose8(pack2<__half>(q[0][0] - low_h(hi[0]), q[0][1] - high_h(hi[0])));
-              b1 = transpose8(pack2<__half>(q[1][0] - low_h(hi[1]), q[1][1] - high_h(hi[1])));
-              mma<__half>(o[2 * j][nt], a0, a1, a2, a3, b0, b1);
-              mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, b0, b1);
+            if constexpr (CW == 2) {
+              const uint32_t r0 = transpose8(pack2<__half>(rest[0][0], rest[0][CW - 1]));
+              const uint32_t r1 = transpose8(pack2<__half>(rest[1][0], rest[1][CW - 1]));
+              mma<__half>(o[2 * j][nt], a0, a1, a2, a3, r0, r1);
+              mma<__half>(o[2 * j + 1][nt], c0, c1, c2, c3, r0, r1);
             }
           }
         }
@@ -608,11 +612,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
       for (int n = 0; n < CW; ++n) {
         const float z = zo[nt][j][n];
+        auto sum = [&](int jj, int hf) { return CW == 1 ? o[jj][nt][2 * hf] + o[jj][nt][2 * hf + 1] : o[jj][nt][2 * hf + n]; };
         float4 v;
-        v.x = (o[2 * j][nt][n] * back0 * back1 + z) * wgt[n];
-        v.y = (o[2 * j][nt][2 + n] * back0 * odd1 + z) * wgt[n];
-        v.z = (o[2 * j + 1][nt][n] * back0 * back1 + z) * wgt[n];
-        v.w = (o[2 * j + 1][nt][2 + n] * back0 * odd1 + z) * wgt[n];
+        v.x = (sum(2 * j, 0) * back0 * back1 + z) * wgt[n];
+        v.y = (sum(2 * j, 1) * back0 * odd1 + z) * wgt[n];
+        v.z = (sum(2 * j + 1, 0) * back0 * back1 + z) * wgt[n];
+        v.w = (sum(2 * j + 1, 1) * back0 * odd1 + z) * wgt[n];
         *reinterpret_cast<float4*>(red + (warp * C::kSlab + CW * t + n) * (D + 4) + 32 * j + 4 * g) = v;
       }
     __syncthreads();

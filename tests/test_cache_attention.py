@@ -566,3 +566,32 @@ def test_lengths_that_end_anywhere(D, G, L, dtype):
     out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True)
     api.poll_status()
     check(out, lse, q, ks, vs, low, 1 / math.sqrt(D), True, None, dtype)
+
+
+def sizes(q, ks, vs, low, scale, causal, sink):
+    """sum_j w_j·(|z| + s·c) of every output element: what its fp32 sums are made of."""
+    return ref.cached_attention(as_f64(q), ks, [np.abs(v - x) + x for v, x in zip(vs, low)], scale, causal, sink)[0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G,L", [(128, 4, 1), (32, 2, 2), (128, 8, 1), (96, 5, 1), (64, 4, 4), (128, 4, 8), (256, 1, 1), (256, 16, 1)])
+def test_outputs_are_rounded_once(D, G, L, dtype):
+    """P·s is as good as fp32: an output differs from the rounded exact one only where that lies
+    close to the middle of two numbers.  With |S| of a few units an output is off by less than
+    off = 2^-19·sum_j w_j·(|z| + s·c) before it is rounded (2^-20 the sums of the MMA, where lower
+    nibbles keep fewer low bits, 2^-21 P·s, 2^-22 twice the scores and what follows from them), so
+    that the odds of an element are 2·off / step; their sum over all elements, and 4 standard
+    deviations, bounds how many differ.  (P·s rounded to 2^-11 changes one bf16 output in six.)"""
+    rng = np.random.default_rng(37)
+    lens, H = [100, 61, 33, 128], 2
+    cache, table, ks, vs, low = fill(rng, lens, H, D, 16, dtype)
+    q = draw_rows(rng, (len(lens), G * H, L, D), dtype, 0.5)
+    out, _ = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda())
+    api.poll_status()
+    o, _ = ref.cached_attention(as_f64(q), ks, vs, 1 / math.sqrt(D), True, None)
+    off = 2.0**-19 * sizes(q, ks, vs, low, 1 / math.sqrt(D), True, None)
+    step = torch.finfo(TYPES[dtype]).eps * np.exp2(np.floor(np.log2(np.abs(o))))
+    odds = np.minimum(1, 2 * off / step).sum()
+    differ = (as_f64(out) != ref.rounded(o, TYPES[dtype])).sum()
+    assert differ <= odds + 4 * math.sqrt(odds) + 1, f"{differ} of {o.size} differ, {odds:.1f} expected at most"
