@@ -15,11 +15,10 @@
 //  - Codes are not converted.  A nibble masked in place is a subnormal fp16 number, code·2^-24
 //    or, one nibble higher, 16·code·2^-24, which the tensor cores multiply exactly: one AND
 //    gives two operands (5 instructions for 8 codes).  The factors 16 and 2^-24 are undone in
-//    q, in the output and in fp32 scales.
-//    Sums over such small operands keep fewer low bits, the fewer the lower the nibble.  With 11
-//    bits of q it shows: at one token fp16 scores are off by 8.7e-7 rms, with every key nibble
-//    moved to the higher place (2 shifts more a word) by 0.9e-7.  fp16 keys are read so; bf16,
-//    3.3e-7 and 0.6e-7, keeps the fewer instructions (32 sequences 41.5 us, moved 42.8).
+//    the output and in fp32 scales.
+//    Sums over such small operands keep fewer low bits, the fewer the lower the nibble.  In the
+//    scores that would show (at one token off by 8.7e-7 rms in fp16, 3.3e-7 in bf16), so every
+//    key nibble is moved to the higher place, 2 shifts more a word (0.9e-7 and 0.6e-7).
 //  - The product is transposed, S^T = K·Q^T and O^T = V^T·P^T (m16n8k16), so that the cache is
 //    the 16-row operand and 8 query rows fill the other one.
 //  - Scales stay outside the products: S = sum_j s_j·(c_j·q_j) + sum_j z_j·sum(q_j) over the
@@ -240,8 +239,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   // ---- query rows as the B operand, through shared memory.  A row is multiplied by the power of
   // two that brings its largest element to 2^13..2^14 (exact in fp16 down to 2^-27 of that), and by
   // the sign of the scale, so that the largest score is the largest accumulator (0 for a scale of
-  // zero).  Lane (g, t) of a fragment has row g's elements 8t..8t+7 of a group, those of odd
-  // nibbles divided by the 16 that their codes carry (in fp16 all codes carry it).
+  // zero).  Lane (g, t) of a fragment has row g's elements 8t..8t+7 of a group.
   uint16_t* const q_frag = reinterpret_cast<uint16_t*>(smem + C::kQ);
   float* const q_sum = reinterpret_cast<float*>(smem + C::kSums);
   int* const q_exp = reinterpret_cast<int*>(smem + C::kExps);
@@ -263,8 +261,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     for (int j = 0; j < NG; ++j) {
       x[j] *= up;
       const int n = lane % 8;  // element 8·(lane / 8) + n of the group
-      const float v = !kHalf && (n & 1) ? x[j] * 0.0625f : x[j];
-      q_frag[((j * NT + nt) * 32 + g_row * 4 + lane / 8) * 8 + n % 4 * 2 + n / 4] = (uint16_t)f_to_bits<__half>(v);
+      q_frag[((j * NT + nt) * 32 + g_row * 4 + lane / 8) * 8 + n % 4 * 2 + n / 4] = (uint16_t)f_to_bits<__half>(x[j]);
     }
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
@@ -275,10 +272,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     if (lane == 0) q_exp[rr] = e;
   }
   __syncthreads();
-  // The z term's share has bf16's range to be in the accumulators' units (2^-24; 2^-20 in fp16,
-  // from the codes' 16) at once; in fp16 it stays at 2^13 or less and is scaled after its MMA.
-  constexpr int kUp = kHalf ? 20 : 24;
-  constexpr float kZUp = kHalf ? 0x1p-6f : 0x1p-24f;
+  // The z term's share has bf16's range to be in the accumulators' units (2^-20: the codes are 16
+  // times theirs) at once; in fp16 it stays at 2^13 or less and is scaled after its MMA.
+  constexpr int kUp = 20;
+  constexpr float kZUp = kHalf ? 0x1p-6f : 0x1p-20f;
   const uint4* qs = reinterpret_cast<const uint4*>(smem + C::kQ);
   const bool row_here = CW == 2 || g % 2 == 0;  // odd columns of the narrow form are zero
   uint32_t qf[kQSmem ? 1 : NG][4];
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
     for (int n = 0; n < CW; ++n) {  // the accumulators' columns are 2t and 2t + 1
       const int rr = C::kSlab * nt + CW * t + n;
-      const int e = kUp - q_exp[rr], e0 = e / 2;  // -102..139: in two steps
+      const int e = kUp - q_exp[rr], e0 = e / 2;  // -106..135: in two steps
       f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(e0) * pow2(e - e0), 1e-37f);
       lim[nt][n] = a.causal ? len - c.L + (row0 + rr) % c.L + 1 : len;
     }
@@ -394,13 +391,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           for (int ti = 0; ti < UT; ++ti) {
             const uint32_t x0 = kw[ti][0][w], x1 = kw[ti][1][w], y0 = x0 >> 8, y1 = x1 >> 8;
             float acc[4];
-            if constexpr (kHalf) {
-              mma0<__half>(acc, x0 << 4 & 0x00f000f0u, x1 << 4 & 0x00f000f0u, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
-              mma<__half>(acc, x0 >> 4 & 0x00f000f0u, x1 >> 4 & 0x00f000f0u, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
-            } else {
-              mma0<__half>(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
-              mma<__half>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
-            }
+            mma0<__half>(acc, x0 << 4 & 0x00f000f0u, x1 << 4 & 0x00f000f0u, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qq[0], qq[1]);
+            mma<__half>(acc, x0 >> 4 & 0x00f000f0u, x1 >> 4 & 0x00f000f0u, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qq[2], qq[3]);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const float s = bits_to_f<T>(kp[ti][hf][w] & 0xffffu);

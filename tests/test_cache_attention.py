@@ -595,3 +595,18 @@ def test_outputs_are_rounded_once(D, G, L, dtype):
     odds = np.minimum(1, 2 * off / step).sum()
     differ = (as_f64(out) != ref.rounded(o, TYPES[dtype])).sum()
     assert differ <= odds + 4 * math.sqrt(odds) + 1, f"{differ} of {o.size} differ, {odds:.1f} expected at most"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G,L", [(32, 4, 1), (96, 1, 3), (128, 4, 1), (128, 8, 1), (256, 16, 1)])
+def test_bf16_scores_keep_fp32_precision(D, G, L):
+    """The same, and the same bound as fp16's, for bf16: the sums over its codes' lower nibbles lose
+    nothing either."""
+    rng = np.random.default_rng(38)
+    B, H = 16, 8
+    cache, table, ks, vs, low = fill(rng, [1] * B, H, D, 16, "bf16")
+    q = draw_rows(rng, (B, G * H, L, D), "bf16")
+    _, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([1] * B).cuda(), need_lse=True, is_causal=False)
+    api.poll_status()
+    _, want = ref.cached_attention(as_f64(q), ks, vs, 1 / math.sqrt(D), False, None)
+    assert np.linalg.norm(as_f64(lse) - want) <= 2.0**-22 * np.linalg.norm(want)
