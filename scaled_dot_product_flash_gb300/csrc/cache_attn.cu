@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
                 const float p = sc[ti][nt][hf][n], q = pu[nt][hf][n] * s;
                 top[hf][n] = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
                 rest[hf][n] = q - top[hf][n];
-                // A hidden key's z may be NaN: without a weight it counts as 0.
-                if constexpr (kMasked) zo[nt][j][n] = fmaf(p, __uint_as_float(__float_as_uint(z) & (uint32_t)(-__float_as_int(p) >> 31)), zo[nt][j][n]);
+                // A hidden key's z may be NaN and counts as 0; a visible one's is seen, whatever its weight.
+                if constexpr (kMasked) zo[nt][j][n] = fmaf(p, __uint_as_float(__float_as_uint(z) & seen_by(ti, hf, nt, n)), zo[nt][j][n]);
                 else zo[nt][j][n] = fmaf(p, z, zo[nt][j][n]);
               }
             }

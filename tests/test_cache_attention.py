@@ -610,3 +610,32 @@ def test_bf16_scores_keep_fp32_precision(D, G, L):
     api.poll_status()
     _, want = ref.cached_attention(as_f64(q), ks, vs, 1 / math.sqrt(D), False, None)
     assert np.linalg.norm(as_f64(lse) - want) <= 2.0**-22 * np.linalg.norm(want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G,L", [(128, 4, 1), (64, 8, 1), (128, 2, 8)])
+def test_a_nan_value_without_weight_is_nan_wherever_it_lies(D, G, L):
+    """A visible key whose probability is 0 (a score of -1000) and whose values of one group are
+    NaN: 0·NaN is NaN, in a whole unit as in one that the sequence's or a query's end cuts; the
+    queries before it do not see it."""
+    rng = np.random.default_rng(39)
+    H, page = 2, 32
+    lens = [200, 200, 200, 33]
+    bad = [10, 150, 199, 32]                                           # its position: inside, and last
+    table, pages = make_table(rng, lens, page)
+    cache = dirty_cache(pages, H, page, D, "bf16")
+    k, v = (draw_rows(rng, (len(lens), H, 200, D), "bf16") for _ in range(2))
+    k[..., 0] = 0
+    for b, n in enumerate(lens):
+        k[b, :, 200 - n + bad[b], 0] = -1000 * math.sqrt(D)
+        v[b, :, 200 - n + bad[b], 37] = float("nan")
+    q = draw_rows(rng, (len(lens), G * H, L, D), "bf16")
+    q[..., 0] = 1.0
+    api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints(lens).cuda())
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True)
+    api.poll_status()
+    assert torch.isfinite(lse).all() and torch.isfinite(out[..., :32]).all() and torch.isfinite(out[..., 64:]).all()
+    for b, n in enumerate(lens):
+        for i in range(L):
+            got = out[b, :, i, 32:64].isnan()
+            assert bool(got.all()) if n - L + i >= bad[b] else not bool(got.any()), (b, i)
