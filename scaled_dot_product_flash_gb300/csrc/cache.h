@@ -52,7 +52,8 @@ struct CacheAttnArgs {
   const float* sinks;  // nullable
   Layout lq, lo;
   int Hq, G;
-  float scale_log2;
+  float scale_mant;    // scale·log2e = scale_mant·2^scale_exp, |scale_mant| in [1/2, 1) or 0
+  int scale_exp;
   int causal;
   int max_len;         // longest sequence, in tokens
   float* workspace;

@@ -251,7 +251,7 @@ extern "C" int sdpa_cache_attn(const sdpa_cache_t* cache, const void* q, void* o
   a.out = out;
   a.lse = lse;
   a.sinks = sinks;
-  a.scale_log2 = scale * kLog2e;
+  a.scale_mant = (float)std::frexp((double)scale * 1.4426950408889634, &a.scale_exp);
   a.causal = is_causal != SDPA_CAUSAL_NONE;
   a.workspace = static_cast<float*>(workspace);
   a.wait_limit_ns = wait_limit_ns();

@@ -70,8 +70,8 @@ struct Cfg {
   static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQ = kBody;                              // q fragments: [group][NT][lane] of 16 bytes
   static constexpr int kSums = kQ + NT * Tl::NG * 32 * 16;      // q's group sums, fp32 [row][group]
-  static constexpr int kExps = kSums + kRows * Tl::NG * 4;      // q's exponents, int [row]
-  static constexpr int kSmem = kExps + kRows * 4;
+  static constexpr int kUnits = kSums + kRows * Tl::NG * 4;     // the scores' units, float2 [row]
+  static constexpr int kSmem = kUnits + kRows * 8;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -242,7 +242,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   // zero).  Lane (g, t) of a fragment has row g's elements 8t..8t+7 of a group.
   uint16_t* const q_frag = reinterpret_cast<uint16_t*>(smem + C::kQ);
   float* const q_sum = reinterpret_cast<float*>(smem + C::kSums);
-  int* const q_exp = reinterpret_cast<int*>(smem + C::kExps);
+  // A score is its accumulator times |scale|·log2e·2^(kUp - e), one fp32 number f unless that is
+  // far from 1 (a row of large elements; a scale of 1e30): then f is about its square root, and
+  // accumulators are multiplied by the other root first, a power of two.
+  constexpr int kUp = 20;
+  float2* const q_unit = reinterpret_cast<float2*>(smem + C::kUnits);
+  bool far = false;
 #pragma unroll
   for (int n_row = 0; n_row < kMine; ++n_row) {
     const int rr = warp + n_row * kWarps;
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     // A row of zeros (or subnormals) takes 2^126; one with an infinity 2^-115, and turns NaN by itself.
     const int e = min(126, 13 - ((__float_as_int(top) >> 23) - 127));
-    const float up = a.scale_log2 == 0.f ? 0.f : copysignf(pow2(e), a.scale_log2);
+    const float up = a.scale_mant == 0.f ? 0.f : copysignf(pow2(e), a.scale_mant);
     const int nt = CW == 2 ? rr / 8 : 0, g_row = CW == 2 ? rr % 8 : 2 * rr;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
@@ -269,12 +274,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       for (int off = 16; off > 0; off >>= 1) x[j] += __shfl_xor_sync(0xffffffffu, x[j], off);
       if (lane == j) q_sum[rr * NG + j] = x[j];
     }
-    if (lane == 0) q_exp[rr] = e;
+    const int u = a.scale_exp + kUp - e, root = u / 2;
+    const bool wide = a.scale_mant != 0.f && (u < -100 || u > 100);
+    far = far || wide;
+    if (lane == 0) {
+      const float mant = a.scale_mant == 0.f ? 1.f : fabsf(a.scale_mant);
+      if (wide) q_unit[rr] = make_float2(mant * pow2(max(-126, min(127, u - root))), pow2(max(-126, min(127, root))));
+      else q_unit[rr] = make_float2(a.scale_mant == 0.f ? 1.f : mant * pow2(u), 1.f);
+    }
   }
-  __syncthreads();
+  far = __syncthreads_or(far);
   // The z term's share has bf16's range to be in the accumulators' units (2^-20: the codes are 16
   // times theirs) at once; in fp16 it stays at 2^13 or less and is scaled after its MMA.
-  constexpr int kUp = 20;
   constexpr float kZUp = kHalf ? 0x1p-6f : 0x1p-20f;
   const uint4* qs = reinterpret_cast<const uint4*>(smem + C::kQ);
   const bool row_here = CW == 2 || g % 2 == 0;  // odd columns of the narrow form are zero
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
     }
   }
   uint32_t qz[NT][JB][2];  // group sums of the row, split in three (z term)
-  float f[NT][CW];         // per row of this lane's columns: |scale|·log2e·2^(kUp - e) > 0
+  float f[NT][CW];         // per row of this lane's columns: score per accumulator, > 0
   int lim[NT][CW];         // the same: positions below this are visible
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -305,8 +316,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
     for (int n = 0; n < CW; ++n) {  // the accumulators' columns are 2t and 2t + 1
       const int rr = C::kSlab * nt + CW * t + n;
-      const int e = kUp - q_exp[rr], e0 = e / 2;  // -106..135: in two steps
-      f[nt][n] = a.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * pow2(e0) * pow2(e - e0), 1e-37f);
+      f[nt][n] = q_unit[rr].x;
       lim[nt][n] = a.causal ? len - c.L + (row0 + rr) % c.L + 1 : len;
     }
   }
@@ -402,6 +412,20 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           }
         }
       }
+    }
+
+    if (far) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int n = 0; n < CW; ++n) {
+          const float root = q_unit[C::kSlab * nt + CW * t + n].y;
+#pragma unroll
+          for (int ti = 0; ti < UT; ++ti) {
+            sc[ti][nt][0][n] *= root;
+            sc[ti][nt][1][n] *= root;
+          }
+        }
     }
 
     // ---- softmax.  The reference m of a row need not be its running maximum: it stays until

@@ -639,3 +639,33 @@ def test_a_nan_value_without_weight_is_nan_wherever_it_lies(D, G, L):
         for i in range(L):
             got = out[b, :, i, 32:64].isnan()
             assert bool(got.all()) if n - L + i >= bad[b] else not bool(got.any()), (b, i)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [None, 1.0, -0.25, 1e30, 1e-30])
+@pytest.mark.parametrize("D,G,L", [(32, 4, 1), (128, 8, 1), (64, 4, 4), (256, 2, 1)])
+def test_queries_up_to_the_largest(D, G, L, scale):
+    """Rows of 2^90 to bf16's largest numbers, and tiny ones, whose scores are ordinary because the
+    keys are small, and keys of zero, whose scores are 0 whatever the query and the scale."""
+    rng = np.random.default_rng(40)
+    H, n = 1, 70
+    used = 1 / math.sqrt(D) if scale is None else scale
+    for power in (127, 126, 120, 90, -100):
+        key = -power - math.log2(abs(used)) + 1.0 - math.log2(D) / 2   # |S| of a few units
+        for zero in (False, True):
+            if not zero and abs(key) > 118:
+                continue
+            table, pages = make_table(rng, [n], 16)
+            cache = dirty_cache(pages, H, 16, D, "bf16")
+            v = draw_rows(rng, (1, H, n, D), "bf16")
+            k = torch.zeros_like(v) if zero else (draw_rows(rng, (1, H, n, D), "bf16").double() * 2.0**key).to(v.dtype)
+            # Uniform in (-1, 1), so that no element passes the type's largest number; the first row is plain.
+            q = torch.from_numpy(rng.uniform(-1, 1, (1, G * H, L, D))) * 2.0**power
+            q[:, 0] *= 2.0**-power * 2.0**min(power, 60)
+            q = q.to(v.dtype)
+            api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints([n]).cuda())
+            out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda(), scale=scale, need_lse=True)
+            api.poll_status()
+            code, s, z = ref.quantise(as_f64(v)[0], torch.bfloat16)
+            ks, vs, low = [held(as_f64(k)[0], "bf16")], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
+            check(out, lse, q, ks, vs, low, float(np.float32(used)), True, None, "bf16")
