@@ -24,12 +24,17 @@
 //  - Scales stay outside the products: S = sum_j s_j·(c_j·q_j) + sum_j z_j·sum(q_j) over the
 //    groups j, the first in fp32 FMAs over one accumulator a group, the second as one MMA in
 //    the element type whose q sums are split in three so that nothing is lost.  For the values
-//    the probabilities take the scale; P·s (normalised by a power of two that follows the
-//    largest scale) enters as two fp16 numbers, its leading 11 bits and what they leave, 2^-21
-//    relative in all.  One fp16 number would be cheaper (32 sequences 41.5 us) but is off by
-//    2^-11 of s·c, several 2^-12 of an output where s·c and z nearly cancel, so that a tenth of
-//    the bf16 outputs were rounded the other way.  P·z is summed in fp32 FMAs.  So nothing is
-//    rounded to fewer bits than fp32 sums show but the output.
+//    the probabilities take the scale; P·s, times a power of two, enters as two fp16 numbers, its
+//    leading 11 bits and what they leave, 2^-21 relative in all and 2^-22 of the largest P·s.
+//    One fp16 number would be cheaper (32 sequences 41.5 us) but is off by 2^-11 of s·c, several
+//    2^-12 of an output where s·c and z nearly cancel, so that a tenth of the bf16 outputs were
+//    rounded the other way.  P·z is summed in fp32 FMAs.  So nothing is rounded to fewer bits than
+//    fp32 sums show but the output.
+//  - fp16 has 40 binades, P·s in bf16 over 250.  So every row has a power of two for each group
+//    of values, chosen from products P·s that the row has really seen: a key that it does not
+//    see, or whose weight is nothing, does not move it, whatever its values.  They seldom move:
+//    a warp looks at P·s only when a score passes the row's reference or a scale of the unit
+//    passes what the powers in use allow, a vote a unit.
 //
 // Measured (bf16, 32 query and 8 KV heads, D = 128, a call replayed from a graph): one sequence of
 // 131072 tokens 33.8 us, 168 MB, 5.0 TB/s (kernel alone 33.0 us under ncu with a cold L2, 65% of
@@ -71,7 +76,8 @@ struct Cfg {
   static constexpr int kQ = kBody;                              // q fragments: [group][NT][lane] of 16 bytes
   static constexpr int kSums = kQ + NT * Tl::NG * 32 * 16;      // q's group sums, fp32 [row][group]
   static constexpr int kUnits = kSums + kRows * Tl::NG * 4;     // the scores' units, float2 [row]
-  static constexpr int kSmem = kUnits + kRows * 8;
+  static constexpr int kPowers = kUnits + kRows * 8;            // each warp's powers of two, fp32 [warp][group][row]
+  static constexpr int kSmem = kPowers + kWarps * Tl::NG * kRows * 4;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -112,7 +118,9 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127 (0 for -127)
+__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x >= 0: floor(log2 x), -127 below 2^-126
+constexpr int kFree = 119;  // exponent of a power of two that nothing has fixed yet
 
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* p) {
@@ -322,9 +330,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   }
   const int seen = a.causal ? len - c.L + 1 : len;  // every row sees the positions below this
 
-  float o[2 * NG][NT][4];  // O^T, times 2^(k - 24)
+  float o[2 * NG][NT][4];  // O^T, times wt·2^-24
   float zo[NT][NG][CW];    // this lane's keys' P·z
-  float m[NT][CW], l[NT][CW], high[NT][CW];  // reference, sum, score that calls for a new reference
+  float m[NT][CW], l[NT][CW];  // reference (P <= 1), sum
+  float wt[NT][NG][CW];    // P·s enters the MMA times this power of two, at most 2^15
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -332,13 +341,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
     for (int n = 0; n < CW; ++n) {
 #pragma unroll
-      for (int j = 0; j < NG; ++j) zo[nt][j][n] = 0.f;
-      m[nt][n] = high[nt][n] = minus_inf();
+      for (int j = 0; j < NG; ++j) {
+        zo[nt][j][n] = 0.f;
+        wt[nt][j][n] = pow2(kFree);
+      }
+      m[nt][n] = minus_inf();
       l[nt][n] = 0.f;
     }
   }
-  int k = kHalf ? 21 : 118;  // P·s enters the MMA times 2^k, at most 2^8·2^7 (and P·2^k is finite)
-  uint32_t slimit = 1;       // scales whose bits reach this call for a smaller k
+  uint32_t slimit[JB];  // scales of group 4·jb + t whose bits reach this call for other powers
+#pragma unroll
+  for (int jb = 0; jb < JB; ++jb) slimit[jb] = 1;
+  float* const powers = reinterpret_cast<float*>(smem + C::kPowers) + warp * (NG * C::kRows);
+  bool fresh = true;  // no unit yet
 
   // One unit in shared memory: scores, softmax, values.  Only units that a sequence's or a
   // row's end cuts, or that lack a tile, take the masked form.
@@ -428,10 +443,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         }
     }
 
-    // ---- softmax.  The reference m of a row need not be its running maximum: it stays until
-    // some score is more than 2^8 above it (P <= 2^8 then), and so does the power of two of the
-    // value scales until one is over 2^7 times too large.  One vote covers both.
-    bool over = false;
+    // ---- softmax.  The reference m of a row starts 2^8 above its largest score and stays until
+    // some score passes it; wt stays until a scale could take P·s·wt over 2^15.  One vote covers
+    // both.
+    bool move = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -448,26 +463,26 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
             }
             top = fmaxf(top, x);
           }
-        over = over || top > high[nt][n];
+        move = move || fmaf(top, f[nt][n], -m[nt][n]) > 0.f;
       }
-    uint32_t smax = 0;  // lane (g, t) looks at group t of rows g and g + 8
+    uint32_t smax[JB];  // lane (g, t) looks at group 4·jb + t of rows g and g + 8
 #pragma unroll
-    for (int ti = 0; ti < UT; ++ti)
+    for (int jb = 0; jb < JB; ++jb) {
+      smax[jb] = 0;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int ti = 0; ti < UT; ++ti)
 #pragma unroll
-        for (int jb = 0; jb < JB; ++jb) {
+        for (int hf = 0; hf < 2; ++hf) {
           uint32_t w = reinterpret_cast<const uint32_t*>(st + ti * Tl::kBytes + Tl::kVp)[(jb * 16 + g + 8 * hf) * W + tw];
           if constexpr (kMasked) w &= key_there(ti, hf);
-          smax = __vmaxu2(smax, w);
+          smax[jb] = __vmaxu2(smax[jb], w);
         }
-    smax &= 0xffffu;  // scales are not negative: their bits order them
-    if (__any_sync(0xffffffffu, over || smax >= slimit)) {
-      smax = __reduce_max_sync(0xffffffffu, smax);
-      const int k_new = min(k, 5 - ((__float_as_int(bits_to_f<T>(smax)) >> 23) - 127));
-      const float down = k - k_new > 126 ? 0.f : pow2(k_new - k);
-      k = k_new;
-      slimit = f_to_bits<T>(min(7 - k, 127) < 16 || !kHalf ? pow2(min(7 - k, 127)) : 65504.f);
+      smax[jb] &= 0xffffu;  // scales are not negative: their bits order them
+      move = move || smax[jb] >= slimit[jb];
+    }
+    if (__any_sync(0xffffffffu, move)) {
+      float al[NT][CW];
+      bool plain = fresh;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -477,29 +492,125 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           for (int ti = 0; ti < UT; ++ti) top = fmaxf(top, fmaxf(sc[ti][nt][0][n], sc[ti][nt][1][n]));
 #pragma unroll
           for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          const float m_new = fmaxf(m[nt][n], top * f[nt][n]);
-          const float al = m_new == minus_inf() ? 1.f : ex2(m[nt][n] - m_new), both = al * down;
+          const float m_old = m[nt][n], m_new = fmaf(top, f[nt][n], -m_old) > 0.f ? __fmaf_ru(top, f[nt][n], 8.f) : m_old;
+          al[nt][n] = m_new == m_old ? 1.f : ex2(m_old - m_new);
           m[nt][n] = m_new;
-          high[nt][n] = (m_new + 8.f) / f[nt][n];
-          l[nt][n] *= al;
+          plain = plain && m_new > minus_inf();
+        }
+      // Largest scale (high half) and the complement of the smallest one of group 4·jb + t.
+      uint32_t range[JB];
 #pragma unroll
-          for (int j = 0; j < NG; ++j) zo[nt][j][n] *= al;
+      for (int jb = 0; jb < JB; ++jb) {
+        range[jb] = 0;
 #pragma unroll
-          for (int j = 0; j < 2 * NG; ++j) {
-            o[j][nt][n] *= both;
-            o[j][nt][2 + n] *= both;
-            if constexpr (CW == 1) {
-              o[j][nt][1] *= both;
-              o[j][nt][3] *= both;
+        for (int ti = 0; ti < UT; ++ti)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(st + ti * Tl::kBytes + Tl::kVp)[(jb * 16 + g + 8 * hf) * W + tw];
+            uint32_t both = w << 16 | (~w & 0xffffu);
+            if constexpr (kMasked) both &= key_there(ti, hf);
+            range[jb] = __vmaxu2(range[jb], both);
+          }
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) range[jb] = __vmaxu2(range[jb], __shfl_xor_sync(0xffffffffu, range[jb], off));
+        plain = plain && exponent(bits_to_f<T>(range[jb] >> 16)) - exponent(bits_to_f<T>(~range[jb] & 0xffffu)) <= 4;
+      }
+      if (__all_sync(0xffffffffu, plain)) {
+        // A first unit of the usual kind: every row sees a key, so that its largest P is 2^-8, and
+        // no scale is under 2^-5 of its group's largest.  The power that takes that one to
+        // 2^10..2^11 then has a product P·s of at least 2^-3 in every row.
+        int now[JB];
+#pragma unroll
+        for (int jb = 0; jb < JB; ++jb) {
+          now[jb] = min(kFree - 1, 10 - exponent(bits_to_f<T>(range[jb] >> 16)));
+          slimit[jb] = max(1u, f_to_bits<T>(pow2(15 - now[jb])));
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          const float power = pow2(__shfl_sync(0xffffffffu, now[j / W], j % W));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int n = 0; n < CW; ++n) wt[nt][j][n] = power;
+        }
+      } else {
+        // The products themselves, row by row and group by group, in loops that are not unrolled
+        // (code that seldom runs costs what it takes to fetch it), with the powers in shared memory.
+        float* const mine = powers + CW * t;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int n = 0; n < CW; ++n)
+#pragma unroll
+            for (int j = 0; j < NG; ++j) mine[j * C::kRows + C::kSlab * nt + n] = wt[nt][j][n];
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int n = 0; n < CW; ++n) {
+            const int e_al = al[nt][n] > 0.f ? exponent(al[nt][n]) : -512;  // -512: what was seen before counts for nothing
+            float p[UT][2];
+#pragma unroll
+            for (int ti = 0; ti < UT; ++ti)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) p[ti][hf] = ex2(fmaf(sc[ti][nt][hf][n], f[nt][n], -fmaxf(m[nt][n], -3.4e38f)));
+            float* at = mine + C::kSlab * nt + n;
+#pragma unroll 1
+            for (int j = 0; j < NG; ++j, at += C::kRows) {
+              const int jb = JB == 1 ? 0 : j / W, w = JB == 1 ? j : j % W;
+              float ps = 0.f;  // the unit's largest P·s (fmaxf drops what is NaN: places without a key)
+#pragma unroll
+              for (int ti = 0; ti < UT; ++ti)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  ps = fmaxf(ps, p[ti][hf] * bits_to_f<T>(reinterpret_cast<const uint32_t*>(st + ti * Tl::kBytes + Tl::kVp)[(jb * 16 + g + 8 * hf) * W + w] & 0xffffu));
+#pragma unroll
+              for (int off = 4; off <= 16; off <<= 1) ps = fmaxf(ps, __shfl_xor_sync(0xffffffffu, ps, off));
+              // What the row had seen before was at least 2^-3 / its power.  The new power leaves
+              // the largest product so far at 2^-3 or more; above that it is the old one, or the
+              // one that takes the unit's largest scale to 2^10..2^11 (P <= 1).
+              const int e_s = exponent(bits_to_f<T>(__shfl_sync(0xffffffffu, JB == 1 || j < W ? range[0] : range[JB - 1], w) >> 16));
+              const int was = exponent(*at), e_ps = max(exponent(ps), was == kFree ? -127 : e_al - 3 - was);
+              __syncwarp();
+              *at = pow2(e_ps <= -127 ? kFree : min(kFree - 1, max(-3 - e_ps, min(was, 10 - e_s))));  // (the same in the lanes of a column)
             }
           }
+        __syncwarp();
+#pragma unroll
+        for (int jb = 0; jb < JB; ++jb) {
+          float most = 0.f;
+#pragma unroll 1
+          for (int r = 0; r < C::kRows; ++r) most = fmaxf(most, powers[(jb * W + tw) * C::kRows + r]);
+          slimit[jb] = max(1u, f_to_bits<T>(pow2(15 - exponent(most))));
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int n = 0; n < CW; ++n) {
+            l[nt][n] *= al[nt][n];
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+              const float power = mine[j * C::kRows + C::kSlab * nt + n];
+              const float both = al[nt][n] * pow2(max(-127, min(126, exponent(power) - exponent(wt[nt][j][n]))));
+              wt[nt][j][n] = power;
+              zo[nt][j][n] *= al[nt][n];
+#pragma unroll
+              for (int jj = 2 * j; jj < 2 * j + 2; ++jj) {
+                o[jj][nt][n] *= both;
+                o[jj][nt][2 + n] *= both;
+                if constexpr (CW == 1) {
+                  o[jj][nt][1] *= both;
+                  o[jj][nt][3] *= both;
+                }
+              }
+            }
+          }
+      }
     }
-    const float up = pow2(k);
+    fresh = false;
     __syncwarp();
 #pragma unroll
     for (int ti = 0; ti < UT; ++ti) {
-      float pu[NT][2][CW];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -510,7 +621,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
             const float p = ex2(fmaf(sc[ti][nt][hf][n], f[nt][n], -ref));
             sc[ti][nt][hf][n] = p;
             l[nt][n] += p;
-            pu[nt][hf][n] = p * up;
           }
       // ---- values
 #pragma unroll
@@ -539,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
               const float s = bits_to_f<T>(vp[hf][w] & 0xffffu), z = bits_to_f<T>(vp[hf][w] >> 16);
 #pragma unroll
               for (int n = 0; n < CW; ++n) {
-                const float p = sc[ti][nt][hf][n], q = pu[nt][hf][n] * s;
+                const float p = sc[ti][nt][hf][n], q = p * wt[nt][j][n] * s;
                 top[hf][n] = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
                 rest[hf][n] = q - top[hf][n];
                 // A hidden key's z may be NaN and counts as 0; a visible one's is seen, whatever its weight.
@@ -620,14 +730,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][C::kSlab * nt + CW * t + n][0]);
       wgt[n] = m[nt][n] == minus_inf() ? 0.f : ex2(m[nt][n] - M);
     }
-    // o·2^(24 - k), in two steps since k goes down to -122; an odd nibble's also by 1/16.
-    const int half_back = (24 - k) / 2;
-    const float back0 = pow2(half_back), back1 = pow2(24 - k - half_back), odd1 = back1 * 0.0625f;
 #pragma unroll
     for (int j = 0; j < NG; ++j)
 #pragma unroll
       for (int n = 0; n < CW; ++n) {
         const float z = zo[nt][j][n];
+        // o·2^24 / wt, in two steps since that passes 2^127; an odd nibble's also by 1/16.
+        const int back = 24 - exponent(wt[nt][j][n]), half_back = back / 2;
+        const float back0 = pow2(half_back), back1 = pow2(back - half_back), odd1 = back1 * 0.0625f;
         auto sum = [&](int jj, int hf) { return CW == 1 ? o[jj][nt][2 * hf] + o[jj][nt][2 * hf + 1] : o[jj][nt][2 * hf + n]; };
         float4 v;
         v.x = (sum(2 * j, 0) * back0 * back1 + z) * wgt[n];

@@ -669,3 +669,70 @@ def test_queries_up_to_the_largest(D, G, L, scale):
             code, s, z = ref.quantise(as_f64(v)[0], torch.bfloat16)
             ks, vs, low = [held(as_f64(k)[0], "bf16")], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
             check(out, lse, q, ks, vs, low, float(np.float32(used)), True, None, "bf16")
+
+
+def check_groups(out, q, ks, vs, low, scale, causal, dtype, what):
+    """Every element against its own group: eps(T)/2·|o| for its rounding (2^-25 where fp16 has no
+    smaller step) and 2^-15·sum_j w_j·(|z| + s·c), the scores' error (|S| of 20 to 100, 2^-22 and
+    less of them, twice with the sum) on what it is made of, and on nothing larger."""
+    o, _ = ref.cached_attention(as_f64(q), ks, vs, scale, causal, None)
+    tol = torch.finfo(TYPES[dtype]).eps / 2 * np.abs(o) + 2.0**-15 * sizes(q, ks, vs, low, scale, causal, None) + (2.0**-25 if dtype == "f16" else 0)
+    worst = (np.abs(as_f64(out) - o) / np.maximum(tol, 1e-300)).max()
+    assert np.isfinite(as_f64(out)).all() and worst <= 1, f"{what}: {worst:.2f} of the tolerance"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,large,plain", [("bf16", 1e30, 1.0), ("bf16", 1.0, 1e-25), ("f16", 5e3, 2e-3)])
+@pytest.mark.parametrize("D,G,L", [(128, 4, 1), (128, 8, 1), (64, 2, 4), (32, 4, 8), (256, 4, 1), (96, 3, 3)])
+def test_values_that_a_row_does_not_weigh(D, G, L, dtype, large, plain):
+    """A key with large values leaves the rows alone that do not see it (it is the newest, and they
+    are earlier) and those for which its weight is negligible (a score of -100, or -60 in fp16,
+    below the others), wherever it lies; and in one group of 32 values only, or in all."""
+    rng = np.random.default_rng(41)
+    H, page, n, scale = 1, 64, 1400, 1 / math.sqrt(D)
+    below = 100 if dtype == "bf16" else 60
+    for at, group in ((n - 1, False), (3, False), (40, True), (700, False), (n - 1, True), (n - 5, False)):
+        table, pages = make_table(rng, [n], page)
+        cache = dirty_cache(pages, H, page, D, dtype)
+        k, v = (draw_rows(rng, (1, H, n, D), dtype) for _ in range(2))
+        v = (v.double() * plain).to(v.dtype)
+        k[..., 0] = 0
+        k[:, :, at, 0] = -below / scale / 8
+        where = slice(D - 32, D) if group else slice(None)
+        v[:, :, at, where] = (draw_rows(rng, v[:, :, at, where].shape, dtype).double() * large).to(v.dtype)
+        q = draw_rows(rng, (1, G * H, L, D), dtype)
+        q[..., 0] = 8
+        api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints([n]).cuda())
+        out, _ = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda())
+        api.poll_status()
+        code, s, z = ref.quantise(as_f64(v)[0], TYPES[dtype])
+        ks, vs, low = [held(as_f64(k)[0], dtype)], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
+        check_groups(out, q, ks, vs, low, scale, True, dtype, f"key {at}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,large,small", [("bf16", 1.0, 2.0**-26), ("bf16", 2.0**100, 2.0**-100), ("f16", 2.0**13, 2.0**-11)])
+@pytest.mark.parametrize("D,G,L", [(128, 4, 1), (128, 8, 1), (64, 4, 4), (256, 2, 1)])
+def test_groups_far_apart_in_size(D, G, L, dtype, large, small):
+    """Groups of small values beside groups of large ones keep their own precision, also where
+    scores and scales rise along the sequence."""
+    rng = np.random.default_rng(42)
+    H, page, n, scale = 2, 32, 500, 1 / math.sqrt(D)
+    for rising in (False, True):
+        table, pages = make_table(rng, [n], page)
+        cache = dirty_cache(pages, H, page, D, dtype)
+        k, v = (draw_rows(rng, (1, H, n, D), dtype) for _ in range(2))
+        v = v.double() * large
+        v[..., :32] *= small / large
+        if rising:
+            v *= torch.exp2(-torch.arange(n - 1, -1, -1).double() // 100 * 2).view(1, 1, n, 1)
+            k[..., 0] = torch.linspace(-20, 20, n).to(k.dtype)
+        v = v.to(k.dtype)
+        q = draw_rows(rng, (1, G * H, L, D), dtype)
+        q[..., 0] = 1 / scale
+        api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints([n]).cuda())
+        out, _ = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda())
+        api.poll_status()
+        code, s, z = ref.quantise(as_f64(v)[0], TYPES[dtype])
+        ks, vs, low = [held(as_f64(k)[0], dtype)], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
+        check_groups(out, q, ks, vs, low, scale, True, dtype, f"rising {rising}")
