@@ -287,9 +287,9 @@ int sdpa_bwd_noalloc(const void* q, const void* k, const void* v, const void* ou
  *   (axis, batch, row) in position_strides; a stride of 0 broadcasts.  inv_freq [rot/2] fp32,
  *   axes [rot/2] int32 or NULL (axis 0 for all).  Each may overlap inputs, not outputs.
  *   1 <= naxes, rot even, 2 <= rot <= D.
- * Angles are exact to 2^-32 turns plus |position|·(1 + |inv_freq|)·2^-64 turns: they are computed
- * modulo one turn in integers, however far the position.  Rotations run in fp32 and are
- * rounded once.  An axis outside 0..naxes-1 is read as axis 0 and reported by
+ * Angles are computed modulo one turn in integers, however far the position, and are
+ * |position|·(1 + |inv_freq|)·2^-64 turns off at most; the sines and cosines that follow are
+ * fp32, within 5·2^-24 of themselves.  Rotations run in fp32 and are rounded once.  An axis outside 0..naxes-1 is read as axis 0 and reported by
  * sdpa_poll_status (SDPA_ERR_DEVICE_INDEX).  A frequency that is not finite gives NaN.
  */
 typedef struct {

@@ -37,14 +37,17 @@ __device__ __forceinline__ uint64_t turns_per_step(float f) {
   return (bits >> 31) ? 0 - r : r;
 }
 
-// Cosine and sine of a phase in units of 2^-32 turns.  x in [-π/4, π/4] is the distance from
-// the nearest quarter turn; Taylor's series to x^8 and x^9 leave 2.4e-8 and 2e-9 there.
-__device__ __forceinline__ float2 cos_sin(uint32_t phase) {
-  const uint32_t quarter = (phase + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(phase - (quarter << 30)) * 1.4629180792671596e-9f;  // 2π / 2^32
+// Cosine and sine of a phase in units of 2^-64 turns.  x in [-π/4, π/4] is the distance from
+// the nearest quarter turn, 3·2^-24 of itself off (two roundings and the constant's), so that
+// small sines and cosines keep their digits (from the phase's upper 32 bits alone the sine of 2e-6
+// would be 7e-4 of itself off; the wider conversion costs nothing that shows).  Taylor's series to
+// x^9 and x^10 leave 2e-9 and 5e-10; with their last roundings both are within 5·2^-24 of themselves.
+__device__ __forceinline__ float2 cos_sin(uint64_t phase) {
+  const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
+  const float x = (float)(int64_t)(phase - ((uint64_t)quarter << 62)) * 3.4061215800687046e-19f;  // 2π / 2^64
   const float y = x * x;
   const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
-  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
   const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
   return make_float2(((quarter + 1) & 2) ? -a : a, (quarter & 2) ? -b : b);
 }
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(RotaryArgs a, int s
       const unsigned r = row0 + tk, rb = r / (unsigned)a.L;
       const int64_t at = axis * a.pos_axis + rb * a.pos_batch + (r - rb * a.L) * a.pos_row;
       const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.positions)[at] : static_cast<const int32_t*>(a.positions)[at];
-      float2 cs = cos_sin((uint32_t)((step_phase * (uint64_t)pos) >> 32));
+      float2 cs = cos_sin(step_phase * (uint64_t)pos);
       if (!isfinite(f)) cs.x = cs.y = __int_as_float(0x7fffffff);
       tables[tk * half + pair] = cs.x;
       tables[(tokens + tk) * half + pair] = a.inverse ? -cs.y : cs.y;

@@ -281,3 +281,44 @@ def test_captured_forward_and_backward():
     # There and back: the first rounding reaches an element through both of its pair, at most
     # 2^-8·(|y_a| + |y_b|) <= 2^-8·2·max, the second adds 2^-8·max (fp32 terms are 2^-15 of it).
     assert float((back[0].float() - q.float()).abs().max()) <= 3.01 * 2**-8 * float(q.float().abs().max())
+
+
+# The kernel's sines are no longer CUDA's, which the terms at the top of this file name, but
+# series: 5·2^-24 = 3e-7 of themselves.  With four fp32 roundings of products and the sum, 2.4e-7,
+# an output is off by 5.4e-7·(|a| + |b|) at most, which the 1e-6 there covers.
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_sines_and_cosines_keep_their_digits(adjacent, inverse):
+    """Unit pairs (1, 0) and (0, 1) turn into a cosine and a sine without another rounding.  Both
+    are within 6·2^-24 of themselves (x to the nearest quarter turn: rounded to fp32, times a
+    constant that is rounded, rounded, 3·2^-24; series to 2e-9·x^2; two more roundings), small ones
+    too, beside the angle's own |position|·(1 + inv_freq)·2^-64 turns."""
+    from fractions import Fraction
+    pi = Fraction("3.141592653589793238462643383279502884197169399375105820974944592307816406286208998628034825342117067982148086513282306647")
+    rng = np.random.default_rng(13)
+    n = 32
+    inv = np.exp2(rng.uniform(-50, 1, n)).astype(np.float32)
+    inv[0], inv[1], inv[2] = 2e-6, 1.0, np.float32(float(pi / 2))       # the last one is close to quarter turns
+    positions = np.array([0, 1, -1, 2, 3, 355, -710, 103993, 1000003, 2**31 - 1, -2**20])
+    x = torch.zeros(1, 2, len(positions), 2 * n)
+    if adjacent:
+        x[0, 0, :, 0::2], x[0, 1, :, 1::2] = 1, 1
+    else:
+        x[0, 0, :, :n], x[0, 1, :, n:] = 1, 1
+    turn = api.rotary_backward if inverse else api.rotary
+    out, _ = turn(x.cuda(), None, torch.from_numpy(positions).cuda(), torch.from_numpy(inv).cuda(), adjacent=adjacent)
+    api.poll_status()
+    got = as_f64(out)
+    for i, pos in enumerate(positions.tolist()):
+        for p in range(n):
+            a, b = (2 * p, 2 * p + 1) if adjacent else (p, p + n)
+            angle = Fraction(pos) * Fraction(float(inv[p])) * (-1 if inverse else 1)
+            quarter = round(angle / (pi / 2))
+            r = float(angle - quarter * (pi / 2))
+            c, s = [(math.cos(r), math.sin(r)), (-math.sin(r), math.cos(r)), (-math.cos(r), -math.sin(r)), (math.sin(r), -math.cos(r))][quarter % 4]
+            off = abs(pos) * (1 + float(inv[p])) * 2.0**-64 * 2 * math.pi
+            for y, want in ((got[0, 0, i, a], c), (got[0, 0, i, b], s), (got[0, 1, i, a], -s), (got[0, 1, i, b], c)):
+                assert abs(y - want) <= 6 * 2.0**-24 * abs(want) + off, (pos, float(inv[p]), y, want)
