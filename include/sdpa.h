@@ -327,7 +327,8 @@ int sdpa_rotary(const void* q, const void* k, void* q_out, void* k_out, const vo
  *  - A page outside 0..num_pages−1, where a position needs it, or a length below 0 or above
  *    pages_per_seq·page_size is reported by sdpa_poll_status (SDPA_ERR_DEVICE_INDEX) and never
  *    read or written through: such tokens are not written, read as 0 and are hidden from
- *    attention (a length above the table is read as the table's end, one below 0 as 0).
+ *    attention (a length above the table is read as the table's end, one below 0 as 0; a write
+ *    of which no row has a position before the table's end writes nothing of that sequence).
  */
 typedef struct {
   void* data;

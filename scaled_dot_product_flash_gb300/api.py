@@ -376,8 +376,8 @@ def cache_write(cache, k, v, pages, lens, counts=None, stream=None):
     pages int32 [B, n]: the pages of each sequence, in order.  lens int32 [B]: tokens of each
     sequence INCLUDING these: row i of L is position lens[b] - L + i, so a padded batch is
     padded on the left, and rows of negative position are not written.  counts int32 [B]: only
-    the last counts[b] rows are written.  Pages outside the cache are skipped and reported by
-    ``poll_status``.
+    the last counts[b] rows are written.  Pages outside the cache are skipped, a sequence whose
+    rows all lie past its table's end is left as it was, and both are reported by ``poll_status``.
     """
     if stream is not None and stream != torch.cuda.current_stream():
         with torch.cuda.stream(stream):

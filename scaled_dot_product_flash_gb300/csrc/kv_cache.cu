@@ -177,6 +177,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(CacheArgs c) {
   if (!p.any) return;
   const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int count = c.counts ? min(max(c.counts[p.b], 0), c.L) : c.L;
+  // Past the table's end no new row has a place: the tokens that are there stay.
+  const int len = c.lens[p.b], room = c.pages_per_seq * c.page_size;
+  if (len > room && len - count >= room) return;
   const int first = max(0, p.len - count);  // positions first..len-1 are written
   const int v = p.v, hf = p.hf;
   if (p.pos0 + 8 * hf + 8 <= first || p.pos0 + 8 * hf >= p.len) return;

@@ -285,3 +285,30 @@ def test_offsets_past_32_bits():
     api.poll_status()
     check_values(ko, held(as_f64(k), "bf16"), "bf16")
     check_values(vo, held(as_f64(v), "bf16"), "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,lens,counts", [
+    (1, [33, 32, 2**31 - 1], None),                    # one step too long, the last step there is, far too long
+    (3, [35, 32, 40], None), (8, [33, 30, 34], [1, 2, 2]),
+])
+def test_a_loop_that_runs_too_long_loses_nothing(L, lens, counts):
+    """Rows whose positions all lie past the table's end (32 tokens) are not written over the last
+    tokens; the second sequence of the batch, which ends in time, is written."""
+    rng = np.random.default_rng(14)
+    H, D, page = 2, 64, 16
+    table = ints([[0, 3], [1, 4], [2, 5]]).cuda()
+    cache = dirty_cache(6, H, page, D, "bf16")
+    k, v = (draw_rows(rng, (3, H, 32, D), "bf16").cuda() for _ in range(2))
+    api.cache_write(cache, k, v, table, ints([32] * 3).cuda())
+    api.poll_status()
+    before = cache.clone()
+    new = [draw_rows(rng, (3, H, L, D), "bf16").cuda() for _ in range(2)]
+    counts = None if counts is None else ints(counts).cuda()
+    api.cache_write(cache, *new, table, ints(lens).cuda(), counts)
+    with pytest.raises(_lib.SdpaError) as e:
+        api.poll_status()
+    assert e.value.status == INDEX
+    api.cache_write(before, *(x[1:2] for x in new), table[1:2], ints(lens[1:2]).cuda(), None if counts is None else counts[1:2])
+    api.poll_status()
+    assert torch.equal(cache.view(torch.uint8), before.view(torch.uint8))
