@@ -874,6 +874,11 @@ Plan make_plan(const CacheAttnArgs& a) {
   // instead of 9.9 for 8 sequences).
   const int whole = min(1024, (p.nt == 1 ? 65536 : 32768) / a.c.D);
   chunk = a.max_len <= whole ? a.max_len : max(chunk, (int64_t)step);
+  // Partial results take at most 64 MiB, half of L2: beyond that there are more than 2000 blocks of
+  // 16 rows (8000 of 4) anyway, and a workspace that grew with the table would reach gigabytes.
+  const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
+  const int64_t most = max((int64_t)1, ((int64_t)64 << 20) / partial);
+  chunk = max(chunk, (a.max_len + most - 1) / most);
   p.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
   p.splits = (a.max_len + p.chunk - 1) / p.chunk;
   return p;

@@ -736,3 +736,31 @@ def test_groups_far_apart_in_size(D, G, L, dtype, large, small):
         code, s, z = ref.quantise(as_f64(v)[0], TYPES[dtype])
         ks, vs, low = [held(as_f64(k)[0], dtype)], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
         check_groups(out, q, ks, vs, low, scale, True, dtype, f"rising {rising}")
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,L,D", [(1, 32, 8, 4096, 128), (1, 32, 8, 512, 128), (1, 4, 1, 1, 128), (4096, 32, 8, 1, 64), (64, 64, 8, 16, 256), (2, 16, 1, 1024, 32)])
+@pytest.mark.parametrize("tokens", [2048, 131072, 1 << 30])
+def test_the_workspace_stays_small(B, Hq, Hkv, L, D, tokens):
+    """Partial results of all rows take 64 MiB at most, however wide the table is."""
+    build.build()
+    page = 16384 if tokens > 131072 else 128
+    c = _lib.Cache(*dict(GOOD, num_pages=4, page_size=page, Hkv=Hkv, D=D, pages_stride=tokens // page, pages_per_seq=tokens // page).values())
+    assert _lib.sdpa_cache_attn_workspace_size(c, B, Hq, L, 0) <= 64 << 20
+
+
+@pytest.mark.gpu
+def test_many_rows_and_a_wide_table():
+    """Rows enough that the workspace's bound sets the chunks, on a table far wider than the
+    sequences: one of three chunks, an empty one, and one of a few tokens."""
+    rng = np.random.default_rng(44)
+    lens, Hq, L, D, page = [20000, 0, 40], 16, 700, 32, 1024
+    cache, table, ks, vs, low = fill(rng, lens, 1, D, page, "bf16", width=128)
+    q = draw_rows(rng, (3, Hq, L, D), "bf16")
+    c = api._cache(cache, table.cuda(), ints(lens).cuda(), 3)
+    assert 32 << 20 < _lib.sdpa_cache_attn_workspace_size(c, 3, Hq, L, 0) <= 64 << 20
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True)
+    api.poll_status()
+    rows = [0, 1, 350, 660, 661, 698, 699]                              # 660: the first that sees one of 40
+    for i in rows:                                                      # a row is the last one of a sequence cut behind it
+        seen = [[x[:, :max(0, n - L + i + 1)] for x, n in zip(xs, lens)] for xs in (ks, vs, low)]
+        check(out[:, :, i:i + 1], lse[:, :, i:i + 1], q[:, :, i:i + 1], *seen, 1 / math.sqrt(D), True, None, "bf16")
