@@ -764,3 +764,16 @@ def test_many_rows_and_a_wide_table():
     for i in rows:                                                      # a row is the last one of a sequence cut behind it
         seen = [[x[:, :max(0, n - L + i + 1)] for x, n in zip(xs, lens)] for xs in (ks, vs, low)]
         check(out[:, :, i:i + 1], lse[:, :, i:i + 1], q[:, :, i:i + 1], *seen, 1 / math.sqrt(D), True, None, "bf16")
+
+
+@pytest.mark.gpu
+def test_a_bound_past_32_bits_is_no_bound():
+    """max_len beyond every length, as large as a Python integer may be, changes nothing."""
+    rng = np.random.default_rng(46)
+    cache, table, *_ = fill(rng, [90, 17], 2, 64, 16, "bf16")
+    q = draw_rows(rng, (2, 4, 1, 64), "bf16").cuda()
+    args = (q, cache, table.cuda(), ints([90, 17]).cuda())
+    want, _ = api.cache_attention(*args)
+    for most in (2**31 - 1, 2**31, 2**32 + 1, 2**63):
+        assert torch.equal(api.cache_attention(*args, max_len=most)[0], want)
+    api.poll_status()
