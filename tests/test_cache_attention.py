@@ -777,3 +777,23 @@ def test_a_bound_past_32_bits_is_no_bound():
     for most in (2**31 - 1, 2**31, 2**32 + 1, 2**63):
         assert torch.equal(api.cache_attention(*args, max_len=most)[0], want)
     api.poll_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("G,L", [(4, 1), (8, 1), (4, 4)])
+@pytest.mark.parametrize("D", [32, 64, 96, 256])
+@pytest.mark.parametrize("lens", [[3000, 700, 0, 1025], [20000, 5]])
+def test_sequences_of_several_chunks(lens, D, G, L, dtype):
+    """Joins of a few chunks by four warps and of many by sixteen, with the head dims whose rows do
+    and do not divide a block's threads, in every form."""
+    rng = np.random.default_rng(45)
+    cache, table, ks, vs, low = fill(rng, lens, 1, D, 64, dtype)
+    q = draw_rows(rng, (len(lens), G, L, D), dtype)
+    sink = torch.from_numpy(rng.standard_normal(G).astype(np.float32)).cuda()
+    c = api._cache(cache, table.cuda(), ints(lens).cuda(), len(lens))
+    splits = _lib.sdpa_cache_attn_workspace_size(c, len(lens), G, L, 0) // (len(lens) * G * L * (D + 2) * 4)
+    assert splits > 16 if max(lens) > 3000 else 1 < splits <= 16
+    out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True, sinks=sink)
+    api.poll_status()
+    check(out, lse, q, ks, vs, low, 1 / math.sqrt(D), True, sink.cpu().numpy(), dtype)
