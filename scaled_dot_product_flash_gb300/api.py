@@ -452,7 +452,7 @@ def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
         raise ValueError("lse must be a contiguous fp32 [B, Hq, L] tensor")
     if sinks is not None:
         _check_sinks("sinks", sinks, Hq)
-    max_len = 0 if max_len is None else min(int(max_len), 2**31 - 1)  # a C int
+    max_len = 0 if max_len is None else max(0, min(int(max_len), 2**31 - 1))  # a C int
     need = _lib.sdpa_cache_attn_workspace_size(c, B, Hq, L, max_len)
     if workspace is None and need:
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8)

@@ -80,17 +80,8 @@ struct Cfg {
   static constexpr int kSmem = kPowers + kWarps * Tl::NG * kRows * 4;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Transposes an 8 x 8 matrix of 16-bit elements held two a lane.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
+using tc::ex2;
+
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
@@ -121,20 +112,6 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127 (0 for -127)
 __device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x >= 0: floor(log2 x), -127 below 2^-126
 constexpr int kFree = 119;  // exponent of a power of two that nothing has fixed yet
-
-template <int W>
-__device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* p) {
-  if constexpr (W == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-  } else if constexpr (W == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r[0] = v.x; r[1] = v.y;
-  } else {
-#pragma unroll
-    for (int w = 0; w < W; ++w) r[w] = reinterpret_cast<const uint32_t*>(p)[w];
-  }
-}
 
 __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc::smem_u32(dst)),
@@ -495,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           const float m_old = m[nt][n], m_new = fmaf(top, f[nt][n], -m_old) > 0.f ? __fmaf_ru(top, f[nt][n], 8.f) : m_old;
           al[nt][n] = m_new == m_old ? 1.f : ex2(m_old - m_new);
           m[nt][n] = m_new;
-          plain = plain && m_new > minus_inf();
+          plain = plain && fabsf(m_new) < 0x1p20f;
         }
       // Largest scale (high half) and the complement of the smallest one of group 4·jb + t.
       uint32_t range[JB];
@@ -516,14 +493,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         plain = plain && exponent(bits_to_f<T>(range[jb] >> 16)) - exponent(bits_to_f<T>(~range[jb] & 0xffffu)) <= 4;
       }
       if (__all_sync(0xffffffffu, plain)) {
-        // A first unit of the usual kind: every row sees a key, so that its largest P is 2^-8, and
-        // no scale is under 2^-5 of its group's largest.  The power that takes that one to
-        // 2^10..2^11 then has a product P·s of at least 2^-3 in every row.
+        // A first unit of the usual kind: every row sees a key, so that its largest P is 2^-8 (less
+        // where scores are so large that m is rounded), and no scale is under 2^-5 of its group's
+        // largest.  The power that takes that one to 2^10..2^11 then has a product P·s of at least
+        // 2^-3 in every row.
         int now[JB];
 #pragma unroll
         for (int jb = 0; jb < JB; ++jb) {
           now[jb] = min(kFree - 1, 10 - exponent(bits_to_f<T>(range[jb] >> 16)));
-          slimit[jb] = max(1u, f_to_bits<T>(pow2(15 - now[jb])));
+          slimit[jb] = max(1u, f_to_bits<T>(pow2(min(127, 15 - now[jb]))));
         }
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
@@ -581,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
           float most = 0.f;
 #pragma unroll 1
           for (int r = 0; r < C::kRows; ++r) most = fmaxf(most, powers[(jb * W + tw) * C::kRows + r]);
-          slimit[jb] = max(1u, f_to_bits<T>(pow2(15 - exponent(most))));
+          slimit[jb] = max(1u, f_to_bits<T>(pow2(min(127, 15 - exponent(most)))));
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

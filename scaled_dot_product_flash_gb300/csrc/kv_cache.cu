@@ -22,12 +22,6 @@ namespace {
 
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
 // Eight 16-bit elements as fp32.
 template <typename T>
 __device__ __forceinline__ void unpack8(float (&x)[8], const uint4& w) {
@@ -129,19 +123,6 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t* r) {
   else {
 #pragma unroll
     for (int w = 0; w < W; ++w) reinterpret_cast<uint32_t*>(p)[w] = r[w];
-  }
-}
-template <int W>
-__device__ __forceinline__ void load_words(uint32_t* r, const uint8_t* p) {
-  if constexpr (W == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-  } else if constexpr (W == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r[0] = v.x; r[1] = v.y;
-  } else {
-#pragma unroll
-    for (int w = 0; w < W; ++w) r[w] = reinterpret_cast<const uint32_t*>(p)[w];
   }
 }
 

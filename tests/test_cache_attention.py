@@ -774,7 +774,7 @@ def test_a_bound_past_32_bits_is_no_bound():
     q = draw_rows(rng, (2, 4, 1, 64), "bf16").cuda()
     args = (q, cache, table.cuda(), ints([90, 17]).cuda())
     want, _ = api.cache_attention(*args)
-    for most in (2**31 - 1, 2**31, 2**32 + 1, 2**63):
+    for most in (2**31 - 1, 2**31, 2**32 + 1, 2**63, 5 - 2**32):         # 0 and less: the table's end
         assert torch.equal(api.cache_attention(*args, max_len=most)[0], want)
     api.poll_status()
 
@@ -797,3 +797,26 @@ def test_sequences_of_several_chunks(lens, D, G, L, dtype):
     out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints(lens).cuda(), need_lse=True, sinks=sink)
     api.poll_status()
     check(out, lse, q, ks, vs, low, 1 / math.sqrt(D), True, sink.cpu().numpy(), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G,L", [(64, 4, 1), (128, 8, 1), (64, 8, 2)])
+def test_scores_that_fp32_holds_coarsely(D, G, L):
+    """Scores of 2^20 to 2^28, where one step of fp32 (in base 2) is up to 32: the largest key alone has weight,
+    whatever a row's reference is rounded to."""
+    rng = np.random.default_rng(47)
+    n, page = 200, 16
+    table, pages = make_table(rng, [n], page)
+    cache = dirty_cache(pages, 1, page, D, "bf16")
+    v = draw_rows(rng, (1, 1, n, D), "bf16")
+    size = torch.from_numpy(rng.uniform(0.25, 0.5, (1, 1, n, 1))).to(v.dtype)
+    size[0, 0, [3, 77, 190]] = 1.0                                     # ties, exactly
+    api.cache_write(cache, size.expand(1, 1, n, D).contiguous().cuda(), v.cuda(), table.cuda(), ints([n]).cuda())
+    code, s, z = ref.quantise(as_f64(v)[0], torch.bfloat16)
+    ks, vs, low = [as_f64(size.expand(1, 1, n, D))[0]], [ref.values(code, s, z)], [ref.values(code, s, np.zeros_like(z))]
+    for power in (20, 24, 28):
+        q = torch.full((1, G * 1, L, D), 1.0) * 2.0**power * torch.from_numpy(rng.uniform(0.5, 1, (1, G, L, 1)))
+        q = q.to(v.dtype)
+        out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda(), scale=1 / D, need_lse=True, is_causal=False)
+        api.poll_status()
+        check(out, lse, q, ks, vs, low, 1 / D, False, None, "bf16")
