@@ -12,23 +12,24 @@
 //    warp streams its tiles into a shared-memory ring of its own with plain bulk copies (one
 //    per tile, issued a few units ahead, no tensor map, no block barrier) and reads fragments
 //    with 16-byte loads.
-//  - Codes are not converted.  A nibble masked in place is a subnormal fp16 number, code·2^-24
-//    or, one nibble higher, 16·code·2^-24, which the tensor cores multiply exactly: one AND
-//    gives two operands (5 instructions for 8 codes).  The factors 16 and 2^-24 are undone in
-//    the output and in fp32 scales.
-//    Sums over such small operands keep fewer low bits, the fewer the lower the nibble.  In the
-//    scores that would show (at one token off by 8.7e-7 rms in fp16, 3.3e-7 in bf16), so every
-//    key nibble is moved to the higher place, 2 shifts more a word (0.9e-7 and 0.6e-7).
+//  - Key codes are not converted.  A nibble masked in place is a subnormal fp16 number, 16·code·2^-24
+//    in bits 4 to 7, which the tensor cores multiply exactly; the factors are undone in fp32 scales.
+//    (In bits 0 to 3, two shifts a word less, sums keep fewer low bits: at one token scores were
+//    off by 8.7e-7 rms in fp16 and 3.3e-7 in bf16, so 0.9e-7 and 0.6e-7.)
 //  - The product is transposed, S^T = K·Q^T and O^T = V^T·P^T (m16n8k16), so that the cache is
 //    the 16-row operand and 8 query rows fill the other one.
 //  - Scales stay outside the products: S = sum_j s_j·(c_j·q_j) + sum_j z_j·sum(q_j) over the
 //    groups j, the first in fp32 FMAs over one accumulator a group, the second as one MMA in
-//    the element type whose q sums are split in three so that nothing is lost.  For the values
-//    the probabilities take the scale; P·s, times a power of two, enters as two fp16 numbers, its
-//    leading 11 bits and what they leave, 2^-21 relative in all and 2^-22 of the largest P·s.
-//    One fp16 number would be cheaper (32 sequences 41.5 us) but is off by 2^-11 of s·c, several
-//    2^-12 of an output where s·c and z nearly cancel, so that a tenth of the bf16 outputs were
-//    rounded the other way.  P·z is summed in fp32 FMAs.  So nothing is rounded to fewer bits than
+//    the element type whose q sums are split in three so that nothing is lost.
+//  - For the values the probabilities take the scale: O = sum P·s·(c - 8) + sum P·(z + 8·s), the
+//    second in fp32 FMAs.  The 8 costs an fp16 operation for two codes (one sequence 35.6 us
+//    without, 39.5 with): an MMA cuts off what falls below the last bit of its sum, and sums of
+//    codes of 0 to 15 grow to hundreds of times an output, so that a seventh of the bf16 outputs
+//    of 131072 tokens were rounded the other way; now 3 in 10000, fewer than with fp32 matrix
+//    products.  (A second MMA that takes 8 off, 37.7 us, leaves 2 in 100.)
+//    P·s, times a power of two, enters as two fp16 numbers, its leading 11 bits and what they
+//    leave, 2^-21 relative in all and 2^-22 of the largest P·s; the first alone, cheaper by 5 us in
+//    the drafts below, would change one output in ten.  So nothing is rounded to fewer bits than
 //    fp32 sums show but the output.
 //  - fp16 has 40 binades, P·s in bf16 over 250.  So every row has a power of two for each group
 //    of values, chosen from products P·s that the row has really seen: a key that it does not
@@ -108,6 +109,18 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The codes in two of a word's nibbles, less 8, as fp16: the nibble under the exponent of 1024 is
+// 1024 + c, or, one place higher, 1024 + 16·c.
+__device__ __forceinline__ uint32_t low_codes(uint32_t x) {
+  const uint32_t b = (x & 0x000f000fu) | 0x64006400u;
+  const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&b), __float2half2_rn(-1032.f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t x) {
+  const uint32_t b = (x & 0x00f000f0u) | 0x64006400u;
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&b), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127 (0 for -127)
 __device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x >= 0: floor(log2 x), -127 below 2^-126
@@ -307,8 +320,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
   }
   const int seen = a.causal ? len - c.L + 1 : len;  // every row sees the positions below this
 
-  float o[2 * NG][NT][4];  // O^T, times wt·2^-24
-  float zo[NT][NG][CW];    // this lane's keys' P·z
+  float o[2 * NG][NT][4];  // wt·sum of P·s·(c - 8)
+  float zo[NT][NG][CW];    // this lane's keys' P·(z + 8·s)
   float m[NT][CW], l[NT][CW];  // reference (P <= 1), sum
   float wt[NT][NG][CW];    // P·s enters the MMA times this power of two, at most 2^15
 #pragma unroll
@@ -617,14 +630,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
         for (int w = 0; w < W; ++w) {
           const int j = jb * W + w;
           const uint32_t x0 = vw[0][w], x1 = vw[1][w], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u, a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
-          const uint32_t c0 = y0 & 0x000f000fu, c1 = y0 & 0x00f000f0u, c2 = y1 & 0x000f000fu, c3 = y1 & 0x00f000f0u;
+          const uint32_t a0 = low_codes(x0), a1 = high_codes(x0), a2 = low_codes(x1), a3 = high_codes(x1);
+          const uint32_t c0 = low_codes(y0), c1 = high_codes(y0), c2 = low_codes(y1), c3 = high_codes(y1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float top[2][CW], rest[2][CW];  // P·s: its leading 11 bits, and the rest
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const float s = bits_to_f<T>(vp[hf][w] & 0xffffu), z = bits_to_f<T>(vp[hf][w] >> 16);
+              const float s = bits_to_f<T>(vp[hf][w] & 0xffffu), z = fmaf(8.f, s, bits_to_f<T>(vp[hf][w] >> 16));
 #pragma unroll
               for (int n = 0; n < CW; ++n) {
                 const float p = sc[ti][nt][hf][n], q = p * wt[nt][j][n] * s;
@@ -713,15 +726,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, CW>::kWarps * 32, Cfg<D, NT, CW>::k
 #pragma unroll
       for (int n = 0; n < CW; ++n) {
         const float z = zo[nt][j][n];
-        // o·2^24 / wt, in two steps since that passes 2^127; an odd nibble's also by 1/16.
-        const int back = 24 - exponent(wt[nt][j][n]), half_back = back / 2;
-        const float back0 = pow2(half_back), back1 = pow2(back - half_back), odd1 = back1 * 0.0625f;
+        const float back = pow2(-exponent(wt[nt][j][n]));
         auto sum = [&](int jj, int hf) { return CW == 1 ? o[jj][nt][2 * hf] + o[jj][nt][2 * hf + 1] : o[jj][nt][2 * hf + n]; };
         float4 v;
-        v.x = (sum(2 * j, 0) * back0 * back1 + z) * wgt[n];
-        v.y = (sum(2 * j, 1) * back0 * odd1 + z) * wgt[n];
-        v.z = (sum(2 * j + 1, 0) * back0 * back1 + z) * wgt[n];
-        v.w = (sum(2 * j + 1, 1) * back0 * odd1 + z) * wgt[n];
+        v.x = fmaf(sum(2 * j, 0), back, z) * wgt[n];
+        v.y = fmaf(sum(2 * j, 1), back, z) * wgt[n];
+        v.z = fmaf(sum(2 * j + 1, 0), back, z) * wgt[n];
+        v.w = fmaf(sum(2 * j + 1, 1), back, z) * wgt[n];
         *reinterpret_cast<float4*>(red + (warp * C::kSlab + CW * t + n) * (D + 4) + 32 * j + 4 * g) = v;
       }
     __syncthreads();

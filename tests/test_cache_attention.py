@@ -820,3 +820,32 @@ def test_scores_that_fp32_holds_coarsely(D, G, L):
         out, lse = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda(), scale=1 / D, need_lse=True, is_causal=False)
         api.poll_status()
         check(out, lse, q, ks, vs, low, 1 / D, False, None, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,L", [(4, 1), (8, 1), (4, 4)])
+def test_sums_over_long_sequences(G, L):
+    """100000 tokens, whose outputs are some 300 times smaller than one value.  A chain of 64 MMAs,
+    each of which may cut off 2^-23 of its sum, is off by 2^-17 of that sum at most, and the sums are
+    no larger than the outputs' random part r = sqrt(sum_j w_j²·(s·(c - 8))²), a few times, and the
+    output itself: off = 2^-17·(3·r + |o|).  Odds as in ``test_outputs_are_rounded_once``.  (Codes
+    of 0 to 15 add up to 500 times an output, and change one in seven.)"""
+    rng = np.random.default_rng(48)
+    n, D = 100000, 32
+    table, pages = make_table(rng, [n], 1024)
+    cache = dirty_cache(pages, 1, 1024, D, "bf16")
+    k, v = (draw_rows(rng, (1, 1, n, D), "bf16") for _ in range(2))
+    api.cache_write(cache, k.cuda(), v.cuda(), table.cuda(), ints([n]).cuda())
+    q = draw_rows(rng, (1, G, L, D), "bf16")
+    out, _ = api.cache_attention(q.cuda(), cache, table.cuda(), ints([n]).cuda(), is_causal=False)
+    api.poll_status()
+    code, s, _ = ref.quantise(as_f64(v)[0, 0], torch.bfloat16)
+    weight = as_f64(q)[0].reshape(-1, D) @ held(as_f64(k)[0, 0], "bf16").T / math.sqrt(D)
+    weight = np.exp(weight - weight.max(1, keepdims=True))
+    weight /= weight.sum(1, keepdims=True)
+    o = weight @ held(as_f64(v)[0, 0], "bf16")
+    r = np.sqrt(weight**2 @ (s * (code - 8.0))**2)
+    step = torch.finfo(torch.bfloat16).eps * np.exp2(np.floor(np.log2(np.abs(o))))
+    odds = np.minimum(1, 2.0**-16 * (3 * r + np.abs(o)) / step).sum()
+    differ = (as_f64(out)[0].reshape(-1, D) != ref.rounded(o, torch.bfloat16)).sum()
+    assert differ <= odds + 4 * math.sqrt(odds) + 1, f"{differ} of {o.size} differ, {odds:.1f} expected at most"
