@@ -38,12 +38,12 @@
 //    passes what the powers in use allow, a vote a unit.
 //
 // Measured (bf16, 32 query and 8 KV heads, D = 128, a call replayed from a graph): one sequence of
-// 131072 tokens 33.8 us, 168 MB, 5.0 TB/s (kernel alone 33.0 us under ncu with a cold L2, 65% of
-// DRAM's peak, issue slots 52%, ALU 51%; 31 us with the arithmetic of the units left out: what
-// remains above the copy rate's 24.8 us is the first copies' chain of lookups, some 2.5 us, and the
-// join).  32 sequences of 256 to 8192 tokens 41.6 us, 174 MB, 4.2 TB/s.  Eight queries each of 4
-// sequences of 2048 to 8192 (32 rows a KV head, 27 MB) 31.5 us: bound by instructions, a chunk
-// of 16 rows takes 3300 cycles for 32 keys on the SM's 8 warps.
+// 131072 tokens 39.5 us, 168 MB, 4.2 TB/s (kernel alone 37.9 us under ncu with a cold L2, 57% of
+// DRAM's peak, issue slots 62%, ALU 59%: bound by its instructions on 12 warps an SM; 31 us with
+// the arithmetic of the units left out, of which the first copies' chain of lookups takes some 2.5).
+// 32 sequences of 256 to 8192 tokens 49.2 us, 174 MB, 3.5 TB/s.  Eight queries each of 4 sequences of
+// 2048 to 8192 (32 rows a KV head, 27 MB) 40.1 us: issue slots 46%, ALU 34%, tensor pipe 24%, so bound
+// by the latency of dependent instructions, with two warps a scheduler at 255 registers.
 #include <atomic>
 
 #include "cache.h"
@@ -63,11 +63,11 @@ struct Cfg {
   static constexpr int UT = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // tiles a unit
   static constexpr int kUnit = UT * kTile;                    // tokens a unit
   // Warps a block, and blocks an SM.  The narrow form ran best on 12 warps of up to 168 registers
-  // an SM (131072 tokens, D = 128: 37.4 us; 8 warps of 222 registers 36.2, but 49.4 with chunks
-  // that keep fewer blocks busy; 16 warps of 128 registers, which spill, 41.0; 20 of 96, 54.1).
+  // an SM (131072 tokens, D = 128: 39.5 us; 8 warps of 182 registers 42.7; 16 warps of 128
+  // registers, which spill, 43.8; 20 of 96, 55.8).
   static constexpr int kWarps = CW == 1 ? 4 : 8;
   static constexpr int kBlocks = CW == 1 ? 3 : NT == 1 && D <= 128 ? 2 : 1;
-  static constexpr int kStages = 2;  // a third one changed nothing (37.5 us)
+  static constexpr int kStages = 2;  // a third one: 40.0 us, and one block of the 8-row form instead of two
   static constexpr int kUnitBytes = UT * Tl::kBytes;
   static constexpr int kSlab = 4 * CW;       // rows of a row tile
   static constexpr int kRows = kSlab * NT;
@@ -838,8 +838,8 @@ struct Plan {
 Plan make_plan(const CacheAttnArgs& a) {
   Plan p;
   const int R = a.G * a.c.L;
-  // The forms, both sides of each border measured (131072 tokens, 4 rows): plain 43.4 us, narrow
-  // 37.4; 8192 tokens, 32 rows: tiles of 8 rows 36.5 us, of 16 31.4, of 32 (which spill) 49.1.
+  // The forms, both sides of each border measured (131072 tokens, 4 rows): plain 51.9 us, narrow
+  // 39.6; 8192 tokens, 32 rows: tiles of 8 rows 44.1 us, of 16 40.1, of 32 (which spill) 60.9.
   p.cw = R <= 4 ? 1 : 2;
   p.nt = R <= 8 ? 1 : 2;
   p.rows = 4 * p.cw * p.nt;
@@ -848,19 +848,19 @@ Plan make_plan(const CacheAttnArgs& a) {
   const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (p.cw == 1 ? 3 : p.nt == 1 && a.c.D <= 128 ? 2 : 1);
   const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * p.row_tiles;
   // Few pairs: one wave of blocks, whatever the chunk.  Many: chunks short enough that sequences of
-  // unequal length share the SMs (32 of 256..8192 tokens: 2048 tokens 45.5 us, 1536 41.9, 1024 42.3,
-  // 512 46.9; 32 rows: 36.2, 31.4, 35.0, 41.8).  Equal shares of all tokens, cut on the device, ran
-  // slower (49.5 us, and 36.9 instead of 33.8 for one sequence): finding a share costs 1.7 us, each
-  // further sequence in it about 4.
+  // unequal length share the SMs (32 of 256..8192 tokens: 2048 tokens 53.4 us, 1536 49.2, 1024 49.0,
+  // 512 52.5; 32 rows: 47.9, 40.1, 43.2, 48.3).  Equal shares of all tokens, cut on the device, ran
+  // slower (with the units at 41.9 and 33.8 us: 49.5, and 36.9 for one sequence): finding a share
+  // costs 1.7 us, each further sequence in it about 4.
   const int64_t want = max((int64_t)1, slots / pairs);
   int64_t chunk = (a.max_len + want - 1) / want;
   if (pairs * 4 > slots) chunk = min(chunk, (int64_t)1536);
   // A second chunk costs the join, some 1.5 us, whatever it saves: none while one block's warps read
   // the sequence in less.  One call of 8 KV heads, whole against chunks of 256: D = 128, 512 tokens,
-  // 5.8 us, 6.8, 1024 tokens 8.6, 6.9; D = 64, 1024 tokens 6.2, 6.4; D = 256, 512 tokens 10.8, 9.0;
-  // 32 rows (D = 64) 512 tokens 7.1, 7.6, 1024 tokens 9.2, 7.6.  Longer ones: chunks of at least
-  // 256 (1024 to 4096 tokens, D = 128: 6.9 to 7.7 us; of 512 8.2 to 8.5, of 128 6.6 to 7.7, but 11.0
-  // instead of 9.9 for 8 sequences).
+  // 6.5 us, 7.1, 1024 tokens 10.1, 7.1; D = 64, 1024 tokens 6.9, 6.5; D = 256, 512 tokens 13.0, 10.1;
+  // 32 rows (D = 64) 512 tokens 7.6, 8.7, 1024 tokens 10.2, 9.1.  Longer ones: chunks of at least
+  // 256 (1024 to 4096 tokens, D = 128: 7.1 to 8.0 us; of 512 8.8 to 9.3, of 128 6.8 to 7.8, but 10.0
+  // instead of 9.4 for 32 rows of 1024).
   const int whole = min(1024, (p.nt == 1 ? 65536 : 32768) / a.c.D);
   chunk = a.max_len <= whole ? a.max_len : max(chunk, (int64_t)step);
   // Partial results take at most 64 MiB, half of L2: beyond that there are more than 2000 blocks of
@@ -917,7 +917,7 @@ cudaError_t attn_t(const CacheAttnArgs& a, bool join, cudaStream_t s) {
     }
   }
   // A row of few chunks is joined by four warps; with many, 16 warps read them side by side
-  // (131072 tokens in 57 chunks: 36.6 us a call with 4 warps, 34.1 with 16; 6 chunks: 41.9, 46.2).
+  // (131072 tokens in 57 chunks: 42.0 us a call with 4 warps, 39.6 with 16; 6 chunks: 49.2, 54.7).
   return p.splits > 16 ? join_t<T, D, 512>(a, p, s) : join_t<T, D, 128>(a, p, s);
 }
 

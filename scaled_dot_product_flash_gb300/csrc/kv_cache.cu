@@ -10,9 +10,10 @@
 //
 // Bound: HBM for prompts (4 bytes in and 1.25 out for an element of K and of V, or the
 // reverse), launch latency for single tokens.  Measured (bf16, 8 heads, D = 128): two prompts of
-// 4096 tokens written in 15.5 us under ncu, 44 MB, 2.9 TB/s: issue slots 68%, ALU 51%, about 19
-// instructions an element and lane; the last 8192 rows of four prefixes of 2048 to 8192 read back in
-// 26.3 us from a graph, 160 MB, 6.1 TB/s, 0.9 of the copy rate.  A thread an 8-element piece with 2-byte stores of the value halves took 31 us and
+// 4096 tokens written in 15.7 us under ncu, 44 MB, 2.8 TB/s: a warp loads its half tile, waits and
+// then has some 19 instructions an element and lane (issue slots 70%, ALU 52%, warps active 52%, no
+// load ahead of the arithmetic); the last 8192 rows of four prefixes of 2048 to 8192 read back in
+// 26.7 us from a graph, 160 MB, 6.0 TB/s, 0.88 of the copy rate.  A thread an 8-element piece with 2-byte stores of the value halves took 31 us and
 // 41 us.  Half a tile of keys or of values a warp: a whole tile a warp was as fast on prompts, but
 // one token's write and read took 15.2 us instead of 7.3, on one warp's chain of 16 groups.
 #include "cache.h"

@@ -11,8 +11,8 @@
 // compute their sines and cosines once, into shared memory, while the first heads' loads are
 // on their way; then a thread keeps those of VP pairs of one token in registers and turns that
 // token's heads hg, hg + HG, ... in 16-byte pieces.
-// Measured (bf16, B = 2, 32 + 8 heads, L = 4096, D = 128; 168 MB): 31.0 us a call from a graph,
-// 5.4 TB/s, 0.80 of the copy rate; waiting on loads (long scoreboard 8.8 of 14 cycles a warp and
+// Measured (bf16, B = 2, 32 + 8 heads, L = 4096, D = 128; 168 MB): 31.3 us a call from a graph,
+// 5.4 TB/s, 0.79 of the copy rate; waiting on loads (long scoreboard 8.8 of 14 cycles a warp and
 // instruction).  With the sines computed by every thread for 8 heads (64-bit divisions, CUDA's
 // sincospif) it took 35 to 50 us; fp32 (B = 8, 8 + 8 heads, L = 577, D = 64) 7.5 us, 5.0 TB/s.
 #include "cache.h"
