@@ -367,11 +367,12 @@ int sdpa_cache_read(const sdpa_cache_t* cache, void* k, void* v, const sdpa_layo
  * those of q and out.  is_causal: SDPA_CAUSAL_NONE (every query sees all lens[b] tokens) or
  * SDPA_CAUSAL_BOTTOM_RIGHT (query i sees positions up to lens[b] − Lq + i, its own);
  * SDPA_CAUSAL_TOP_LEFT is SDPA_ERR_UNSUPPORTED.  A row that sees nothing gets out = 0 and
- * lse = −inf (with a sink, the sink's).
+ * lse = −inf (with a sink, the sink's).  Sums are as exact as fp32 ones, whatever the sizes of
+ * queries and values; scaled scores stay below 2^28.
  * max_len bounds lens (<= 0: the table's end) and fixes the launch; longer sequences are
  * reported and read as max_len long, from their first token.
- * workspace as in sdpa_bwd, of sdpa_cache_attn_workspace_size bytes (may be 0, then it may
- * be NULL); that size depends on the current device and needs no GPU memory.
+ * workspace as in sdpa_bwd, of sdpa_cache_attn_workspace_size bytes (64 MiB at most; may be 0,
+ * then it may be NULL); that size depends on the current device and needs no GPU memory.
  */
 size_t sdpa_cache_attn_workspace_size(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len);
 int sdpa_cache_attn(const sdpa_cache_t* cache, const void* q, void* out, float* lse,
