@@ -381,6 +381,73 @@ int sdpa_cache_attn(const sdpa_cache_t* cache, const void* q, void* out, float* 
                     size_t workspace_bytes, void* stream);
 
 /*
+ * A paged cache of keys and values in 16 bits.  Its memory is an array
+ * [num_pages][2][Hkv][page_size][D] of `dtype`, keys before values: position j of sequence b
+ * lies in page pages[b][j / page_size], at place j % page_size.  These calls take the
+ * sdpa_cache_t of the 4-bit cache, with data in this layout, and follow its rules: dtype, D,
+ * page_size, limits (but B·Hkv·L at most 2^29), rows that are the LAST ones of each sequence,
+ * what becomes of pages and lengths out of range.  counts (device int32 [B], 4-byte aligned, or
+ * NULL for L each): only the last counts[b] rows of sequence b are real; a count is taken
+ * within 0..L.
+ */
+size_t sdpa_paged_page_bytes(int page_size, int Hkv, int D, int dtype); /* 4·Hkv·page_size·D, or 0 */
+
+/*
+ * Copies the real rows of k and v [B,Hkv,L,D] into the cache (layouts[0] and [1] are theirs).
+ * No other token changes; two tokens of one call must not share a place.
+ */
+int sdpa_paged_write(const sdpa_cache_t* cache, const void* k, const void* v,
+                     const sdpa_layout_t* layouts, const int* counts, int B, int L, void* stream);
+
+/*
+ * Attention of q [B,Hq,Lq,D] over the cached keys and values, as sdpa_cache_attn has it (sinks,
+ * lse, is_causal, max_len, workspace), for one token or a few a sequence and for chunks of
+ * thousands.  Rows that are not real see nothing, whatever is in them.  A token that a row does not
+ * see leaves no trace in it, whatever its key and value; a NaN in one that it sees makes the row's
+ * outputs NaN.
+ */
+size_t sdpa_paged_attn_workspace_size(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len);
+int sdpa_paged_attn(const sdpa_cache_t* cache, const void* q, void* out, float* lse,
+                    const float* sinks, const sdpa_layout_t* layouts, const int* counts, int B, int Hq,
+                    int Lq, float scale, int is_causal, int max_len, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * The attention weight that cached tokens gather: for each token j < lens[b] and KV head g,
+ *     weights[b][g][j] = old + Σ over the real rows i that see j and the query heads h of g of
+ *                        exp(scale·q[b,h,i]·k_j − lse[b,h,i])
+ * with lse [B,Hq,Lq] as sdpa_paged_attn wrote it for the same call (so sinks take their share),
+ * old = weights[b][g][j], or 0 for the tokens of the real rows themselves, j >= lens[b] −
+ * counts[b].  A row whose lse is −inf adds nothing; a token on a bad page gets nothing.
+ *   weights fp32 [B][Hkv][slots], element strides (batch, head) in weight_strides, read and
+ *   written; sequences longer than slots are reported and cut, as by max_len.
+ * Sums have one order: results are bitwise reproducible.
+ */
+int sdpa_paged_weights(const sdpa_cache_t* cache, const void* q, const float* lse, float* weights,
+                       const int64_t* weight_strides, int slots, const sdpa_layout_t* layout,
+                       const int* counts, int B, int Hq, int Lq, float scale, int is_causal,
+                       int max_len, void* stream);
+
+/*
+ * Eviction: each KV head of each sequence of more than `budget` tokens keeps `budget` of them,
+ * the last `recent` ones (0 <= recent <= budget) and of the others those of the largest weight
+ * (ties go to the earlier token; a NaN counts as less than any number), moved together to the
+ * positions 0..budget−1 in their order, in place.  Heads keep tokens of their own, so
+ * position j no longer means the same token in each.  Positions past the kept ones hold what they held.
+ *   new_lens    int32 [B]: min(lens[b], budget); may be cache->lens itself
+ *   kept        int32 [B][Hkv][budget]: the positions that the kept tokens had, ascending, −1
+ *               past the last
+ *   weights     fp32 [B][Hkv][slots], read; new_weights the same shape, written: the kept
+ *               tokens' weights, 0 in the slots past them; may be weights itself.
+ *               weight_strides: (batch, head) of weights, then of new_weights.
+ * Sequences of at most `budget` tokens keep all of them.  A token whose page is bad, or
+ * whose new place's is, is not moved (reported).  Two tokens must not share a place.
+ */
+int sdpa_paged_evict(const sdpa_cache_t* cache, const float* weights, float* new_weights,
+                     const int64_t* weight_strides, int slots, int* new_lens, int* kept, int B,
+                     int budget, int recent, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word that kernels set
  * when a bounded wait gives up or an index that they read is out of range (the first of
  * them since the last poll).  Returns SDPA_OK, SDPA_ERR_DEVICE_TIMEOUT,
@@ -433,7 +500,13 @@ typedef enum {
   SDPA_KERNEL_CACHE_READ = 9,
   SDPA_KERNEL_CACHE_ATTN = 10, /* attention over the 4-bit cache */
   SDPA_KERNEL_CACHE_JOIN = 11, /* its second kernel, where a sequence is split */
-  SDPA_KERNEL_COUNT = 12
+  SDPA_KERNEL_PAGED_WRITE = 12,
+  SDPA_KERNEL_PAGED_ATTN = 13,    /* attention over 16-bit pages */
+  SDPA_KERNEL_PAGED_JOIN = 14,    /* its second kernel, where a sequence is split */
+  SDPA_KERNEL_PAGED_WEIGHTS = 15,
+  SDPA_KERNEL_PAGED_SELECT = 16,  /* eviction: which tokens stay */
+  SDPA_KERNEL_PAGED_MOVE = 17,    /* eviction: their keys and values */
+  SDPA_KERNEL_COUNT = 18
 } sdpa_kernel_t;
 int sdpa_timing_enable(int on);
 int sdpa_timing_read(int kernel, double* total_ms, uint64_t* launches);

@@ -97,11 +97,20 @@ SIGNATURES = {
     "sdpa_cache_attn_workspace_size": (_sz, [_vp, _i, _i, _i, _i]),
     "sdpa_cache_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _vp, _sz,
                              _vp]),
+    "sdpa_paged_page_bytes": (_sz, [_i, _i, _i, _i]),
+    "sdpa_paged_write": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "sdpa_paged_attn_workspace_size": (_sz, [_vp, _i, _i, _i, _i]),
+    "sdpa_paged_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _vp, _sz,
+                             _vp]),
+    "sdpa_paged_weights": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _f, _i, _i,
+                                _vp]),
+    "sdpa_paged_evict": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp]),
 }
 BWD_NOALLOC_MAX_ROWS = 1 << 20
 KERNELS = {"fwd": 0, "delta": 1, "dq": 2, "dkdv": 3, "vec_fwd": 4, "vec_bwd": 5, "sink_grad": 6,
            "rotary": 7, "cache_write": 8, "cache_read": 9, "cache_attn": 10,
-           "cache_join": 11}
+           "cache_join": 11, "paged_write": 12, "paged_attn": 13, "paged_join": 14,
+           "paged_weights": 15, "paged_select": 16, "paged_move": 17}
 
 _lib = None
 
@@ -244,6 +253,40 @@ def sdpa_cache_attn(cache, q, out, lse, sinks, layouts, B, Hq, Lq, scale, is_cau
     """cache: a ``Cache``, or its bytes; layouts: Int64x6 of q and out, or their bytes."""
     return load().sdpa_cache_attn(_struct(cache), q, out, lse, sinks, layouts, B, Hq, Lq,
                                   scale, is_causal, max_len, workspace, workspace_bytes, stream)
+
+
+def sdpa_paged_page_bytes(page_size, Hkv, D, dtype) -> int:
+    return load().sdpa_paged_page_bytes(page_size, Hkv, D, dtype)
+
+
+def sdpa_paged_write(cache, k, v, layouts, counts, B, L, stream):
+    """cache: a ``Cache``, or its bytes; layouts: Int64x6 of k and v, or their bytes."""
+    return load().sdpa_paged_write(_struct(cache), k, v, layouts, counts, B, L, stream)
+
+
+def sdpa_paged_attn_workspace_size(cache, B, Hq, Lq, max_len) -> int:
+    return load().sdpa_paged_attn_workspace_size(_struct(cache), B, Hq, Lq, max_len)
+
+
+def sdpa_paged_attn(cache, q, out, lse, sinks, layouts, counts, B, Hq, Lq, scale, is_causal,
+                    max_len, workspace, workspace_bytes, stream):
+    """cache: a ``Cache``, or its bytes; layouts: Int64x6 of q and out, or their bytes."""
+    return load().sdpa_paged_attn(_struct(cache), q, out, lse, sinks, layouts, counts, B, Hq, Lq,
+                                  scale, is_causal, max_len, workspace, workspace_bytes, stream)
+
+
+def sdpa_paged_weights(cache, q, lse, weights, weight_strides, slots, layout, counts, B, Hq, Lq,
+                       scale, is_causal, max_len, stream):
+    """weight_strides: bytes of two int64 (batch, head); layout: Int64x3 of q, or their bytes."""
+    return load().sdpa_paged_weights(_struct(cache), q, lse, weights, weight_strides, slots,
+                                     layout, counts, B, Hq, Lq, scale, is_causal, max_len, stream)
+
+
+def sdpa_paged_evict(cache, weights, new_weights, weight_strides, slots, new_lens, kept, B, budget,
+                     recent, stream):
+    """weight_strides: bytes of four int64 (batch, head of weights, then of new_weights)."""
+    return load().sdpa_paged_evict(_struct(cache), weights, new_weights, weight_strides, slots,
+                                   new_lens, kept, B, budget, recent, stream)
 
 
 def sdpa_poll_status(stream):

@@ -470,6 +470,204 @@ def cache_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
     return out, lse
 
 
+# ---- 16-bit paged cache
+
+
+_pack2, _pack4 = (struct.Struct(f"{n}q").pack for n in (2, 4))
+
+
+def paged_empty(num_pages, num_kv_heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda"):
+    """Memory of a paged cache of keys and values in 16 bits: a tensor of ``dtype`` (fp16 or
+    bf16) [num_pages, 2, num_kv_heads, page_size, head_dim], keys before values."""
+    code = DTYPE_CODE.get(dtype, 0)
+    if not _lib.sdpa_paged_page_bytes(page_size, num_kv_heads, head_dim, code) or num_pages < 1:
+        raise ValueError("a cache needs fp16 or bf16, a supported head dim and pages of a "
+                         "multiple of 16 tokens")
+    return torch.empty((num_pages, 2, num_kv_heads, page_size, head_dim), dtype=dtype,
+                       device=device)
+
+
+def _paged(cache, pages, lens, B):
+    """sdpa_cache_t, packed: a 16-bit cache with one call's page table [B, n] and lengths [B]."""
+    dtype = cache.dtype
+    if cache.dim() != 5 or not cache.is_cuda or not cache.is_contiguous() or cache.shape[1] != 2:
+        raise ValueError("cache must be a contiguous CUDA tensor made by paged_empty")
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("cache must be fp16 or bf16")
+    if pages.dtype is not torch.int32 or pages.dim() != 2 or pages.shape[0] != B or pages.stride(1) != 1:
+        raise ValueError(f"pages must be an int32 [{B}, n] tensor with contiguous rows")
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+        raise ValueError(f"lens must be a contiguous int32 [{B}] tensor")
+    n, _, H, page_size, D = cache.shape
+    entries = pages.shape[1]
+    return _pack_cache(cache.data_ptr(), n, page_size, H, D, DTYPE_CODE[dtype], pages.data_ptr(),
+                       pages.stride(0) if B > 1 else entries, entries, lens.data_ptr())
+
+
+def _counts(counts, B):
+    if counts is None:
+        return None
+    if counts.dtype is not torch.int32 or counts.shape != (B,) or not counts.is_contiguous():
+        raise ValueError(f"counts must be a contiguous int32 [{B}] tensor")
+    return counts.data_ptr()
+
+
+def _weight_rows(name, t, shape):
+    """(batch, head) strides of fp32 weights [B, Hkv, slots] with contiguous rows."""
+    if t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 3 or (
+            tuple(t.shape[:2]) != tuple(shape[:2]) or len(shape) == 3 and t.shape[2] != shape[2]):
+        raise ValueError(f"{name} must be an fp32 CUDA tensor {[*shape[:2]]} + [slots], not "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    b, h, e = t.stride()
+    B, H, n = t.shape
+    if e != 1 and n > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return (b if B > 1 else H * max(h, n)), (h if H > 1 else n)
+
+
+def paged_write(cache, k, v, pages, lens, counts=None, stream=None):
+    """Copies the rows of k and v [B,Hkv,L,D] into the cache, in place; the other arguments as in
+    ``cache_write``."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return paged_write(cache, k, v, pages, lens, counts)
+    shape, ks = _rows("k", k, cache.dtype)
+    _, vs = _rows("v", v, cache.dtype, shape)
+    B, H, L, D = shape
+    c = _paged(cache, pages, lens, B)
+    if H != cache.shape[2] or D != cache.shape[4]:
+        raise ValueError("k and v must be [B, Hkv, L, D] of the cache's heads and head dim")
+    st = _lib.sdpa_paged_write(c, k.data_ptr(), v.data_ptr(), _pack6(*ks, *vs), _counts(counts, B),
+                               B, L, _here(cache, k, v, pages, lens, counts))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_paged_write")
+
+
+def _max_len(max_len):
+    return 0 if max_len is None else max(0, min(int(max_len), 2**31 - 1))  # a C int
+
+
+def paged_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right", need_lse=False,
+                    out=None, lse=None, sinks=None, counts=None, max_len=None, workspace=None,
+                    stream=None):
+    """Attention of q [B,Hq,L,D] over the keys and values of a 16-bit cache; returns (out, lse or
+    None).
+
+    For one token or a few a sequence as for chunks of a prompt (write their rows first).
+    counts int32 [B]: only the last counts[b] rows are real; the others of a padded batch give
+    0 (lse -inf).  The other arguments as in ``cache_attention``.
+    """
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return paged_attention(q, cache, pages, lens, scale, is_causal, need_lse, out, lse,
+                                   sinks, counts, max_len, workspace)
+    dtype = cache.dtype
+    shape, qs = _rows("q", q, dtype)
+    B, Hq, L, D = shape
+    c = _paged(cache, pages, lens, B)
+    if D != cache.shape[4]:
+        raise ValueError("q must be [B, Hq, L, D] of the cache's head dim")
+    if out is None:
+        out = torch.empty_like(q)
+    _, os = _rows("out", out, dtype, shape)
+    if not need_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((B, Hq, L), device=q.device, dtype=torch.float32)
+    elif lse.shape != (B, Hq, L) or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, Hq, L] tensor")
+    if sinks is not None:
+        _check_sinks("sinks", sinks, Hq)
+    max_len = _max_len(max_len)
+    need = _lib.sdpa_paged_attn_workspace_size(c, B, Hq, L, max_len)
+    if workspace is None and need:
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    elif workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    st = _lib.sdpa_paged_attn(
+        c, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if sinks is None else sinks.data_ptr(), _pack6(*qs, *os), _counts(counts, B), B, Hq, L,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _causal(is_causal), max_len,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _here(q, cache, pages, lens, out, lse, sinks, counts, workspace))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_paged_attn")
+    return out, lse
+
+
+def paged_weights(q, cache, pages, lens, lse, weights, scale=None, is_causal="bottom_right",
+                  counts=None, max_len=None, stream=None):
+    """Adds the attention weight of this call's queries to that of the cached tokens, in place;
+    returns ``weights``.
+
+    Call it after ``paged_attention`` with the same arguments and the lse that it gave.  weights
+    fp32 [B,Hkv,slots]: one sum a token and KV head, over all queries so far and the query heads
+    that share the KV head.  The tokens of the call's own rows (the last counts[b], or L) start
+    from 0, whatever their slots held.
+    """
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return paged_weights(q, cache, pages, lens, lse, weights, scale, is_causal, counts,
+                                 max_len)
+    shape, qs = _rows("q", q, cache.dtype)
+    B, Hq, L, D = shape
+    c = _paged(cache, pages, lens, B)
+    if D != cache.shape[4]:
+        raise ValueError("q must be [B, Hq, L, D] of the cache's head dim")
+    if lse.shape != (B, Hq, L) or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, Hq, L] tensor")
+    ws = _weight_rows("weights", weights, (B, cache.shape[2]))
+    st = _lib.sdpa_paged_weights(
+        c, q.data_ptr(), lse.data_ptr(), weights.data_ptr(), _pack2(*ws), weights.shape[2],
+        _pack3(*qs), _counts(counts, B), B, Hq, L,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _causal(is_causal),
+        _max_len(max_len), _here(q, cache, pages, lens, lse, weights, counts))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_paged_weights")
+    return weights
+
+
+def paged_evict(cache, pages, lens, weights, budget, recent=0, new_lens=None, new_weights=None,
+                kept=None, stream=None):
+    """Shrinks each sequence of more than ``budget`` tokens to that many, in place; returns
+    (new_lens, new_weights, kept).
+
+    Each KV head keeps its ``recent`` last tokens and of the others those with the largest
+    ``weights`` (fp32 [B,Hkv,slots], see ``paged_weights``; ties go to the earlier token), moved
+    together in their order.  new_lens int32 [B] is min(lens, budget), new_weights holds the kept
+    tokens' weights and 0 behind them, kept int32 [B,Hkv,budget] the positions that they had (-1
+    behind them).  ``new_lens=lens, new_weights=weights`` updates both in place.
+    """
+    if stream is not None and stream != torch.cuda.current_stream():
+        with torch.cuda.stream(stream):
+            return paged_evict(cache, pages, lens, weights, budget, recent, new_lens, new_weights,
+                               kept)
+    B, H, budget = lens.numel(), cache.shape[2] if cache.dim() == 5 else 0, int(budget)
+    c = _paged(cache, pages, lens, B)
+    ws = _weight_rows("weights", weights, (B, H))
+    if not 0 <= recent <= budget or not 1 <= budget < 2**31:
+        raise ValueError("budget must be at least 1 and recent within 0 .. budget")
+    if new_weights is None:
+        new_weights = torch.empty_like(weights)
+    ns = _weight_rows("new_weights", new_weights, tuple(weights.shape))
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    elif new_lens.dtype is not torch.int32 or new_lens.shape != (B,) or not new_lens.is_contiguous():
+        raise ValueError(f"new_lens must be a contiguous int32 [{B}] tensor")
+    if kept is None:
+        kept = torch.empty((B, H, budget), dtype=torch.int32, device=cache.device)
+    elif kept.dtype is not torch.int32 or kept.shape != (B, H, budget) or not kept.is_contiguous():
+        raise ValueError(f"kept must be a contiguous int32 [{B}, {H}, {budget}] tensor")
+    st = _lib.sdpa_paged_evict(
+        c, weights.data_ptr(), new_weights.data_ptr(), _pack4(*ws, *ns), weights.shape[2],
+        new_lens.data_ptr(), kept.data_ptr(), B, budget, int(recent),
+        _here(cache, pages, lens, weights, new_lens, new_weights, kept))
+    if st != _lib.OK:
+        raise _lib.SdpaError(st, "sdpa_paged_evict")
+    return new_lens, new_weights, kept
+
+
 def poll_status(stream=None):
     """Synchronise the stream; raise if a kernel reported a timed-out wait or an index out of
     range."""

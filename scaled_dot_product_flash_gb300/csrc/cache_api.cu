@@ -1,10 +1,12 @@
-// C ABI of the rotary embedding and the 4-bit paged cache: argument checks and launches.
+// C ABI of the rotary embedding and of the paged caches, in 4 and in 16 bits: argument checks
+// and launches.
 // The operations and every convention are documented in include/sdpa.h.
 #include <cmath>
 #include <cstring>
 
 #include "cache.h"
 #include "host.h"
+#include "paged.h"
 
 using namespace sdpa;
 
@@ -260,4 +262,198 @@ extern "C" int sdpa_cache_attn(const sdpa_cache_t* cache, const void* q, void* o
   const cudaError_t e = launch_one(SDPA_KERNEL_CACHE_ATTN, s, [&] { return launch_cache_attn(a, cache->dtype, s); });
   if (e != cudaSuccess || !need) return status_of(e);
   return status_of(launch_one(SDPA_KERNEL_CACHE_JOIN, s, [&] { return launch_cache_join(a, cache->dtype, s); }));
+}
+
+// ---- the cache of 16-bit pages
+
+namespace {
+
+size_t paged_page_bytes(int page_size, int Hkv, int D) { return (size_t)2 * Hkv * page_size * D * 2; }
+size_t paged_bytes(const CacheArgs& c) { return (size_t)c.num_pages * paged_page_bytes(c.page_size, c.Hkv, c.D); }
+
+int check_paged(const sdpa_cache_t* cache, int B, int L, CacheArgs* c) {
+  const int st = check_cache(cache, B, L, c);
+  if (st != SDPA_OK) return st;
+  // 2^29: the rows of keys and values together are a 32-bit number; 2^40: strides of a tensor map.
+  if ((double)B * c->Hkv * L > 536870912.0 || (double)paged_page_bytes(c->page_size, c->Hkv, c->D) >= 1099511627776.0) return SDPA_ERR_UNSUPPORTED;
+  return SDPA_OK;
+}
+
+// Checks the sizes of an attention call (or of its weights) and fills them in.
+int check_paged_attn(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len, PagedArgs* a) {
+  std::memset(a, 0, sizeof(*a));
+  const int st = check_paged(cache, B, Lq, &a->c);
+  if (st != SDPA_OK) return st;
+  if (Hq < 1 || Hq % a->c.Hkv != 0) return SDPA_ERR_INVALID_ARG;
+  if (Hq > 65535 || (double)B * Hq * Lq > 2147483647.0) return SDPA_ERR_UNSUPPORTED;
+  a->Hq = Hq;
+  a->G = Hq / a->c.Hkv;
+  const int table = a->c.pages_per_seq * a->c.page_size;
+  a->max_len = max_len <= 0 || max_len > table ? table : max_len;
+  return paged_attn_launchable(*a) ? SDPA_OK : SDPA_ERR_UNSUPPORTED;
+}
+
+int check_mode(float scale, int is_causal) {
+  if (!std::isfinite(scale) || is_causal < SDPA_CAUSAL_NONE || is_causal > SDPA_CAUSAL_BOTTOM_RIGHT) return SDPA_ERR_INVALID_ARG;
+  return is_causal == SDPA_CAUSAL_TOP_LEFT ? SDPA_ERR_UNSUPPORTED : SDPA_OK;
+}
+
+// Bytes of an array [B][Hkv][slots] of fp32 with these strides, 0 if two rows share an element.
+size_t weight_bytes(int B, int Hkv, int slots, int64_t batch, int64_t head) {
+  const int64_t most = (int64_t)1 << 40;
+  if (slots < 1 || batch < 0 || head < 0 || batch > most || head > most) return 0;
+  const bool inner_head = B == 1 || batch >= (Hkv - 1) * head + slots;
+  const bool inner_batch = Hkv == 1 || head >= (B - 1) * batch + slots;
+  if (!((Hkv == 1 || head >= slots) && inner_head) && !((B == 1 || batch >= slots) && inner_batch)) return 0;
+  return (size_t)((B - 1) * batch + (Hkv - 1) * head + slots) * sizeof(float);
+}
+
+}  // namespace
+
+extern "C" size_t sdpa_paged_page_bytes(int page_size, int Hkv, int D, int dtype) {
+  return sdpa_cache_page_bytes(page_size, Hkv, D, dtype) ? paged_page_bytes(page_size, Hkv, D) : 0;
+}
+
+extern "C" int sdpa_paged_write(const sdpa_cache_t* cache, const void* k, const void* v,
+                                const sdpa_layout_t* layouts, const int* counts, int B, int L, void* stream) {
+  CacheArgs c;
+  int st = check_paged(cache, B, L, &c);
+  if (st != SDPA_OK) return st;
+  if (!k || !v || !layouts || !aligned16(k) || !aligned16(v) || !aligned4(counts)) return SDPA_ERR_INVALID_ARG;
+  size_t kb, vb;
+  if (!check_layout(layouts[0], B, c.Hkv, L, c.D, 2, &c.lk, &kb) || !check_layout(layouts[1], B, c.Hkv, L, c.D, 2, &c.lv, &vb))
+    return SDPA_ERR_INVALID_ARG;
+  const size_t n = paged_bytes(c);
+  if (overlaps(c.data, n, k, kb) || overlaps(c.data, n, v, vb) || overlaps(c.data, n, counts, (size_t)B * sizeof(int)) || overlaps_tables(c.data, n, c))
+    return SDPA_ERR_INVALID_ARG;
+  c.k = const_cast<void*>(k);
+  c.v = const_cast<void*>(v);
+  c.counts = counts;
+  if ((st = error_word(&c.err)) != SDPA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return status_of(launch_one(SDPA_KERNEL_PAGED_WRITE, s, [&] { return launch_paged_write(c, s); }));
+}
+
+extern "C" size_t sdpa_paged_attn_workspace_size(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len) {
+  PagedArgs a;
+  return check_paged_attn(cache, B, Hq, Lq, max_len, &a) == SDPA_OK ? paged_attn_workspace(a) : 0;
+}
+
+extern "C" int sdpa_paged_attn(const sdpa_cache_t* cache, const void* q, void* out, float* lse,
+                               const float* sinks, const sdpa_layout_t* layouts, const int* counts, int B,
+                               int Hq, int Lq, float scale, int is_causal, int max_len, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  PagedArgs a;
+  int st = check_paged_attn(cache, B, Hq, Lq, max_len, &a);
+  if (st != SDPA_OK || (st = check_mode(scale, is_causal)) != SDPA_OK) return st;
+  if (!q || !out || !layouts || !aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned4(sinks) || !aligned4(counts))
+    return SDPA_ERR_INVALID_ARG;
+  size_t qb, ob;
+  if (!check_layout(layouts[0], B, Hq, Lq, a.c.D, 2, &a.lq, &qb) || !check_layout(layouts[1], B, Hq, Lq, a.c.D, 2, &a.lo, &ob))
+    return SDPA_ERR_INVALID_ARG;
+  const size_t need = paged_attn_workspace(a);
+  if (need && (!workspace || workspace_bytes < need)) return SDPA_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return SDPA_ERR_INVALID_ARG;
+  const size_t lb = lse ? (size_t)B * Hq * Lq * sizeof(float) : 0;
+  const void* ins[] = {q, a.c.data, sinks, counts};
+  const size_t in_bytes[] = {qb, paged_bytes(a.c), (size_t)Hq * sizeof(float), (size_t)B * sizeof(int)};
+  void* outs[] = {out, lse, workspace};
+  const size_t out_bytes[] = {ob, lb, need};
+  for (int x = 0; x < 3; ++x) {
+    if (overlaps_tables(outs[x], outs[x] ? out_bytes[x] : 0, a.c)) return SDPA_ERR_INVALID_ARG;
+    for (int y = 0; y < 4; ++y)
+      if (overlaps(outs[x], out_bytes[x], ins[y], in_bytes[y]) || (y > x && y < 3 && overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])))
+        return SDPA_ERR_INVALID_ARG;
+  }
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.sinks = sinks;
+  a.c.counts = counts;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.causal = is_causal != SDPA_CAUSAL_NONE;
+  a.workspace = static_cast<float*>(workspace);
+  a.wait_limit_ns = wait_limit_ns();
+  if ((st = error_word(&a.c.err)) != SDPA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_one(SDPA_KERNEL_PAGED_ATTN, s, [&] { return launch_paged_attn(a, cache->dtype, s); });
+  if (e != cudaSuccess || !need) return status_of(e);
+  return status_of(launch_one(SDPA_KERNEL_PAGED_JOIN, s, [&] { return launch_paged_join(a, cache->dtype, s); }));
+}
+
+extern "C" int sdpa_paged_weights(const sdpa_cache_t* cache, const void* q, const float* lse, float* weights,
+                                  const int64_t* weight_strides, int slots, const sdpa_layout_t* layout,
+                                  const int* counts, int B, int Hq, int Lq, float scale, int is_causal,
+                                  int max_len, void* stream) {
+  PagedArgs a;
+  int st = check_paged_attn(cache, B, Hq, Lq, max_len, &a);
+  if (st != SDPA_OK || (st = check_mode(scale, is_causal)) != SDPA_OK) return st;
+  if (!q || !lse || !weights || !weight_strides || !layout || !aligned16(q) || !aligned4(lse) || !aligned4(weights) || !aligned4(counts))
+    return SDPA_ERR_INVALID_ARG;
+  size_t qb;
+  if (!check_layout(*layout, B, Hq, Lq, a.c.D, 2, &a.lq, &qb)) return SDPA_ERR_INVALID_ARG;
+  const size_t wb = weight_bytes(B, a.c.Hkv, slots, weight_strides[0], weight_strides[1]);
+  if (!wb) return SDPA_ERR_INVALID_ARG;
+  if (overlaps(weights, wb, q, qb) || overlaps(weights, wb, lse, (size_t)B * Hq * Lq * sizeof(float)) || overlaps(weights, wb, a.c.data, paged_bytes(a.c)) ||
+      overlaps(weights, wb, counts, (size_t)B * sizeof(int)) || overlaps_tables(weights, wb, a.c))
+    return SDPA_ERR_INVALID_ARG;
+  if (slots < a.max_len) a.max_len = slots;
+  a.q = q;
+  a.lse = const_cast<float*>(lse);
+  a.c.counts = counts;
+  a.weights = weights;
+  a.w_batch = weight_strides[0];
+  a.w_head = weight_strides[1];
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.causal = is_causal != SDPA_CAUSAL_NONE;
+  a.wait_limit_ns = wait_limit_ns();
+  if ((st = error_word(&a.c.err)) != SDPA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return status_of(launch_one(SDPA_KERNEL_PAGED_WEIGHTS, s, [&] { return launch_paged_weights(a, cache->dtype, s); }));
+}
+
+extern "C" int sdpa_paged_evict(const sdpa_cache_t* cache, const float* weights, float* new_weights,
+                                const int64_t* weight_strides, int slots, int* new_lens, int* kept, int B,
+                                int budget, int recent, void* stream) {
+  EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int st = check_paged(cache, B, 1, &a.c);
+  if (st != SDPA_OK) return st;
+  if (!weights || !new_weights || !weight_strides || !new_lens || !kept || !aligned4(weights) || !aligned4(new_weights) || !aligned4(new_lens) || !aligned4(kept))
+    return SDPA_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || recent > budget) return SDPA_ERR_INVALID_ARG;
+  if (budget > 1 << 30 || (int64_t)2 * a.c.Hkv > 65535) return SDPA_ERR_UNSUPPORTED;
+  const size_t wb = weight_bytes(B, a.c.Hkv, slots, weight_strides[0], weight_strides[1]);
+  const size_t nb = weight_bytes(B, a.c.Hkv, slots, weight_strides[2], weight_strides[3]);
+  if (!wb || !nb) return SDPA_ERR_INVALID_ARG;
+  // In place means the very same elements; any other overlap of an output is refused.
+  const bool w_in_place = weights == new_weights && weight_strides[0] == weight_strides[2] && weight_strides[1] == weight_strides[3];
+  const bool l_in_place = new_lens == cache->lens;
+  const size_t n = paged_bytes(a.c), lb = (size_t)B * sizeof(int), kb = (size_t)B * a.c.Hkv * budget * sizeof(int);
+  const size_t tb = table_bytes(B, a.c.pages_stride, a.c.pages_per_seq);
+  const void* outs[] = {a.c.data, new_weights, new_lens, kept};
+  const size_t out_bytes[] = {n, nb, lb, kb};
+  for (int x = 0; x < 4; ++x) {
+    if (overlaps(outs[x], out_bytes[x], a.c.pages, tb) || (!(x == 1 && w_in_place) && overlaps(outs[x], out_bytes[x], weights, wb)) ||
+        (!(x == 2 && l_in_place) && overlaps(outs[x], out_bytes[x], a.c.lens, lb)))
+      return SDPA_ERR_INVALID_ARG;
+    for (int y = x + 1; y < 4; ++y)
+      if (overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])) return SDPA_ERR_INVALID_ARG;
+  }
+  a.weights = weights;
+  a.new_weights = new_weights;
+  a.w_batch = weight_strides[0];
+  a.w_head = weight_strides[1];
+  a.nw_batch = weight_strides[2];
+  a.nw_head = weight_strides[3];
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.budget = budget;
+  a.recent = recent;
+  a.slots = slots;
+  if ((st = error_word(&a.c.err)) != SDPA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_one(SDPA_KERNEL_PAGED_SELECT, s, [&] { return launch_paged_select(a, s); });
+  if (e != cudaSuccess) return status_of(e);
+  return status_of(launch_one(SDPA_KERNEL_PAGED_MOVE, s, [&] { return launch_paged_move(a, s); }));
 }

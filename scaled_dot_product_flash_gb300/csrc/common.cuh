@@ -36,6 +36,10 @@ enum KernelId : unsigned {
   kKidCacheWrite = 11,
   kKidCacheRead = 12,
   kKidCacheAttn = 13,
+  kKidPagedWrite = 14,
+  kKidPagedAttn = 15,
+  kKidPagedWeights = 16,
+  kKidPagedEvict = 17,
 };
 
 __device__ __forceinline__ void report_error(unsigned* err, unsigned code, unsigned kid) {

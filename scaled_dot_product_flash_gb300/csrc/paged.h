@@ -1,0 +1,108 @@
+// Internal parameters, launchers and device helpers of the 16-bit paged cache (its layout and
+// conventions are documented in include/sdpa.h).
+#pragma once
+
+#include "cache.h"
+#include "tc_common.cuh"
+
+namespace sdpa {
+
+// Attention over the cache, and the weights that its tokens gather (c.counts: real rows).
+struct PagedArgs {
+  CacheArgs c;
+  const void* q;
+  void* out;
+  float* lse;           // attention: written, nullable; weights: read
+  const float* sinks;   // nullable
+  Layout lq, lo;
+  int Hq, G;
+  float scale_log2;     // scale·log2(e)
+  int causal;
+  int max_len;          // longest sequence, in tokens
+  float* workspace;
+  float* weights;       // [B][Hkv][slots]
+  int64_t w_batch, w_head;
+  uint64_t wait_limit_ns;
+};
+bool paged_attn_launchable(const PagedArgs& a);   // whether its blocks fit a grid
+size_t paged_attn_workspace(const PagedArgs& a);  // 0: one kernel does it all
+cudaError_t launch_paged_attn(const PagedArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedArgs& a, int dtype, cudaStream_t s);  // after it, with a workspace
+cudaError_t launch_paged_weights(const PagedArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_paged_write(const CacheArgs& a, cudaStream_t s);
+
+// Partial results of attention: how many chunks of how many tokens.
+struct Cut {
+  int chunk, splits;
+};
+
+struct EvictArgs {
+  CacheArgs c;
+  const float* weights;
+  float* new_weights;
+  int64_t w_batch, w_head, nw_batch, nw_head;
+  int* kept;      // [B][Hkv][budget]
+  int* new_lens;  // [B]
+  int budget, recent, slots;  // slots: entries of a row of weights
+};
+cudaError_t launch_paged_select(const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_paged_move(const EvictArgs& a, cudaStream_t s);
+
+// 4-D tensor map over a cache of 16-bit pages: box of `rows` tokens of 64 elements at
+// (x = element, y = place in the page, h = Hkv·(0 keys, 1 values) + head, b = page).
+inline bool make_tmap_pages(CUtensorMap* map, const CacheArgs& c, int rows) {
+  const int64_t head = (int64_t)c.page_size * c.D;
+  return make_tmap_4d(map, c.data, c.D, c.page_size, 2 * c.Hkv, c.num_pages, Layout{2 * c.Hkv * head, head, c.D}, rows);
+}
+
+// What the rows of a call see.  Row i (0 <= i < L) of a sequence of len tokens has position
+// len - L + i; it is real if it is among the last `count` rows.
+struct Rows {
+  int len, first, L;  // first: the first real row
+  int causal;
+  // Tokens [0, limit) are seen by row i.
+  __device__ __forceinline__ int limit(int i) const {
+    if (i < first) return 0;
+    return causal ? max(0, len - L + i + 1) : len;
+  }
+};
+__device__ __forceinline__ Rows rows_of(const CacheArgs& c, int b, int causal, int most, unsigned kid) {
+  Rows r;
+  r.len = cache_len(c, b, most, kid);
+  const int count = c.counts ? min(max(c.counts[b], 0), c.L) : c.L;
+  r.first = c.L - count;
+  r.L = c.L;
+  r.causal = causal;
+  return r;
+}
+
+// Element offset of a row of a page: which = 0 keys, 1 values.
+__device__ __forceinline__ int64_t paged_row(const CacheArgs& c, int page, int which, int h, int place) {
+  return ((((int64_t)page * 2 + which) * c.Hkv + h) * c.page_size + place) * c.D;
+}
+
+// Columns d..d+3 of Σ exp2(c·q·k_j − M)·v_j over the tokens [from, to) of sequence b that query
+// (hq, i) of KV head h sees, product by product in fp32: the way out for outputs that came out NaN,
+// where a value that the row does not see, or the remainder of a weight times an infinite one, gave 0·∞.
+template <typename T, int D>
+__device__ __noinline__ float4 sum_apart(const PagedArgs& a, int b, int h, int hq, int i, int d, int from, int to, float M) {
+  const CacheArgs& c = a.c;
+  const T* q = row_ptr<T>(a.q, a.lq, b, hq, i);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = from; j < to; ++j) {
+    const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
+    if ((unsigned)page >= (unsigned)c.num_pages) continue;
+    const T* k = reinterpret_cast<const T*>(c.data) + paged_row(c, page, 0, h, place);
+    const T* v = reinterpret_cast<const T*>(c.data) + paged_row(c, page, 1, h, place) + d;
+    float s = 0.f;
+    for (int x = 0; x < D; ++x) s = fmaf(Elem<T>::to_f(q[x]), Elem<T>::to_f(k[x]), s);
+    const float p = tc::ex2(s * a.scale_log2 - M);
+    o.x = fmaf(p, Elem<T>::to_f(v[0]), o.x);
+    o.y = fmaf(p, Elem<T>::to_f(v[1]), o.y);
+    o.z = fmaf(p, Elem<T>::to_f(v[2]), o.z);
+    o.w = fmaf(p, Elem<T>::to_f(v[3]), o.w);
+  }
+  return o;
+}
+
+}  // namespace sdpa

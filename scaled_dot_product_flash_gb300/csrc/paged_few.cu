@@ -1,0 +1,678 @@
+// Attention over a 16-bit paged cache for few query rows a KV head, and the kernel that joins the
+// chunks of a sequence (conventions in include/sdpa.h).
+//
+// Rows.  The G·L query rows of a KV head (row r = query r / G of head r % G of the group) are cut
+// into blocks of 16·NT; a block takes one of them and one chunk of the sequence, and its warps
+// take units of 16 tokens of that chunk in turn, each with a running maximum, sum and output of its
+// own, merged at the end.  Chunks are joined by a second kernel, placed while the first still runs.
+//
+// Bound: the bytes of the cache, 4·D a token and KV head, each read once.  So a unit's keys and
+// values come by bulk tensor loads into a ring of the warp's own, a few units ahead, without a block
+// barrier (16 tokens never cross a page, whose size is a multiple of 16); the products are warp-level
+// MMAs, m16n8k16, S = Q·K^T and O += P·V, whose accumulator of the first is the operand of the second.
+// P enters O as two 16-bit numbers, head and remainder, so that O is as exact as with fp32 weights: the
+// second MMA is hidden behind the copies.
+// The running maximum is raised only when a score passes it by 2^8: one vote a unit, no shuffles.
+// An output that is NaN without a reason in its row's scores has met a value that is not finite,
+// perhaps one that its row does not see: it is summed anew, one product after the other.
+#include <atomic>
+
+#include "paged.h"
+
+namespace sdpa {
+namespace {
+
+using tc::ex2;
+
+constexpr float kRescale = 8.f;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kCB = (D + 63) / 64;        // 64-element blocks of a row
+  static constexpr int kBlk = kTile * 128;         // bytes of one block of a unit's keys or values
+  static constexpr int kHalf = kCB * kBlk, kUnit = 2 * kHalf;
+  static constexpr int kWarps = D == 256 ? 4 : 8;
+  static constexpr int kStages = kCB == 1 ? 4 : 3;
+  static constexpr int kRows = kTile * NT;
+  static constexpr int kRing = kWarps * kStages * kUnit;
+  static constexpr int kMerge = kWarps * kTile * (D + 4) * 4;  // one row tile of every warp's output
+  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
+};
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// The ring of one warp: units of 16 tokens of one KV head, keys and (kBoth) values, loaded ahead.
+template <int D, int kWarps, int kStages, bool kBoth>
+struct Ring {
+  static constexpr int kCB = (D + 63) / 64, kBlk = kTile * 128, kHalf = kCB * kBlk;
+  static constexpr int kUnit = kBoth ? 2 * kHalf : kHalf;
+  const CUtensorMap* map;
+  const CacheArgs* c;
+  const int* table;
+  uint8_t* base;
+  uint64_t* full;
+  int h, start, end, warp, lane, units;  // units: of this warp
+  int issued, entry, base_unit;          // entry: page of unit base_unit + lane
+  uint32_t there, phase;                 // stages that hold a unit; the parity to wait for
+
+  __device__ __forceinline__ int pos(int u) const { return start + (warp + u * kWarps) * kTile; }
+  // This lane's entry of the page table, and whether it is a page.
+  __device__ __forceinline__ void look(int u0, unsigned kid) {
+    base_unit = u0;
+    entry = -1;
+    const int p = u0 + lane < units ? pos(u0 + lane) : end;
+    if (p < end) {
+      entry = table[p / c->page_size];
+      if ((unsigned)entry >= (unsigned)c->num_pages) {
+        report_error(c->err, kDevErrIndex, kid);
+        entry = -1;
+      }
+    }
+  }
+  // Starts the loads of the warp's next unit (all lanes).
+  __device__ __forceinline__ void issue(unsigned kid) {
+    const int u = issued++, s = u % kStages;
+    if (u >= units) return;
+    if (u - base_unit >= 32) look(u, kid);
+    const int page = __shfl_sync(0xffffffffu, entry, u - base_unit);
+    there &= ~(1u << s);
+    if (page < 0) return;
+    there |= 1u << s;
+    if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], kUnit);
+    __syncwarp();
+    if (lane < kUnit / kBlk) {
+      const int which = lane / kCB, cb = lane % kCB;
+      tc::tma_load_4d(base + s * kUnit + lane * kBlk, map, &full[s], cb * 64, pos(u) % c->page_size, which * c->Hkv + h, page);
+    }
+  }
+  // Waits for unit u; false if it is not there (its page is bad) or the wait gave up (ok = false).
+  __device__ __forceinline__ bool wait(int u, bool& ok, const tc::WaitCtx& wc) {
+    const int s = u % kStages;
+    if (!(there >> s & 1u)) return false;
+    ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], phase >> s & 1u, wc));
+    if (ok) phase ^= 1u << s;
+    return ok;
+  }
+  // Lets loads still in flight land (after the wait for unit u gave up).
+  __device__ __forceinline__ void drain(int u) {
+    for (int x = u; x < issued && x < units; ++x) {
+      const int s = x % kStages;
+      if (!(there >> s & 1u)) continue;
+      const uint64_t t0 = tc::globaltimer();
+      while (!tc::mbar_try_wait(&full[s], phase >> s & 1u) && tc::globaltimer() - t0 < 100000000ull) {
+      }
+    }
+  }
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
+    paged_few_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, Cut cut, int row_tiles) {
+  using C = Cfg<D, NT>;
+  constexpr int kWarps = C::kWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kWarps][C::kStages];
+  __shared__ float stat[kWarps][C::kRows][2];
+  __shared__ int abort_flag;
+  const CacheArgs& c = a.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int b = blockIdx.z, h = blockIdx.y / row_tiles, rt = blockIdx.y % row_tiles;
+  const int R = a.G * c.L, row0 = rt * C::kRows;
+  const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
+  const int i_last = (min(R, row0 + C::kRows) - 1) / a.G, i_first = max(row0 / a.G, rows.first);
+  const int least = rows.limit(i_first), most = i_first <= i_last ? rows.limit(i_last) : 0;
+  const int start = (int)min((int64_t)blockIdx.x * cut.chunk, (int64_t)most), end = (int)min((int64_t)start + cut.chunk, (int64_t)most);
+  if (start >= end && cut.splits > 1) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    return;
+  }
+  if (lane < C::kStages) tc::mbar_init(&full[warp][lane], 1);
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&map);
+  }
+  __syncthreads();
+  const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidPagedAttn};
+  const int all = (end - start + kTile - 1) / kTile;
+  Ring<D, kWarps, C::kStages, true> ring{&map, &c, c.pages + b * c.pages_stride, smem + warp * C::kStages * C::kUnit, full[warp], h, start, end,
+                                         warp, lane, all > warp ? (all - warp + kWarps - 1) / kWarps : 0, 0, -1, 0, 0u, 0u};
+  ring.look(0, kKidPagedAttn);
+#pragma unroll
+  for (int s = 0; s < C::kStages; ++s) ring.issue(kKidPagedAttn);
+
+  // Query rows as MMA operands; rows that are not there are zeros.
+  uint32_t qa[NT][D / 16][4];
+  int lim[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = row0 + kTile * nt + 8 * x + g, i = r / a.G;
+      lim[nt][x] = r < R ? rows.limit(i) : 0;
+      const bool real = r < R && i >= rows.first;
+      const T* q = real ? row_ptr<T>(a.q, a.lq, b, h * a.G + r % a.G, i) + 2 * t : nullptr;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int k8 = 0; k8 < 2; ++k8) qa[nt][ks][x + 2 * k8] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * k8) : 0u;
+    }
+
+  float o[NT][D / 8][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      m[nt][x] = minus_inf();
+      l[nt][x] = 0.f;
+    }
+  }
+  const float c2 = a.scale_log2;
+  // ldmatrix rows: keys for S (matrices: keys 0-7 and 8-15, each two 8-element pieces), keys for O.
+  const int k_row = lane / 16 * 8 + lane % 8, k_piece = lane / 8 % 2, v_row = lane % 16, v_piece = lane / 16;
+  bool ok = true;
+  for (int u = 0; u < ring.units; ++u) {
+    if (ring.wait(u, ok, wc)) {
+      const uint8_t* unit = ring.base + u % C::kStages * C::kUnit;
+      const uint32_t ks0 = tc::smem_u32(unit), vs0 = ks0 + C::kHalf;
+      const int k0 = ring.pos(u);
+      float s[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][n][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t kb[4];
+        ldsm(kb, ks0 + ks / 4 * C::kBlk + tc::sw128_off(k_row, ks % 4 * 2 + k_piece));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma<T>(s[nt][0], qa[nt][ks], kb[0], kb[1]);
+          mma<T>(s[nt][1], qa[nt][ks], kb[2], kb[3]);
+        }
+      }
+      // A unit that some row sees only in part: hidden scores are -inf; values that no row sees
+      // become 0, since what lies there may be anything.
+      const bool cut_unit = k0 + kTile > least;
+      if (k0 + kTile > most) {
+        for (int x = lane; x < kTile * C::kCB * 8; x += 32) {
+          const int row = x / (C::kCB * 8), piece = x % (C::kCB * 8);
+          if (k0 + row >= most)
+            *reinterpret_cast<uint4*>(const_cast<uint8_t*>(unit) + C::kHalf + piece / 8 * C::kBlk + tc::sw128_off(row, piece % 8)) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_async_smem();  // before the stage's next load
+        __syncwarp();
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float top[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = s[nt][n][e] * c2;
+            if (cut_unit && k0 + 8 * n + 2 * t + e % 2 >= lim[nt][e / 2]) v = minus_inf();
+            s[nt][n][e] = v;
+          }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) top[x] = fmaxf(fmaxf(s[nt][0][2 * x], s[nt][0][2 * x + 1]), fmaxf(s[nt][1][2 * x], s[nt][1][2 * x + 1]));
+        if (__any_sync(0xffffffffu, top[0] > m[nt][0] + kRescale || top[1] > m[nt][1] + kRescale)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float v = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            const float up = fmaxf(m[nt][x], v);
+            const float f = up == minus_inf() ? 1.f : ex2(m[nt][x] - up);
+            m[nt][x] = up;
+            l[nt][x] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              o[nt][d][2 * x] *= f;
+              o[nt][d][2 * x + 1] *= f;
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float shift = m[nt][x] == minus_inf() ? 0.f : m[nt][x];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p = ex2(s[nt][n][2 * x + e] - shift);
+              s[nt][n][2 * x + e] = p;
+              l[nt][x] += p;
+            }
+        }
+      }
+      uint32_t hi[NT][4], lo[NT][4];  // P and what its rounding leaves, as operands
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p0 = s[nt][n][2 * x], p1 = s[nt][n][2 * x + 1];
+            const uint32_t w = tc::pack2<T>(p0, p1);
+            float h0, h1;
+            tc::unpack2<T>(w, h0, h1);
+            hi[nt][2 * n + x] = w;
+            lo[nt][2 * n + x] = tc::pack2<T>(p0 - h0, p1 - h1);
+          }
+#pragma unroll
+      for (int dd = 0; dd < D / 16; ++dd) {
+        uint32_t vb[4];
+        ldsm_t(vb, vs0 + dd / 4 * C::kBlk + tc::sw128_off(v_row, dd % 4 * 2 + v_piece));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma<T>(o[nt][2 * dd], hi[nt], vb[0], vb[1]);
+          mma<T>(o[nt][2 * dd + 1], hi[nt], vb[2], vb[3]);
+          mma<T>(o[nt][2 * dd], lo[nt], vb[0], vb[1]);
+          mma<T>(o[nt][2 * dd + 1], lo[nt], vb[2], vb[3]);
+        }
+      }
+    }
+    if (!ok) {
+      ring.drain(u);
+      break;
+    }
+    __syncwarp();
+    ring.issue(kKidPagedAttn);
+  }
+
+  // ---- the warps' results, one row tile after the other
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 1);
+      l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 2);
+      if (lim[nt][x] == 0) {  // a row that sees nothing
+        m[nt][x] = minus_inf();
+        l[nt][x] = 0.f;
+      }
+      if (t == 0) {
+        stat[warp][kTile * nt + 8 * x + g][0] = m[nt][x];
+        stat[warp][kTile * nt + 8 * x + g][1] = l[nt][x];
+      }
+    }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");
+  float* red = reinterpret_cast<float*>(smem);  // [warp][16][D + 4]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float M = minus_inf();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][kTile * nt + 8 * x + g][0]);
+      // (a warp that saw nothing but NaN has no maximum and a sum of NaN)
+      const float wgt = m[nt][x] == minus_inf() ? 1.f : ex2(m[nt][x] - M);
+      float* to = red + (warp * kTile + 8 * x + g) * (D + 4) + 2 * t;
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+        *reinterpret_cast<float2*>(to + 8 * d) =
+            lim[nt][x] == 0 ? make_float2(0.f, 0.f) : make_float2(o[nt][d][2 * x] * wgt, o[nt][d][2 * x + 1] * wgt);
+    }
+    __syncthreads();
+    for (int y = threadIdx.x; y < kTile * (D / 4); y += kWarps * 32) {
+      const int q = y / (D / 4), d = y % (D / 4) * 4, r = row0 + kTile * nt + q;
+      if (r >= R) continue;
+      float M = minus_inf(), sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][kTile * nt + q][0]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = stat[w][kTile * nt + q][0], lw = stat[w][kTile * nt + q][1];
+        sum += mw == minus_inf() ? lw : lw * ex2(mw - M);
+        const float4 z = *reinterpret_cast<const float4*>(red + (w * kTile + q) * (D + 4) + d);
+        v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
+      }
+      const int hq = h * a.G + r % a.G, i = r / a.G;
+      const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
+      if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w))
+        v = sum_apart<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M);
+      if (cut.splits > 1) {
+        const int64_t at = row * cut.splits + blockIdx.x;
+        *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;
+        if (d == 0) {
+          float* ml = a.workspace + (int64_t)c.B * a.Hq * c.L * cut.splits * D + 2 * at;
+          ml[0] = M;
+          ml[1] = sum;
+        }
+      } else {
+        const float fold = fold_sink(a.sinks, hq, M, sum), inv = sum == 0.f ? 0.f : fold / sum;
+        T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
+        *reinterpret_cast<uint2*>(out) = make_uint2(tc::pack2<T>(v.x * inv, v.y * inv), tc::pack2<T>(v.z * inv, v.w * inv));
+        if (a.lse && d == 0) a.lse[row] = sum == 0.f ? minus_inf() : (M + log2f(sum)) * kLn2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the chunks of one query row: D/4 threads a chunk, several chunks side by side.
+template <typename T, int D, int kThreads>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedArgs a, Cut cut) {
+  constexpr int U = D / 4, kSide = kThreads / U;
+  __shared__ float4 part[kSide][U];
+  __shared__ float red[kThreads / 32], sums[kThreads / 32];
+  const CacheArgs& c = a.c;
+  const int64_t row = blockIdx.x;
+  const int i = (int)(row % c.L), hq = (int)(row / c.L % a.Hq), b = (int)(row / c.L / a.Hq);
+  const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
+  const int n = (int)(((int64_t)rows.limit(i) + cut.chunk - 1) / cut.chunk);  // chunks that the row sees
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* ml = a.workspace + (int64_t)c.B * a.Hq * c.L * cut.splits * D + 2 * row * cut.splits;
+  float M = minus_inf(), L = 0.f;
+  for (int x = threadIdx.x; x < n; x += kThreads) M = fmaxf(M, ml[2 * x]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, red[w]);
+  // (a chunk without a maximum has a sum of 0, or NaN and outputs of NaN)
+  for (int x = threadIdx.x; x < n; x += kThreads) L += ml[2 * x] == minus_inf() ? ml[2 * x + 1] : ml[2 * x + 1] * ex2(ml[2 * x] - M);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = L;
+  const int side = threadIdx.x / U, d = threadIdx.x % U * 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (side < kSide) {
+#pragma unroll 4
+    for (int x = side; x < n; x += kSide) {
+      const float mx = ml[2 * x], w = mx == minus_inf() ? 1.f : ex2(mx - M);
+      const float4 y = *reinterpret_cast<const float4*>(a.workspace + (row * cut.splits + x) * D + d);
+      v.x = fmaf(w, y.x, v.x);
+      v.y = fmaf(w, y.y, v.y);
+      v.z = fmaf(w, y.z, v.z);
+      v.w = fmaf(w, y.w, v.w);
+    }
+    part[side][d / 4] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x >= U) return;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) L += sums[w];
+  v = part[0][d / 4];
+  for (int x = 1; x < kSide; ++x) {
+    const float4 y = part[x][d / 4];
+    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+  }
+  const float fold = fold_sink(a.sinks, hq, M, L), inv = L == 0.f ? 0.f : fold / L;
+  T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
+  *reinterpret_cast<uint2*>(out) = make_uint2(tc::pack2<T>(v.x * inv, v.y * inv), tc::pack2<T>(v.z * inv, v.w * inv));
+  if (a.lse && d == 0) a.lse[row] = L == 0.f ? minus_inf() : (M + log2f(L)) * kLn2;
+}
+
+// ---- the weights of few rows.  A warp owns its units' tokens, so sums have one order and no atomics.
+template <int D>
+struct WCfg {
+  static constexpr int kNT = D == 256 ? 1 : 2, kRows = kTile * kNT;
+  static constexpr int kWarps = 8, kStages = D == 256 ? 3 : 4;
+  static constexpr int kUnit = (D + 63) / 64 * kTile * 128;
+  static constexpr int kSmem = kWarps * kStages * kUnit + 1024;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(WCfg<D>::kWarps * 32) paged_weights_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, int chunk) {
+  using C = WCfg<D>;
+  constexpr int NT = C::kNT, kWarps = C::kWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kWarps][C::kStages];
+  __shared__ int abort_flag;
+  const CacheArgs& c = a.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedWeights);
+  if (rows.first >= c.L) return;  // no real row
+  const int R = a.G * c.L, start = blockIdx.x * chunk;
+  if (start >= rows.len) return;
+  if (lane < C::kStages) tc::mbar_init(&full[warp][lane], 1);
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) tc::fence_mbar_init();
+  __syncthreads();
+  const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidPagedWeights};
+  const int fresh = rows.len - (c.L - rows.first);  // tokens from here on are the call's own
+  float* weights = a.weights + b * a.w_batch + h * a.w_head;
+  uint32_t phase = 0;
+  bool ok = true;
+  // From the last rows, which see every token, to the first real ones.
+  for (int row0 = (R - 1) / C::kRows * C::kRows; ok && row0 >= 0 && (min(R, row0 + C::kRows) - 1) / a.G >= rows.first; row0 -= C::kRows) {
+    const bool first_pass = row0 + C::kRows >= R;
+    const int i_last = (min(R, row0 + C::kRows) - 1) / a.G;
+    const int end = min(start + chunk, first_pass ? rows.len : rows.limit(i_last));
+    const int all = end > start ? (end - start + kTile - 1) / kTile : 0;
+    Ring<D, kWarps, C::kStages, false> ring{&map, &c, c.pages + b * c.pages_stride, smem + warp * C::kStages * C::kUnit, full[warp], h, start, end,
+                                            warp, lane, all > warp ? (all - warp + kWarps - 1) / kWarps : 0, 0, -1, 0, 0u, phase};
+    ring.look(0, kKidPagedWeights);
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) ring.issue(kKidPagedWeights);
+    uint32_t qa[NT][D / 16][4];
+    int lim[NT][2];
+    float hi[NT][2], lo[NT][2];  // lse·log2(e) in two parts
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = row0 + kTile * nt + 8 * x + g, i = r / a.G;
+        const bool real = r < R && i >= rows.first;
+        const int hq = h * a.G + r % a.G;
+        const float lse = real ? a.lse[((int64_t)b * a.Hq + hq) * c.L + i] : minus_inf();
+        lim[nt][x] = real && lse != minus_inf() ? rows.limit(i) : 0;
+        hi[nt][x] = lse * kLog2e;
+        // (1.93e-8: log2(e) less its fp32 number)
+        lo[nt][x] = fabsf(hi[nt][x]) < __builtin_huge_valf() ? fmaf(lse, kLog2e, -hi[nt][x]) + lse * 1.92596299e-8f : 0.f;
+        const T* q = real ? row_ptr<T>(a.q, a.lq, b, hq, i) + 2 * t : nullptr;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int k8 = 0; k8 < 2; ++k8) qa[nt][ks][x + 2 * k8] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * k8) : 0u;
+      }
+    const int k_row = lane / 16 * 8 + lane % 8, k_piece = lane / 8 % 2;
+    for (int u = 0; u < ring.units; ++u) {
+      const int k0 = ring.pos(u);
+      float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      if (ring.wait(u, ok, wc)) {
+        const uint32_t ks0 = tc::smem_u32(ring.base + u % C::kStages * C::kUnit);
+        float s[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kb[4];
+          ldsm(kb, ks0 + ks / 4 * (kTile * 128) + tc::sw128_off(k_row, ks % 4 * 2 + k_piece));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<T>(s[nt][0], qa[nt][ks], kb[0], kb[1]);
+            mma<T>(s[nt][1], qa[nt][ks], kb[2], kb[3]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = e / 2;
+              const float p = ex2(fmaf(s[nt][n][e], a.scale_log2, -hi[nt][x]) - lo[nt][x]);
+              sum[n][e % 2] += k0 + 8 * n + 2 * t + e % 2 < lim[nt][x] ? p : 0.f;
+            }
+      }
+      if (!ok) {
+        ring.drain(u);
+        break;
+      }
+      __syncwarp();
+      ring.issue(kKidPagedWeights);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off <= 16; off <<= 1) sum[n][e] += __shfl_xor_sync(0xffffffffu, sum[n][e], off);
+          const int key = k0 + 8 * n + 2 * t + e;
+          if (g == 0 && key < end) weights[key] = (first_pass && key >= fresh ? 0.f : weights[key]) + sum[n][e];
+        }
+    }
+    phase = ring.phase;
+    __syncwarp();
+  }
+}
+
+// ---- host
+
+int row_tiles_of(const PagedArgs& a, int rows) { return (a.G * a.c.L + rows - 1) / rows; }
+int rows_a_block(const PagedArgs& a) { return a.c.D == 256 || a.G * a.c.L <= kTile ? kTile : 2 * kTile; }
+
+// How a call's sequences are cut into chunks.
+Cut cut_few(const PagedArgs& a) {
+  const int64_t slots = a.c.num_sms > 0 ? a.c.num_sms : 1;
+  const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * row_tiles_of(a, rows_a_block(a));
+  const int step = 256;
+  const int64_t want = max((int64_t)1, slots / pairs);
+  int64_t chunk = (a.max_len + want - 1) / want;
+  if (pairs * 4 > slots) chunk = min(chunk, (int64_t)2048);
+  chunk = a.max_len <= 512 ? a.max_len : max(chunk, (int64_t)step);
+  const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
+  const int64_t most = max((int64_t)1, ((int64_t)64 << 20) / partial);
+  chunk = max(chunk, (a.max_len + most - 1) / most);
+  Cut cut;
+  cut.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
+  cut.splits = (a.max_len + cut.chunk - 1) / cut.chunk;
+  return cut;
+}
+
+// Sets a kernel's shared-memory limit once on each device.
+template <typename K>
+cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename T, int D, int NT>
+cudaError_t few_nt(const PagedArgs& a, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  auto* kern = paged_few_kernel<T, D, NT>;
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, C::kSmem, ready);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!make_tmap_pages(&map, a.c, kTile)) return cudaErrorInvalidValue;
+  const Cut cut = cut_few(a);
+  const int tiles = row_tiles_of(a, C::kRows);
+  kern<<<dim3(cut.splits, tiles * a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, cut, tiles);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int kThreads>
+cudaError_t join_t(const PagedArgs& a, const Cut& cut, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.c.B * a.Hq * a.c.L));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];  // its blocks may be placed while the last chunks are still running
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, kThreads>, a, cut);
+}
+
+enum class Do { kAttn, kJoin, kWeights };
+
+template <typename T, int D>
+cudaError_t run_d(const PagedArgs& a, Do what, cudaStream_t s) {
+  if (what == Do::kJoin) {
+    const Cut cut = cut_few(a);
+    return cut.splits > 16 ? join_t<T, D, 512>(a, cut, s) : join_t<T, D, 128>(a, cut, s);
+  }
+  if (what == Do::kWeights) {
+    using C = WCfg<D>;
+    auto* kern = paged_weights_kernel<T, D>;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem(kern, C::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    CUtensorMap map;
+    if (!make_tmap_pages(&map, a.c, kTile)) return cudaErrorInvalidValue;
+    const int chunk = 1024;
+    kern<<<dim3((a.max_len + chunk - 1) / chunk, a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, chunk);
+    return cudaGetLastError();
+  }
+  if constexpr (D == 256) return few_nt<T, D, 1>(a, s);
+  else return rows_a_block(a) == kTile ? few_nt<T, D, 1>(a, s) : few_nt<T, D, 2>(a, s);
+}
+
+template <typename T>
+cudaError_t run_t(const PagedArgs& a, Do what, cudaStream_t s) {
+  switch (a.c.D) {
+    case 32: return run_d<T, 32>(a, what, s);
+    case 64: return run_d<T, 64>(a, what, s);
+    case 96: return run_d<T, 96>(a, what, s);
+    case 128: return run_d<T, 128>(a, what, s);
+    case 256: return run_d<T, 256>(a, what, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t run(const PagedArgs& a, int dtype, Do what, cudaStream_t s) {
+  return dtype == 1 ? run_t<__half>(a, what, s) : run_t<__nv_bfloat16>(a, what, s);
+}
+
+}  // namespace
+
+bool paged_attn_launchable(const PagedArgs& a) { return (int64_t)a.c.Hkv * row_tiles_of(a, rows_a_block(a)) <= 65535; }
+size_t paged_attn_workspace(const PagedArgs& a) {
+  const Cut cut = cut_few(a);
+  return cut.splits == 1 ? 0 : (size_t)a.c.B * a.Hq * a.c.L * cut.splits * (a.c.D + 2) * sizeof(float);
+}
+cudaError_t launch_paged_attn(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kAttn, s); }
+cudaError_t launch_paged_join(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kJoin, s); }
+cudaError_t launch_paged_weights(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kWeights, s); }
+
+}  // namespace sdpa
