@@ -2,6 +2,8 @@
 // conventions are documented in include/sdpa.h).
 #pragma once
 
+#include <atomic>
+
 #include "cache.h"
 #include "tc_common.cuh"
 
@@ -35,6 +37,25 @@ cudaError_t launch_paged_write(const CacheArgs& a, cudaStream_t s);
 struct Cut {
   int chunk, splits;
 };
+
+// Attention's form for many rows a KV head.
+bool paged_chunk_takes(const PagedArgs& a);
+Cut paged_chunk_cut(const PagedArgs& a);
+int64_t paged_chunk_blocks(const PagedArgs& a);
+cudaError_t launch_paged_chunk(const PagedArgs& a, int dtype, cudaStream_t s);
+
+// Sets a kernel's shared-memory limit once on each device.
+template <typename K>
+cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 struct EvictArgs {
   CacheArgs c;

@@ -1,0 +1,623 @@
+// Attention over a 16-bit paged cache for many query rows a KV head: TMA + tcgen05 + TMEM
+// (conventions in include/sdpa.h).
+//
+// Rows.  A Q tile of 128 rows holds `tokens` consecutive queries of `heads` query heads of one KV
+// head (row = token·heads + head), the split of the group's heads that needs the fewest tiles, so
+// that short chunks fill a tile with the heads that share its keys, and the rows of a tile end at
+// almost the same token under the causal mask.  One box of the tensor map of q loads them, the same
+// box of the map of out stores them; rows that the split leaves over are zeros.
+// Keys.  A tile of 128 keys is put together from the pages: boxes of as many tokens as page size
+// and tile have in common (16 to 128), one lane each, at the place that the page table names; boxes
+// past the last key, or on a bad page, are loaded from outside the tensor, which fills zeros.  Values
+// behind the sequence's last token are cleared in shared memory before they meet P.
+//
+// The pipeline is that of the dense forward kernel: a block of 12 warps computes two Q tiles;
+// warps 0-3 / 4-7 are the softmax of tile 0 / 1, one thread a row; warp 8 loads; warps 9 / 10
+// issue the MMAs of tile 0 / 1.  S_w = Q_w·K^T goes to TMEM columns [128w, 128w + 128), P_w over its first
+// 64 as the A operand of O_w += P_w·V at columns [256 + 128w, +D), PV in two halves of 64 keys.  The two
+// softmax warpgroups take turns at the exponentials.  The running maximum is raised when a row's
+// maximum grows by 2^8.  Rows that see few keys take P as head and remainder (16 more bits), see split_tile.
+// With few blocks the keys are cut into chunks whose unnormalised results the join kernel adds up.
+#include "paged.h"
+
+namespace sdpa {
+namespace {
+using namespace tc;
+
+constexpr int kBM = 128;        // rows of a Q tile
+constexpr int kBN = 128;        // keys of a KV tile
+constexpr int kStages = 4;      // ring of K and V tiles
+constexpr int kThreads = 384;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+// The block is launched with 168 registers a thread: 128·56 + 256·224 = 384·168.
+constexpr int kRegsLow = 56, kRegsHigh = 224;
+constexpr float kRescale = 8.f;
+
+// How query rows are put into tiles, and keys into boxes and chunks.
+struct Tiling {
+  int heads, tokens;  // of a Q tile
+  int groups;         // of heads: G / heads
+  int blocks;         // of two Q tiles (one for D = 256): queries of a sequence
+  int box;            // tokens of a box of keys
+  Cut cut;
+};
+
+template <int D>
+struct Layout128 {
+  static constexpr int kCB = (D + 63) / 64;  // blocks of 64 elements
+  static constexpr int kTileBytes = kBM * kCB * 128;
+  static constexpr int kQOff = 0, kRingOff = 2 * kTileBytes;
+  static constexpr int kBytes = kRingOff + kStages * kTileBytes + 1024;
+};
+
+struct Bars {
+  uint64_t q_full, kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], mma_done[2], turn[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <typename T>
+constexpr bool kIsBf16 = std::is_same<T, __nv_bfloat16>::value;
+
+// What a block of Q tiles works on.
+struct Work {
+  int b, h, group, i0;  // sequence, KV head, group of its query heads, first query
+  int split, k_lo;      // chunk of keys
+};
+__device__ __forceinline__ Work work_of(const PagedArgs& a, const Tiling& t, int queries) {
+  // All sequences and heads of one block of queries, then the next; under the causal mask the last
+  // (heaviest) queries first, so that the tail of the grid is light.
+  const int units = a.c.B * a.c.Hkv * t.groups;
+  const int unit = blockIdx.x % units, rank = blockIdx.x / units;
+  Work w;
+  w.group = unit % t.groups;
+  w.h = unit / t.groups % a.c.Hkv;
+  w.b = unit / t.groups / a.c.Hkv;
+  w.split = rank % t.cut.splits;
+  w.i0 = (a.causal ? t.blocks - 1 - rank / t.cut.splits : rank / t.cut.splits) * queries;
+  w.k_lo = (int)min((int64_t)w.split * t.cut.chunk, (int64_t)1 << 30);
+  return w;
+}
+
+// One Q tile: its queries [i0, i1), the keys that some row of it sees in this chunk, and those
+// that every real row sees.
+struct Span {
+  int i0, i1, end, least;
+};
+__device__ __forceinline__ Span span_of(const Rows& rows, const Tiling& t, int i0, const Work& w) {
+  Span s;
+  s.i0 = i0;
+  s.i1 = min(rows.L, i0 + t.tokens);
+  const bool any = i0 < s.i1 && s.i1 > rows.first;
+  s.end = any ? (int)min((int64_t)rows.limit(s.i1 - 1), (int64_t)w.k_lo + t.cut.chunk) : 0;
+  s.least = any ? rows.limit(max(i0, rows.first)) : 0;
+  return s;
+}
+__device__ __forceinline__ int tiles_in(const Span& s, int k_lo) { return s.end > k_lo ? (s.end - k_lo + kBN - 1) / kBN : 0; }
+
+// A KV tile takes P as head and remainder where some row may see few keys: |O| can then lie near
+// the largest values, and P's rounding would add to O as much as O's own.
+__device__ __forceinline__ bool split_tile(const Span& s, int k0) { return k0 == 0 && s.least <= kBN; }
+
+// Whether a page table entry that the keys [lo, hi) need is bad (every thread of the block calls it).
+__device__ __forceinline__ bool pages_bad(const CacheArgs& c, int b, int lo, int hi) {
+  bool bad = false;
+  if (hi > lo)
+    for (int e = lo / c.page_size + threadIdx.x; e <= (hi - 1) / c.page_size; e += blockDim.x)
+      bad |= (unsigned)c.pages[b * c.pages_stride + e] >= (unsigned)c.num_pages;
+  if (bad) report_error(c.err, kDevErrIndex, kKidPagedAttn);
+  return __syncthreads_or(bad);
+}
+
+// Coordinates of the box of keys at position pos: its page (past the last one where there is none
+// to read) and its place in it.
+struct Box {
+  int page, place;
+};
+__device__ __forceinline__ Box box_at(const CacheArgs& c, const int* table, int pos, int end) {
+  Box x{c.num_pages, 0};
+  if (pos < end) {
+    const int slot = pos / c.page_size, page = table[slot];
+    x.place = pos - slot * c.page_size;
+    if ((unsigned)page < (unsigned)c.num_pages) x.page = page;
+  }
+  return x;
+}
+
+// Hides the keys of bad pages in a row of scores; returns the factor that the scores then take.
+__device__ __forceinline__ float hide_bad_pages(uint32_t (&sv)[kBN], const CacheArgs& c, const int* table, int k0, int end, float scale2) {
+  const int lane = threadIdx.x % 32, pos = k0 + lane * kTile;
+  const bool fine = lane >= kBN / kTile || pos >= end || (unsigned)table[pos / c.page_size] < (unsigned)c.num_pages;
+  const uint32_t ok = __ballot_sync(0xffffffffu, fine);
+  // (a scale of zero would turn the hidden ones into NaN)
+#pragma unroll
+  for (int e = 0; e < kBN; ++e) {
+    if (scale2 == 0.f) sv[e] = 0u;
+    if (!(ok >> (e / kTile) & 1u)) sv[e] = scale2 < 0.f ? 0x7f800000u : 0xff800000u;
+  }
+  return scale2 == 0.f ? 1.f : scale2;
+}
+
+// Clears row `row` (this thread's) of a V tile if it lies behind the last token.
+template <int kCB>
+__device__ __forceinline__ void clear_behind(uint8_t* tile, int row, int k0, int len) {
+  if (k0 + row >= len) {
+#pragma unroll 1
+    for (int x = 0; x < kCB * 8; ++x) *reinterpret_cast<uint4*>(tile + x / 8 * 16384 + row * 128 + x % 8 * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
+}
+
+// Maximum of c·s over the keys e < lim of a row of scores; -inf without any.
+template <bool kCut>
+__device__ __forceinline__ float row_max(const uint32_t (&sv)[kBN], float c, int lim) {
+  constexpr int kH = kBN / 2;
+  if (kCut && lim <= 0) return minus_inf();
+  const float worst = c >= 0.f ? minus_inf() : -minus_inf();
+  float acc[4] = {worst, worst, worst, worst};
+  if (c >= 0.f) {
+#pragma unroll
+    for (int e = 0; e < kH; ++e)
+      acc[e % 4] = fmax3(acc[e % 4], !kCut || e < lim ? __uint_as_float(sv[e]) : worst, !kCut || kH + e < lim ? __uint_as_float(sv[kH + e]) : worst);
+    return fmaxf(fmaxf(acc[0], acc[1]), fmaxf(acc[2], acc[3])) * c;
+  }
+#pragma unroll
+  for (int e = 0; e < kH; ++e)
+    acc[e % 4] = fmin3(acc[e % 4], !kCut || e < lim ? __uint_as_float(sv[e]) : worst, !kCut || kH + e < lim ? __uint_as_float(sv[kH + e]) : worst);
+  return fminf(fminf(acc[0], acc[1]), fminf(acc[2], acc[3])) * c;
+}
+
+// P = 2^(c·s − m) of a row into TMEM, packed in pairs at columns [0, 64), and its sum.  With kSplit
+// also what the packing leaves, at columns [64, 128).  `half` is told when the first 64 keys are there.
+template <typename T, bool kCut, bool kSplit>
+__device__ __forceinline__ float exponentials(const uint32_t (&sv)[kBN], uint32_t s_addr, float c, float neg_m, int lim, uint64_t* half) {
+  constexpr int kPiece = kSplit ? 16 : 64;  // keys packed at once
+  const uint64_t cc = f2pack(c, c), nm = f2pack(neg_m, neg_m);
+  uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+  for (int q = 0; q < kBN / kPiece; ++q) {
+    uint32_t pk[kPiece / 2], rest[kPiece / 2];
+#pragma unroll
+    for (int e = 0; e < kPiece / 2; ++e) {
+      const int col = kPiece * q + 2 * e;
+      uint64_t x = ffma2(f2pack(__uint_as_float(sv[col]), __uint_as_float(sv[col + 1])), cc, nm);
+      if constexpr (kCut) {
+        float x0, x1;
+        f2unpack(x, x0, x1);
+        x = f2pack(col < lim ? x0 : minus_inf(), col + 1 < lim ? x1 : minus_inf());
+      }
+      float p0, p1;
+      ex2_pair(x, p0, p1);
+      acc[e % 2] = fadd2(acc[e % 2], f2pack(p0, p1));
+      pk[e] = tc::pack2<T>(p0, p1);
+      if constexpr (kSplit) {
+        float h0, h1;
+        unpack2<T>(pk[e], h0, h1);
+        rest[e] = tc::pack2<T>(p0 - h0, p1 - h1);
+      }
+    }
+    if constexpr (kSplit) {
+      tmem_st8(s_addr + 8 * q, pk);
+      tmem_st8(s_addr + 64 + 8 * q, rest);
+    } else {
+      tmem_st32(s_addr + 32 * q, pk);
+      if (q == 0 && half) {
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(half);
+      }
+    }
+  }
+  float a, b, d, e;
+  f2unpack(acc[0], a, b);
+  f2unpack(acc[1], d, e);
+  return (a + b) + (d + e);
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > 100000000ull) return;
+}
+
+// One row's state at the end: writes its output into the staging tile (or its partial result
+// into the workspace) and its logsumexp.
+template <typename T, int D>
+__device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, const Tiling& t, const Rows& rows, const Span& span, int r, uint32_t o_addr,
+                                           uint8_t* stage, float m, float l, bool any) {
+  const int i = span.i0 + r / t.heads, hq = w.h * a.G + w.group * t.heads + r % t.heads;
+  const bool there = r < t.heads * t.tokens && i < span.i1;
+  const int lim = there ? rows.limit(i) : 0;
+  const int to = min(span.end, lim);
+  if (to <= w.k_lo) {  // nothing seen here (what TMEM holds may be anything)
+    m = minus_inf();
+    l = 0.f;
+  }
+  const bool nothing = l == 0.f;
+  const int64_t row = ((int64_t)w.b * a.Hq + hq) * a.c.L + i;
+  float inv = 1.f, m_all = m, l_all = l;
+  if (t.cut.splits == 1 && there) {
+    const float f = fold_sink(a.sinks, hq, m_all, l_all);
+    inv = f / l_all;
+    if (a.lse) a.lse[row] = l_all == 0.f ? minus_inf() : (m_all + log2f(l_all)) * kLn2;
+  }
+  float* part = a.workspace + (row * t.cut.splits + w.split) * D;
+#pragma unroll 1
+  for (int c32 = 0; c32 < D / 32; ++c32) {
+    uint32_t o[32];
+    if (any) {
+      tmem_ld32(o_addr + c32 * 32, o);
+      tmem_ld_wait(o);
+    }
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      if (nothing) o[e] = 0u;
+      odd |= (o[e] & 0x7fffffffu) > 0x7f800000u;
+    }
+    if (odd && l == l) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 x = sum_apart<T, D>(a, w.b, w.h, hq, i, c32 * 32 + e, w.k_lo, to, m);
+        o[e] = __float_as_uint(x.x);
+        o[e + 1] = __float_as_uint(x.y);
+        o[e + 2] = __float_as_uint(x.z);
+        o[e + 3] = __float_as_uint(x.w);
+      }
+    }
+    __syncwarp();
+    if (t.cut.splits > 1) {
+      if (there && to > w.k_lo)
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(part + c32 * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    } else {
+      uint32_t packed[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        packed[e] = nothing ? 0u : tc::pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+      uint8_t* blk = stage + c32 / 2 * 16384;
+#pragma unroll
+      for (int v4 = 0; v4 < 4; ++v4)
+        *reinterpret_cast<uint4*>(blk + sw128_off(r, c32 % 2 * 4 + v4)) = make_uint4(packed[4 * v4], packed[4 * v4 + 1], packed[4 * v4 + 2], packed[4 * v4 + 3]);
+    }
+  }
+  if (t.cut.splits > 1 && there && to > w.k_lo) {
+    float* ml = a.workspace + (int64_t)a.c.B * a.Hq * a.c.L * t.cut.splits * D + 2 * (row * t.cut.splits + w.split);
+    ml[0] = m;
+    ml[1] = l;
+  }
+}
+
+// Clears the rows of a Q tile that its box does not fill.
+template <int kCB>
+__device__ __forceinline__ void clear_unused(uint8_t* tile, const Tiling& t) {
+  const int used = t.heads * t.tokens, n = (kBM - used) * 8;
+  for (int x = threadIdx.x; x < n * kCB; x += blockDim.x)
+    *reinterpret_cast<uint4*>(tile + x / n * 16384 + used * 128 + x % n * 16) = make_uint4(0, 0, 0, 0);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkv, const __grid_constant__ CUtensorMap to,
+                       PagedArgs a, Tiling t) {
+  using L = Layout128<D>;
+  constexpr int kCB = L::kCB;
+  constexpr uint32_t kIdS = idesc_f16(kBM, kBN, kIsBf16<T>, false, false);
+  constexpr uint32_t kIdO = idesc_f16(kBM, D, kIsBf16<T>, false, true);
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars bars;
+  const CacheArgs& c = a.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Work work = work_of(a, t, 2 * t.tokens);
+  const Rows rows = rows_of(c, work.b, a.causal, a.max_len, kKidPagedAttn);
+  const Span span[2] = {span_of(rows, t, work.i0, work), span_of(rows, t, work.i0 + t.tokens, work)};
+  const int nkv[2] = {tiles_in(span[0], work.k_lo), tiles_in(span[1], work.k_lo)};
+  const int nmax = max(nkv[0], nkv[1]), end = max(span[0].end, span[1].end);
+  if (nmax == 0 && t.cut.splits > 1) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    return;
+  }
+  if (threadIdx.x == 0) {
+    bars.abort = 0;
+    mbar_init(&bars.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars.kv_full[s], 1);
+      mbar_init(&bars.kv_empty[s], 2);  // both issuers
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bars.s_full[w], 1);
+      mbar_init(&bars.p_half[w], kBM);
+      mbar_init(&bars.p_full[w], kBM);
+      mbar_init(&bars.o_done[w], 1);
+      mbar_init(&bars.mma_done[w], 1);
+      mbar_init(&bars.turn[w], 4);  // one arrival a warp of the other warpgroup
+    }
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars.tmem_base, 512);
+    tmem_relinquish();
+  }
+  for (int w = 0; w < 2; ++w) clear_unused<kCB>(sm + L::kQOff + w * L::kTileBytes, t);
+  fence_async_smem();
+  tc_fence_before();
+  const bool bad_pages = pages_bad(c, work.b, work.k_lo, end);  // also the block's barrier
+  tc_fence_after();
+  const uint32_t tbase = bars.tmem_base;
+  const int* table = c.pages + work.b * c.pages_stride;
+  const WaitCtx wc{&bars.abort, 0, a.wait_limit_ns, c.err, kKidPagedAttn};
+  if (warp >= 8) regs_dec<kRegsLow>();
+
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      prefetch_tmap(&tq);
+      prefetch_tmap(&tkv);
+      prefetch_tmap(&to);
+      const int nq = span[1].i0 < c.L ? 2 : 1;
+      mbar_arrive_expect_tx(&bars.q_full, nq * kCB * t.heads * t.tokens * 128);
+      for (int w = 0; w < nq; ++w)
+        for (int cb = 0; cb < kCB; ++cb)
+          tma_load_4d(sm + L::kQOff + w * L::kTileBytes + cb * 16384, &tq, &bars.q_full, cb * 64, work.h * a.G + work.group * t.heads, span[w].i0, work.b);
+    }
+    __syncwarp();
+    // Lane x loads box x / kCB of a tile, column block x % kCB.
+    const int boxes = kBN / t.box, box = lane / kCB, cb = lane % kCB;
+    const bool mine = lane < boxes * kCB;
+    int issued = 0;
+    bool ok = true;
+    Box at = box_at(c, table, work.k_lo + box * t.box, mine ? end : 0);
+    for (int j = 0; ok && j < nmax; ++j) {
+      const Box next = box_at(c, table, work.k_lo + (j + 1) * kBN + box * t.box, mine ? end : 0);
+      for (int kv = 0; kv < 2; ++kv) {
+        const int it = 2 * j + kv, s = it % kStages;
+        ok = __all_sync(kAll, mbar_wait(&bars.kv_empty[s], ((it / kStages) & 1) ^ 1, wc));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[s], L::kTileBytes);
+        __syncwarp();
+        if (mine)
+          tma_load_4d(sm + L::kRingOff + s * L::kTileBytes + cb * 16384 + box * t.box * 128, &tkv, &bars.kv_full[s], cb * 64, at.place, kv * c.Hkv + work.h, at.page);
+        issued = it + 1;
+      }
+      at = next;
+    }
+    if (!ok || bars.abort)  // copies still in flight land before the block exits
+      for (int it = max(0, issued - kStages); it < issued; ++it) drain_wait(&bars.kv_full[it % kStages], (it / kStages) & 1);
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    const int w = __shfl_sync(kAll, warp - kMmaWarp, 0);
+    const int nkv_w = w == 0 ? nkv[0] : nkv[1];
+    const bool few = w == 0 ? split_tile(span[0], work.k_lo) : split_tile(span[1], work.k_lo);  // of the first KV tile
+    bool ok = __all_sync(kAll, mbar_wait(&bars.q_full, 0, wc));
+    tc_fence_after();
+    const uint64_t qd = sdesc_sw128(smem_u32(sm + L::kQOff) + w * L::kTileBytes, 16, 1024);
+    const uint32_t ring = smem_u32(sm + L::kRingOff);
+    const uint32_t s_tm = tbase + w * 128, o_tm = tbase + 256 + w * 128;
+    auto scores = [&](int stage) {
+      const uint64_t kd = sdesc_sw128(ring + stage * L::kTileBytes, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
+        mma_ss_w(s_tm, sdesc_advance(qd, off), sdesc_advance(kd, off), kIdS, kk > 0);
+      }
+    };
+    auto values = [&](int stage, int hi, uint32_t p_tm, bool first) {  // keys [64·hi, 64·hi + 64)
+      const uint64_t vd = sdesc_sw128(ring + stage * L::kTileBytes, 16384, 1024);
+#pragma unroll
+      for (int kk = 4 * hi; kk < 4 * hi + 4; ++kk) mma_ts_w(o_tm, p_tm + kk * 8, sdesc_advance(vd, kk * 2048), kIdO, (!first || kk > 0) ? 1u : 0u);
+    };
+    if (ok && nmax > 0) {
+      ok = __all_sync(kAll, mbar_wait(&bars.kv_full[0], 0, wc));
+      if (ok && nkv_w > 0) {
+        tc_fence_after();
+        scores(0);
+        mma_commit_w(&bars.s_full[w]);
+      }
+      if (ok) mma_commit_w(&bars.kv_empty[0]);
+    }
+    // Every use of a ring stage gets one arrival from each issuer, in order.
+    for (int j = 0; ok && j < nmax; ++j) {
+      const int itv = 2 * j + 1, itk = 2 * j + 2, sv = itv % kStages, sk = itk % kStages;
+      const bool act = j < nkv_w, split = act && j == 0 && few;
+      if (!(ok = __all_sync(kAll, mbar_wait(&bars.kv_full[sv], (itv / kStages) & 1, wc)))) break;
+      if (act) {
+        if (!(ok = __all_sync(kAll, mbar_wait(split ? &bars.p_full[w] : &bars.p_half[w], j & 1, wc)))) break;
+        tc_fence_after();
+        values(sv, 0, s_tm, j == 0);
+        if (!split) {
+          if (!(ok = __all_sync(kAll, mbar_wait(&bars.p_full[w], j & 1, wc)))) break;
+          tc_fence_after();
+        }
+        values(sv, 1, s_tm, false);
+        if (split) {
+          values(sv, 0, s_tm + 64, false);
+          values(sv, 1, s_tm + 64, false);
+        }
+        mma_commit_w(&bars.o_done[w]);
+      }
+      mma_commit_w(&bars.kv_empty[sv]);
+      if (j + 1 < nmax) {
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.kv_full[sk], (itk / kStages) & 1, wc)))) break;
+        if (j + 1 < nkv_w) {
+          if (!(ok = __all_sync(kAll, mbar_wait(&bars.o_done[w], j & 1, wc)))) break;  // P(j) consumed
+          tc_fence_after();
+          scores(sk);
+          mma_commit_w(&bars.s_full[w]);
+        }
+        mma_commit_w(&bars.kv_empty[sk]);
+      }
+    }
+    mma_commit_w(&bars.mma_done[w]);
+    drain_wait(&bars.mma_done[w], 0);
+  } else if (warp < 8) {
+    regs_inc<kRegsHigh>();
+    const int w = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+    const Span sp = w == 0 ? span[0] : span[1];
+    const int mine = w == 0 ? nkv[0] : nkv[1], nboth = min(nkv[0], nkv[1]);
+    const uint32_t s_addr = tmem_addr(tbase, quarter * 32, w * 128), o_addr = tmem_addr(tbase, quarter * 32, 256 + w * 128);
+    const int i = sp.i0 + r / t.heads;
+    const int limit = r < t.heads * t.tokens && i < sp.i1 ? rows.limit(i) : 0;
+    float m = minus_inf(), l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < mine; ++j) {
+      const int k0 = work.k_lo + j * kBN;
+      if (!(ok = __all_sync(kAll, mbar_wait(&bars.s_full[w], j & 1, wc)))) break;
+      tc_fence_after();
+      uint32_t sv[kBN];
+#pragma unroll
+      for (int q4 = 0; q4 < kBN / 32; ++q4) tmem_ld32(s_addr + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q4]));
+      tmem_ld_wait(sv);
+      const bool cut = k0 + kBN > sp.least;
+      const int lim = min(limit - k0, kBN);
+      float cs = a.scale_log2;
+      if (bad_pages) cs = hide_bad_pages(sv, c, table, k0, end, cs);
+      const float top = cut ? row_max<true>(sv, cs, lim) : row_max<false>(sv, cs, lim);
+      const float m_new = fmaxf(m, top);
+      const bool up = m_new > m + kRescale;
+      const float alpha = up ? ex2(m - m_new) : 1.f;  // 0 when m was -inf
+      if (up) {
+        l *= alpha;
+        m = m_new;
+      }
+      if (j > 0 && __any_sync(kAll, up)) {  // rescale O once PV(j-1) has landed
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.o_done[w], (j - 1) & 1, wc)))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c32 = 0; c32 < D / 32; ++c32) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c32 * 32, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(o_addr + c32 * 32, o);
+        }
+        tmem_st_wait();
+      }
+      if (k0 + kBN > rows.len) {  // values behind the last token
+        const int itv = 2 * j + 1;
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.kv_full[itv % kStages], (itv / kStages) & 1, wc)))) break;
+        clear_behind<kCB>(sm + L::kRingOff + itv % kStages * L::kTileBytes, r, k0, rows.len);
+      }
+      if (j < nboth && (w == 1 || j > 0))
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.turn[w], (w == 1 ? j : j - 1) & 1, wc)))) break;
+      const float neg_m = m == minus_inf() ? 0.f : -m;  // (nothing seen so far: P = 0 under any finite shift)
+      const bool split = j == 0 && split_tile(sp, k0);
+      if (split) l += exponentials<T, true, true>(sv, s_addr, cs, neg_m, lim, nullptr);
+      else if (cut) l += exponentials<T, true, false>(sv, s_addr, cs, neg_m, lim, &bars.p_half[w]);
+      else l += exponentials<T, false, false>(sv, s_addr, cs, neg_m, lim, &bars.p_half[w]);
+      tmem_st_wait();
+      tc_fence_before();
+      if (split) mbar_arrive(&bars.p_half[w]);  // one phase a tile
+      // The turn goes to the other tile before P is announced: then no warp's arrival for the next
+      // KV tile can count for this one.
+      if (j < nboth - w) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.turn[1 - w]);
+      }
+      mbar_arrive(&bars.p_full[w]);
+    }
+    if (ok && mine > 0) ok = __all_sync(kAll, mbar_wait(&bars.o_done[w], (mine - 1) & 1, wc));
+    // Output rows are staged in the tile's Q buffer, whose last reader has finished.  (A tile
+    // without keys may still have its queries on their way.)
+    if (ok) ok = __all_sync(kAll, mbar_wait(&bars.q_full, 0, wc));
+    if (sp.i0 < c.L) {
+      uint8_t* stage = sm + L::kQOff + w * L::kTileBytes;
+      if (ok) {
+        tc_fence_after();
+        finish_row<T, D>(a, work, t, rows, sp, r, o_addr, stage, m, l, mine > 0);
+        fence_async_smem();
+      }
+      if (named_sync_and(1 + w, kBM, ok) && r == 0 && t.cut.splits == 1) {
+        for (int cb = 0; cb < kCB; ++cb) tma_store_4d(&to, stage + cb * 16384, cb * 64, work.h * a.G + work.group * t.heads, sp.i0, work.b);
+        bulk_commit();
+        bulk_wait_read();
+      }
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ---- host
+
+// The split of the heads that share a KV head into tiles that takes the fewest tiles; of equal
+// ones the one with the most heads, whose rows end closest together.
+Tiling tiling_of(const PagedArgs& a) {
+  Tiling t = {};
+  int64_t best = INT64_MAX;
+  for (int heads = min(a.G, kBM); heads >= 1; --heads) {
+    if (a.G % heads) continue;
+    const int tokens = kBM / heads;
+    const int64_t tiles = (int64_t)(a.G / heads) * ((a.c.L + tokens - 1) / tokens);
+    if (tiles < best) {
+      best = tiles;
+      t.heads = heads;
+      t.tokens = tokens;
+    }
+  }
+  t.groups = a.G / t.heads;
+  const int queries = (a.c.D == 256 ? 1 : 2) * t.tokens;
+  t.blocks = (a.c.L + queries - 1) / queries;
+  t.box = a.c.D == 256 ? 64 : 128;
+  while (a.c.page_size % t.box) t.box /= 2;
+  // Few blocks: chunks of at least 512 keys, enough of them to fill the device, in 64 MiB of partial results.
+  const int64_t blocks = (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks, sms = a.c.num_sms > 0 ? a.c.num_sms : 1;
+  const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
+  int64_t splits = min(max((int64_t)1, sms / blocks), max((int64_t)1, ((int64_t)64 << 20) / partial));
+  splits = max((int64_t)1, min(splits, (int64_t)a.max_len / 512));
+  const int64_t chunk = ((a.max_len + splits - 1) / splits + kBN - 1) / kBN * kBN;
+  t.cut.chunk = (int)min(chunk, (int64_t)1 << 30);
+  t.cut.splits = (int)((a.max_len + t.cut.chunk - 1) / t.cut.chunk);
+  return t;
+}
+
+// Map of q or out: boxes of `heads` heads of `tokens` rows.
+bool make_tmap_rows(CUtensorMap* map, const void* base, const PagedArgs& a, const Layout& l, const Tiling& t) {
+  const int64_t dims[4] = {a.c.D, a.Hq, a.c.L, a.c.B}, strides[3] = {l.sh, l.sl, l.sb};
+  const int box[4] = {64, t.heads, t.tokens, 1};
+  return make_tmap_box(map, base, dims, strides, box);
+}
+
+template <typename T, int D>
+cudaError_t chunk_d(const PagedArgs& a, cudaStream_t s) {
+  const Tiling t = tiling_of(a);
+  CUtensorMap tq, tkv, to;
+  if (!make_tmap_rows(&tq, a.q, a, a.lq, t) || !make_tmap_rows(&to, a.out, a, a.lo, t) || !make_tmap_pages(&tkv, a.c, t.box)) return cudaErrorInvalidValue;
+  auto* kern = paged_chunk_kernel<T, D>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(kern, Layout128<D>::kBytes, ready);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks * t.cut.splits), kThreads, Layout128<D>::kBytes, s>>>(tq, tkv, to, a, t);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t chunk_t(const PagedArgs& a, cudaStream_t s) {
+  switch (a.c.D) {
+    case 32: return chunk_d<T, 32>(a, s);
+    case 64: return chunk_d<T, 64>(a, s);
+    case 96: return chunk_d<T, 96>(a, s);
+    case 128: return chunk_d<T, 128>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+bool paged_chunk_takes(const PagedArgs& a) { return a.c.D <= 128 && a.G * (int64_t)a.c.L > 32; }
+Cut paged_chunk_cut(const PagedArgs& a) { return tiling_of(a).cut; }
+int64_t paged_chunk_blocks(const PagedArgs& a) {
+  const Tiling t = tiling_of(a);
+  return (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks * t.cut.splits;
+}
+cudaError_t launch_paged_chunk(const PagedArgs& a, int dtype, cudaStream_t s) {
+  return dtype == 1 ? chunk_t<__half>(a, s) : chunk_t<__nv_bfloat16>(a, s);
+}
+
+}  // namespace sdpa

@@ -15,8 +15,6 @@
 // The running maximum is raised only when a score passes it by 2^8: one vote a unit, no shuffles.
 // An output that is NaN without a reason in its row's scores has met a value that is not finite,
 // perhaps one that its row does not see: it is summed anew, one product after the other.
-#include <atomic>
-
 #include "paged.h"
 
 namespace sdpa {
@@ -582,18 +580,7 @@ Cut cut_few(const PagedArgs& a) {
   return cut;
 }
 
-// Sets a kernel's shared-memory limit once on each device.
-template <typename K>
-cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
+Cut cut_of(const PagedArgs& a) { return paged_chunk_takes(a) ? paged_chunk_cut(a) : cut_few(a); }
 
 template <typename T, int D, int NT>
 cudaError_t few_nt(const PagedArgs& a, cudaStream_t s) {
@@ -629,7 +616,7 @@ enum class Do { kAttn, kJoin, kWeights };
 template <typename T, int D>
 cudaError_t run_d(const PagedArgs& a, Do what, cudaStream_t s) {
   if (what == Do::kJoin) {
-    const Cut cut = cut_few(a);
+    const Cut cut = cut_of(a);
     return cut.splits > 16 ? join_t<T, D, 512>(a, cut, s) : join_t<T, D, 128>(a, cut, s);
   }
   if (what == Do::kWeights) {
@@ -666,12 +653,17 @@ cudaError_t run(const PagedArgs& a, int dtype, Do what, cudaStream_t s) {
 
 }  // namespace
 
-bool paged_attn_launchable(const PagedArgs& a) { return (int64_t)a.c.Hkv * row_tiles_of(a, rows_a_block(a)) <= 65535; }
+bool paged_attn_launchable(const PagedArgs& a) {
+  if (paged_chunk_takes(a)) return paged_chunk_blocks(a) <= 0x7fffffff;
+  return (int64_t)a.c.Hkv * row_tiles_of(a, rows_a_block(a)) <= 65535;
+}
 size_t paged_attn_workspace(const PagedArgs& a) {
-  const Cut cut = cut_few(a);
+  const Cut cut = cut_of(a);
   return cut.splits == 1 ? 0 : (size_t)a.c.B * a.Hq * a.c.L * cut.splits * (a.c.D + 2) * sizeof(float);
 }
-cudaError_t launch_paged_attn(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kAttn, s); }
+cudaError_t launch_paged_attn(const PagedArgs& a, int dtype, cudaStream_t s) {
+  return paged_chunk_takes(a) ? launch_paged_chunk(a, dtype, s) : run(a, dtype, Do::kAttn, s);
+}
 cudaError_t launch_paged_join(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kJoin, s); }
 cudaError_t launch_paged_weights(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kWeights, s); }
 

@@ -409,6 +409,9 @@ __device__ __forceinline__ void ex2_pair(uint64_t x, float& p0, float& p1) {
 // false if the driver refuses it.
 bool make_tmap_4d(CUtensorMap* map, const void* base, int D, int rows, int heads, int batch, const Layout& l,
                   int box_rows);
+// 4-D tiled map over a 16-bit tensor of dims[0] contiguous elements and three more dimensions of
+// `strides` elements, boxes of `box`, the rest as make_tmap_4d.
+bool make_tmap_box(CUtensorMap* map, const void* base, const int64_t (&dims)[4], const int64_t (&strides)[3], const int (&box)[4]);
 // 4-D tiled map over the attention mask of p ({Lkv, Lq, Hq, B} with the mask's element
 // strides; broadcast dimensions get extent 1), elements of elem_bytes (1: boolean bytes,
 // 2: 16-bit additive values), box {box_keys, box_rows, 1, 1}, the 128-byte swizzle if
