@@ -43,6 +43,9 @@ bool paged_chunk_takes(const PagedArgs& a);
 Cut paged_chunk_cut(const PagedArgs& a);
 int64_t paged_chunk_blocks(const PagedArgs& a);
 cudaError_t launch_paged_chunk(const PagedArgs& a, int dtype, cudaStream_t s);
+// And the weights'.
+bool paged_gain_takes(const PagedArgs& a);
+cudaError_t launch_paged_gain(const PagedArgs& a, int dtype, cudaStream_t s);
 
 // Sets a kernel's shared-memory limit once on each device.
 template <typename K>

@@ -18,29 +18,18 @@
 // softmax warpgroups take turns at the exponentials.  The running maximum is raised when a row's
 // maximum grows by 2^8.  Rows that see few keys take P as head and remainder (16 more bits), see split_tile.
 // With few blocks the keys are cut into chunks whose unnormalised results the join kernel adds up.
-#include "paged.h"
+#include "paged_tc.cuh"
 
 namespace sdpa {
 namespace {
 using namespace tc;
 
-constexpr int kBM = 128;        // rows of a Q tile
-constexpr int kBN = 128;        // keys of a KV tile
 constexpr int kStages = 4;      // ring of K and V tiles
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 // The block is launched with 168 registers a thread: 128·56 + 256·224 = 384·168.
 constexpr int kRegsLow = 56, kRegsHigh = 224;
 constexpr float kRescale = 8.f;
-
-// How query rows are put into tiles, and keys into boxes and chunks.
-struct Tiling {
-  int heads, tokens;  // of a Q tile
-  int groups;         // of heads: G / heads
-  int blocks;         // of two Q tiles (one for D = 256): queries of a sequence
-  int box;            // tokens of a box of keys
-  Cut cut;
-};
 
 template <int D>
 struct Layout128 {
@@ -56,9 +45,6 @@ struct Bars {
   uint32_t tmem_base;
   int abort;
 };
-
-template <typename T>
-constexpr bool kIsBf16 = std::is_same<T, __nv_bfloat16>::value;
 
 // What a block of Q tiles works on.
 struct Work {
@@ -108,21 +94,6 @@ __device__ __forceinline__ bool pages_bad(const CacheArgs& c, int b, int lo, int
       bad |= (unsigned)c.pages[b * c.pages_stride + e] >= (unsigned)c.num_pages;
   if (bad) report_error(c.err, kDevErrIndex, kKidPagedAttn);
   return __syncthreads_or(bad);
-}
-
-// Coordinates of the box of keys at position pos: its page (past the last one where there is none
-// to read) and its place in it.
-struct Box {
-  int page, place;
-};
-__device__ __forceinline__ Box box_at(const CacheArgs& c, const int* table, int pos, int end) {
-  Box x{c.num_pages, 0};
-  if (pos < end) {
-    const int slot = pos / c.page_size, page = table[slot];
-    x.place = pos - slot * c.page_size;
-    if ((unsigned)page < (unsigned)c.num_pages) x.page = page;
-  }
-  return x;
 }
 
 // Hides the keys of bad pages in a row of scores; returns the factor that the scores then take.
@@ -215,12 +186,6 @@ __device__ __forceinline__ float exponentials(const uint32_t (&sv)[kBN], uint32_
   return (a + b) + (d + e);
 }
 
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer() - t0 > 100000000ull) return;
-}
-
 // One row's state at the end: writes its output into the staging tile (or its partial result
 // into the workspace) and its logsumexp.
 template <typename T, int D>
@@ -287,14 +252,6 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, co
     ml[0] = m;
     ml[1] = l;
   }
-}
-
-// Clears the rows of a Q tile that its box does not fill.
-template <int kCB>
-__device__ __forceinline__ void clear_unused(uint8_t* tile, const Tiling& t) {
-  const int used = t.heads * t.tokens, n = (kBM - used) * 8;
-  for (int x = threadIdx.x; x < n * kCB; x += blockDim.x)
-    *reinterpret_cast<uint4*>(tile + x / n * 16384 + used * 128 + x % n * 16) = make_uint4(0, 0, 0, 0);
 }
 
 template <typename T, int D>
@@ -546,47 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- host
 
-// The split of the heads that share a KV head into tiles that takes the fewest tiles; of equal
-// ones the one with the most heads, whose rows end closest together.
-Tiling tiling_of(const PagedArgs& a) {
-  Tiling t = {};
-  int64_t best = INT64_MAX;
-  for (int heads = min(a.G, kBM); heads >= 1; --heads) {
-    if (a.G % heads) continue;
-    const int tokens = kBM / heads;
-    const int64_t tiles = (int64_t)(a.G / heads) * ((a.c.L + tokens - 1) / tokens);
-    if (tiles < best) {
-      best = tiles;
-      t.heads = heads;
-      t.tokens = tokens;
-    }
-  }
-  t.groups = a.G / t.heads;
-  const int queries = (a.c.D == 256 ? 1 : 2) * t.tokens;
-  t.blocks = (a.c.L + queries - 1) / queries;
-  t.box = a.c.D == 256 ? 64 : 128;
-  while (a.c.page_size % t.box) t.box /= 2;
-  // Few blocks: chunks of at least 512 keys, enough of them to fill the device, in 64 MiB of partial results.
-  const int64_t blocks = (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks, sms = a.c.num_sms > 0 ? a.c.num_sms : 1;
-  const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
-  int64_t splits = min(max((int64_t)1, sms / blocks), max((int64_t)1, ((int64_t)64 << 20) / partial));
-  splits = max((int64_t)1, min(splits, (int64_t)a.max_len / 512));
-  const int64_t chunk = ((a.max_len + splits - 1) / splits + kBN - 1) / kBN * kBN;
-  t.cut.chunk = (int)min(chunk, (int64_t)1 << 30);
-  t.cut.splits = (int)((a.max_len + t.cut.chunk - 1) / t.cut.chunk);
-  return t;
-}
-
-// Map of q or out: boxes of `heads` heads of `tokens` rows.
-bool make_tmap_rows(CUtensorMap* map, const void* base, const PagedArgs& a, const Layout& l, const Tiling& t) {
-  const int64_t dims[4] = {a.c.D, a.Hq, a.c.L, a.c.B}, strides[3] = {l.sh, l.sl, l.sb};
-  const int box[4] = {64, t.heads, t.tokens, 1};
-  return make_tmap_box(map, base, dims, strides, box);
-}
-
 template <typename T, int D>
 cudaError_t chunk_d(const PagedArgs& a, cudaStream_t s) {
-  const Tiling t = tiling_of(a);
+  const Tiling t = paged_tiling(a);
   CUtensorMap tq, tkv, to;
   if (!make_tmap_rows(&tq, a.q, a, a.lq, t) || !make_tmap_rows(&to, a.out, a, a.lo, t) || !make_tmap_pages(&tkv, a.c, t.box)) return cudaErrorInvalidValue;
   auto* kern = paged_chunk_kernel<T, D>;
@@ -610,10 +529,41 @@ cudaError_t chunk_t(const PagedArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// The split of the heads that share a KV head into tiles that takes the fewest tiles; of equal
+// ones the one with the most heads, whose rows end closest together.
+tc::Tiling paged_tiling(const PagedArgs& a) {
+  tc::Tiling t = {};
+  int64_t best = INT64_MAX;
+  for (int heads = min(a.G, tc::kBM); heads >= 1; --heads) {
+    if (a.G % heads) continue;
+    const int tokens = tc::kBM / heads;
+    const int64_t tiles = (int64_t)(a.G / heads) * ((a.c.L + tokens - 1) / tokens);
+    if (tiles < best) {
+      best = tiles;
+      t.heads = heads;
+      t.tokens = tokens;
+    }
+  }
+  t.groups = a.G / t.heads;
+  const int queries = (a.c.D == 256 ? 1 : 2) * t.tokens;
+  t.blocks = (a.c.L + queries - 1) / queries;
+  t.box = a.c.D == 256 ? 64 : 128;
+  while (a.c.page_size % t.box) t.box /= 2;
+  // Few blocks: chunks of at least 512 keys, enough of them to fill the device, in 64 MiB of partial results.
+  const int64_t blocks = (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks, sms = a.c.num_sms > 0 ? a.c.num_sms : 1;
+  const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
+  int64_t splits = min(max((int64_t)1, sms / blocks), max((int64_t)1, ((int64_t)64 << 20) / partial));
+  splits = max((int64_t)1, min(splits, (int64_t)a.max_len / 512));
+  const int64_t chunk = ((a.max_len + splits - 1) / splits + tc::kBN - 1) / tc::kBN * tc::kBN;
+  t.cut.chunk = (int)min(chunk, (int64_t)1 << 30);
+  t.cut.splits = (int)((a.max_len + t.cut.chunk - 1) / t.cut.chunk);
+  return t;
+}
+
 bool paged_chunk_takes(const PagedArgs& a) { return a.c.D <= 128 && a.G * (int64_t)a.c.L > 32; }
-Cut paged_chunk_cut(const PagedArgs& a) { return tiling_of(a).cut; }
+Cut paged_chunk_cut(const PagedArgs& a) { return paged_tiling(a).cut; }
 int64_t paged_chunk_blocks(const PagedArgs& a) {
-  const Tiling t = tiling_of(a);
+  const tc::Tiling t = paged_tiling(a);
   return (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks * t.cut.splits;
 }
 cudaError_t launch_paged_chunk(const PagedArgs& a, int dtype, cudaStream_t s) {

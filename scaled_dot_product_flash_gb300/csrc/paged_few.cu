@@ -665,6 +665,8 @@ cudaError_t launch_paged_attn(const PagedArgs& a, int dtype, cudaStream_t s) {
   return paged_chunk_takes(a) ? launch_paged_chunk(a, dtype, s) : run(a, dtype, Do::kAttn, s);
 }
 cudaError_t launch_paged_join(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kJoin, s); }
-cudaError_t launch_paged_weights(const PagedArgs& a, int dtype, cudaStream_t s) { return run(a, dtype, Do::kWeights, s); }
+cudaError_t launch_paged_weights(const PagedArgs& a, int dtype, cudaStream_t s) {
+  return paged_gain_takes(a) ? launch_paged_gain(a, dtype, s) : run(a, dtype, Do::kWeights, s);
+}
 
 }  // namespace sdpa
