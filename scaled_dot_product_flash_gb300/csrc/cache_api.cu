@@ -422,7 +422,8 @@ extern "C" int sdpa_paged_evict(const sdpa_cache_t* cache, const float* weights,
   if (!weights || !new_weights || !weight_strides || !new_lens || !kept || !aligned4(weights) || !aligned4(new_weights) || !aligned4(new_lens) || !aligned4(kept))
     return SDPA_ERR_INVALID_ARG;
   if (budget < 1 || recent < 0 || recent > budget) return SDPA_ERR_INVALID_ARG;
-  if (budget > 1 << 30 || (int64_t)2 * a.c.Hkv > 65535) return SDPA_ERR_UNSUPPORTED;
+  // (rows of the whole cache are numbered in 32 bits)
+  if (budget > 1 << 30 || (int64_t)2 * a.c.Hkv > 65535 || (double)a.c.num_pages * 2 * a.c.Hkv * a.c.page_size >= 4294967296.0) return SDPA_ERR_UNSUPPORTED;
   const size_t wb = weight_bytes(B, a.c.Hkv, slots, weight_strides[0], weight_strides[1]);
   const size_t nb = weight_bytes(B, a.c.Hkv, slots, weight_strides[2], weight_strides[3]);
   if (!wb || !nb) return SDPA_ERR_INVALID_ARG;
@@ -451,6 +452,7 @@ extern "C" int sdpa_paged_evict(const sdpa_cache_t* cache, const float* weights,
   a.budget = budget;
   a.recent = recent;
   a.slots = slots;
+  a.by_page = divider(a.c.page_size);
   if ((st = error_word(&a.c.err)) != SDPA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_one(SDPA_KERNEL_PAGED_SELECT, s, [&] { return launch_paged_select(a, s); });

@@ -47,6 +47,20 @@ cudaError_t launch_paged_chunk(const PagedArgs& a, int dtype, cudaStream_t s);
 bool paged_gain_takes(const PagedArgs& a);
 cudaError_t launch_paged_gain(const PagedArgs& a, int dtype, cudaStream_t s);
 
+// Division of numbers below 2^31 by a divisor that a call fixes: with l = ceil(log2 d) and
+// m = floor(2^(31+l) / d) + 1, n / d = floor(n·m / 2^(31+l)), since m·d exceeds 2^(31+l) by d <= 2^l
+// at most and n < 2^31.
+struct Divider {
+  uint32_t m;
+  int shift;  // l - 1; a divisor of 1 has shift -1
+  __device__ __forceinline__ int operator()(int n) const { return shift < 0 ? n : (int)(__umulhi((uint32_t)n, m) >> shift); }
+};
+inline Divider divider(int d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  return Divider{(uint32_t)(((uint64_t)1 << (31 + l)) / d + 1), l - 1};
+}
+
 // Sets a kernel's shared-memory limit once on each device.
 template <typename K>
 cudaError_t allow_smem(K* kern, int bytes, std::atomic<uint64_t>& ready) {
@@ -68,6 +82,7 @@ struct EvictArgs {
   int* kept;      // [B][Hkv][budget]
   int* new_lens;  // [B]
   int budget, recent, slots;  // slots: entries of a row of weights
+  Divider by_page;            // by page_size
 };
 cudaError_t launch_paged_select(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_paged_move(const EvictArgs& a, cudaStream_t s);
