@@ -33,9 +33,11 @@ cudaError_t launch_paged_join(const PagedArgs& a, int dtype, cudaStream_t s);  /
 cudaError_t launch_paged_weights(const PagedArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_paged_write(const CacheArgs& a, cudaStream_t s);
 
-// Partial results of attention: how many chunks of how many tokens.
+// How attention's first `rows` queries of each sequence are cut: into `splits` chunks of `chunk` tokens,
+// whose partial results are joined.  They lie in the workspace as [B][Hq][rows][splits] rows of D
+// elements, unnormalised, then as many pairs (maximum, sum).
 struct Cut {
-  int chunk, splits;
+  int chunk, splits, rows;
 };
 
 // Attention's form for many rows a KV head.
@@ -113,6 +115,15 @@ __device__ __forceinline__ Rows rows_of(const CacheArgs& c, int b, int causal, i
   r.L = c.L;
   r.causal = causal;
   return r;
+}
+
+// Index of a partial result.
+__device__ __forceinline__ int64_t part_of(const Cut& cut, int b, int Hq, int hq, int i, int split) {
+  return (((int64_t)b * Hq + hq) * cut.rows + i) * cut.splits + split;
+}
+// Where the pairs of the partial results begin.
+__device__ __forceinline__ float* part_stats(const PagedArgs& a, const Cut& cut) {
+  return a.workspace + (int64_t)a.c.B * a.Hq * cut.rows * cut.splits * a.c.D;
 }
 
 // Element offset of a row of a page: which = 0 keys, 1 values.

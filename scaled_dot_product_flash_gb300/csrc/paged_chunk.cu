@@ -13,7 +13,7 @@
 //
 // The pipeline is that of the dense forward kernel: a block of 12 warps computes two Q tiles;
 // warps 0-3 / 4-7 are the softmax of tile 0 / 1, one thread a row; warp 8 loads; warps 9 / 10
-// issue the MMAs of tile 0 / 1.  S_w = Q_w·K^T goes to TMEM columns [128w, 128w + 128), P_w over its first
+// issue the MMAs of tile 0 / 1; warp 11 looks whether all pages are good.  S_w = Q_w·K^T goes to TMEM columns [128w, 128w + 128), P_w over its first
 // 64 as the A operand of O_w += P_w·V at columns [256 + 128w, +D), PV in two halves of 64 keys.  The two
 // softmax warpgroups take turns at the exponentials.  The running maximum is raised when a row's
 // maximum grows by 2^8.  Rows that see few keys take P as head and remainder (16 more bits), see split_tile.
@@ -26,7 +26,7 @@ using namespace tc;
 
 constexpr int kStages = 4;      // ring of K and V tiles
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kScanWarp = 11;
 // The block is launched with 168 registers a thread: 128·56 + 256·224 = 384·168.
 constexpr int kRegsLow = 56, kRegsHigh = 224;
 constexpr float kRescale = 8.f;
@@ -41,27 +41,30 @@ struct Layout128 {
 
 struct Bars {
   uint64_t q_full, kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], mma_done[2], turn[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], mma_done[2], turn[2], scanned;
   uint32_t tmem_base;
-  int abort;
+  int abort, bad_pages;
 };
 
 // What a block of Q tiles works on.
 struct Work {
   int b, h, group, i0;  // sequence, KV head, group of its query heads, first query
   int split, k_lo;      // chunk of keys
+  bool cut;             // it is one of several
 };
 __device__ __forceinline__ Work work_of(const PagedArgs& a, const Tiling& t, int queries) {
-  // All sequences and heads of one block of queries, then the next; under the causal mask the last
-  // (heaviest) queries first, so that the tail of the grid is light.
+  // All sequences and heads of the last block of queries, then of the one before: under the causal
+  // mask the heaviest first, so that the tail of the grid is light.
   const int units = a.c.B * a.c.Hkv * t.groups;
   const int unit = blockIdx.x % units, rank = blockIdx.x / units;
   Work w;
   w.group = unit % t.groups;
   w.h = unit / t.groups % a.c.Hkv;
   w.b = unit / t.groups / a.c.Hkv;
-  w.split = rank % t.cut.splits;
-  w.i0 = (a.causal ? t.blocks - 1 - rank / t.cut.splits : rank / t.cut.splits) * queries;
+  w.cut = rank >= t.whole;
+  const int block = w.cut ? t.whole + (rank - t.whole) / t.cut.splits : rank;
+  w.split = w.cut ? (rank - t.whole) % t.cut.splits : 0;
+  w.i0 = (t.blocks - 1 - block) * queries;
   w.k_lo = (int)min((int64_t)w.split * t.cut.chunk, (int64_t)1 << 30);
   return w;
 }
@@ -76,7 +79,7 @@ __device__ __forceinline__ Span span_of(const Rows& rows, const Tiling& t, int i
   s.i0 = i0;
   s.i1 = min(rows.L, i0 + t.tokens);
   const bool any = i0 < s.i1 && s.i1 > rows.first;
-  s.end = any ? (int)min((int64_t)rows.limit(s.i1 - 1), (int64_t)w.k_lo + t.cut.chunk) : 0;
+  s.end = any ? (w.cut ? (int)min((int64_t)rows.limit(s.i1 - 1), (int64_t)w.k_lo + t.cut.chunk) : rows.limit(s.i1 - 1)) : 0;
   s.least = any ? rows.limit(max(i0, rows.first)) : 0;
   return s;
 }
@@ -86,14 +89,13 @@ __device__ __forceinline__ int tiles_in(const Span& s, int k_lo) { return s.end 
 // the largest values, and P's rounding would add to O as much as O's own.
 __device__ __forceinline__ bool split_tile(const Span& s, int k0) { return k0 == 0 && s.least <= kBN; }
 
-// Whether a page table entry that the keys [lo, hi) need is bad (every thread of the block calls it).
-__device__ __forceinline__ bool pages_bad(const CacheArgs& c, int b, int lo, int hi) {
+// Whether a page table entry that the keys [lo, hi) need is bad (a warp).
+__device__ __forceinline__ bool pages_bad(const CacheArgs& c, const int* table, int lo, int hi) {
   bool bad = false;
   if (hi > lo)
-    for (int e = lo / c.page_size + threadIdx.x; e <= (hi - 1) / c.page_size; e += blockDim.x)
-      bad |= (unsigned)c.pages[b * c.pages_stride + e] >= (unsigned)c.num_pages;
+    for (int e = lo / c.page_size + threadIdx.x % 32; e <= (hi - 1) / c.page_size; e += 32) bad |= (unsigned)table[e] >= (unsigned)c.num_pages;
   if (bad) report_error(c.err, kDevErrIndex, kKidPagedAttn);
-  return __syncthreads_or(bad);
+  return __any_sync(0xffffffffu, bad);
 }
 
 // Hides the keys of bad pages in a row of scores; returns the factor that the scores then take.
@@ -202,12 +204,13 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, co
   const bool nothing = l == 0.f;
   const int64_t row = ((int64_t)w.b * a.Hq + hq) * a.c.L + i;
   float inv = 1.f, m_all = m, l_all = l;
-  if (t.cut.splits == 1 && there) {
+  if (!w.cut && there) {
     const float f = fold_sink(a.sinks, hq, m_all, l_all);
     inv = f / l_all;
     if (a.lse) a.lse[row] = l_all == 0.f ? minus_inf() : (m_all + log2f(l_all)) * kLn2;
   }
-  float* part = a.workspace + (row * t.cut.splits + w.split) * D;
+  const int64_t at = part_of(t.cut, w.b, a.Hq, hq, i, w.split);
+  float* part = a.workspace + at * D;
 #pragma unroll 1
   for (int c32 = 0; c32 < D / 32; ++c32) {
     uint32_t o[32];
@@ -232,7 +235,7 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, co
       }
     }
     __syncwarp();
-    if (t.cut.splits > 1) {
+    if (w.cut) {
       if (there && to > w.k_lo)
 #pragma unroll
         for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(part + c32 * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -247,8 +250,8 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, co
         *reinterpret_cast<uint4*>(blk + sw128_off(r, c32 % 2 * 4 + v4)) = make_uint4(packed[4 * v4], packed[4 * v4 + 1], packed[4 * v4 + 2], packed[4 * v4 + 3]);
     }
   }
-  if (t.cut.splits > 1 && there && to > w.k_lo) {
-    float* ml = a.workspace + (int64_t)a.c.B * a.Hq * a.c.L * t.cut.splits * D + 2 * (row * t.cut.splits + w.split);
+  if (w.cut && there && to > w.k_lo) {
+    float* ml = part_stats(a, t.cut) + 2 * at;
     ml[0] = m;
     ml[1] = l;
   }
@@ -269,11 +272,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Work work = work_of(a, t, 2 * t.tokens);
+  const int* table = c.pages + work.b * c.pages_stride;
+  // Lane x of the loading warp takes box x / kCB of a tile, column block x % kCB; the first tile's page
+  // table entries are on their way while the length is.
+  const int boxes = kBN / t.box, box = lane / kCB, cb = lane % kCB;
+  Box entry{-1, 0};
+  if (warp == kLoadWarp && box < boxes) entry = entry_at(c, table, work.k_lo + box * t.box);
   const Rows rows = rows_of(c, work.b, a.causal, a.max_len, kKidPagedAttn);
   const Span span[2] = {span_of(rows, t, work.i0, work), span_of(rows, t, work.i0 + t.tokens, work)};
   const int nkv[2] = {tiles_in(span[0], work.k_lo), tiles_in(span[1], work.k_lo)};
   const int nmax = max(nkv[0], nkv[1]), end = max(span[0].end, span[1].end);
-  if (nmax == 0 && t.cut.splits > 1) {
+  if (nmax == 0 && work.cut) {
     asm volatile("griddepcontrol.launch_dependents;");
     return;
   }
@@ -292,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.mma_done[w], 1);
       mbar_init(&bars.turn[w], 4);  // one arrival a warp of the other warpgroup
     }
+    mbar_init(&bars.scanned, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -301,10 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int w = 0; w < 2; ++w) clear_unused<kCB>(sm + L::kQOff + w * L::kTileBytes, t);
   fence_async_smem();
   tc_fence_before();
-  const bool bad_pages = pages_bad(c, work.b, work.k_lo, end);  // also the block's barrier
+  __syncthreads();
   tc_fence_after();
   const uint32_t tbase = bars.tmem_base;
-  const int* table = c.pages + work.b * c.pages_stride;
   const WaitCtx wc{&bars.abort, 0, a.wait_limit_ns, c.err, kKidPagedAttn};
   if (warp >= 8) regs_dec<kRegsLow>();
 
@@ -320,12 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(sm + L::kQOff + w * L::kTileBytes + cb * 16384, &tq, &bars.q_full, cb * 64, work.h * a.G + work.group * t.heads, span[w].i0, work.b);
     }
     __syncwarp();
-    // Lane x loads box x / kCB of a tile, column block x % kCB.
-    const int boxes = kBN / t.box, box = lane / kCB, cb = lane % kCB;
-    const bool mine = lane < boxes * kCB;
+    const bool mine = box < boxes;
     int issued = 0;
     bool ok = true;
-    Box at = box_at(c, table, work.k_lo + box * t.box, mine ? end : 0);
+    Box at = box_of(c, entry, work.k_lo + box * t.box, mine ? end : 0);
     for (int j = 0; ok && j < nmax; ++j) {
       const Box next = box_at(c, table, work.k_lo + (j + 1) * kBN + box * t.box, mine ? end : 0);
       for (int kv = 0; kv < 2; ++kv) {
@@ -407,6 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mma_commit_w(&bars.mma_done[w]);
     drain_wait(&bars.mma_done[w], 0);
+  } else if (warp == kScanWarp) {
+    const bool bad = pages_bad(c, table, work.k_lo, end);
+    if (lane == 0) {
+      bars.bad_pages = bad;
+      mbar_arrive(&bars.scanned);
+    }
   } else if (warp < 8) {
     regs_inc<kRegsHigh>();
     const int w = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
@@ -416,8 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = sp.i0 + r / t.heads;
     const int limit = r < t.heads * t.tokens && i < sp.i1 ? rows.limit(i) : 0;
     float m = minus_inf(), l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < mine; ++j) {
+    bool ok = __all_sync(kAll, mbar_wait(&bars.scanned, 0, wc));
+    const bool bad_pages = bars.bad_pages;
+    for (int j = 0; ok && j < mine; ++j) {
       const int k0 = work.k_lo + j * kBN;
       if (!(ok = __all_sync(kAll, mbar_wait(&bars.s_full[w], j & 1, wc)))) break;
       tc_fence_after();
@@ -485,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         finish_row<T, D>(a, work, t, rows, sp, r, o_addr, stage, m, l, mine > 0);
         fence_async_smem();
       }
-      if (named_sync_and(1 + w, kBM, ok) && r == 0 && t.cut.splits == 1) {
+      if (named_sync_and(1 + w, kBM, ok) && r == 0 && !work.cut) {
         for (int cb = 0; cb < kCB; ++cb) tma_store_4d(&to, stage + cb * 16384, cb * 64, work.h * a.G + work.group * t.heads, sp.i0, work.b);
         bulk_commit();
         bulk_wait_read();
@@ -512,7 +526,7 @@ cudaError_t chunk_d(const PagedArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(kern, Layout128<D>::kBytes, ready);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks * t.cut.splits), kThreads, Layout128<D>::kBytes, s>>>(tq, tkv, to, a, t);
+  kern<<<(unsigned)paged_chunk_blocks(a), kThreads, Layout128<D>::kBytes, s>>>(tq, tkv, to, a, t);
   return cudaGetLastError();
 }
 
@@ -549,14 +563,34 @@ tc::Tiling paged_tiling(const PagedArgs& a) {
   t.blocks = (a.c.L + queries - 1) / queries;
   t.box = a.c.D == 256 ? 64 : 128;
   while (a.c.page_size % t.box) t.box /= 2;
-  // Few blocks: chunks of at least 512 keys, enough of them to fill the device, in 64 MiB of partial results.
-  const int64_t blocks = (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks, sms = a.c.num_sms > 0 ? a.c.num_sms : 1;
-  const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
-  int64_t splits = min(max((int64_t)1, sms / blocks), max((int64_t)1, ((int64_t)64 << 20) / partial));
-  splits = max((int64_t)1, min(splits, (int64_t)a.max_len / 512));
-  const int64_t chunk = ((a.max_len + splits - 1) / splits + tc::kBN - 1) / tc::kBN * tc::kBN;
-  t.cut.chunk = (int)min(chunk, (int64_t)1 << 30);
-  t.cut.splits = (int)((a.max_len + t.cut.chunk - 1) / t.cut.chunk);
+  t.whole = t.blocks;
+  t.cut = Cut{1 << 30, 1, 0};
+  // What does not fill a wave of blocks (one an SM) is cut into chunks of keys, if that is expected
+  // to pay: in microseconds, a pair of tiles takes 1.6 a KV tile, a block 4 more, and the join 4 and
+  // its bytes at 2.5 TB/s.  Where queries differ much in what they see, whole waves end evenly anyway.
+  const int64_t units = (int64_t)a.c.B * a.c.Hkv * t.groups, all = units * t.blocks, sms = a.c.num_sms > 0 ? a.c.num_sms : 1;
+  const int tiles = (a.max_len + tc::kBN - 1) / tc::kBN;
+  const bool even = !a.causal || (int64_t)2 * (a.max_len - a.c.L + queries) >= a.max_len;
+  if (all >= sms && !even) return t;
+  const int whole = (int)(all / sms * sms / units);
+  const int64_t rest = units * (t.blocks - whole);
+  const int rows = min(a.c.L, (t.blocks - whole) * queries);
+  const double partial = (double)a.c.B * a.Hq * rows * (a.c.D + 2) * sizeof(float);
+  double best_time = 1e30;
+  int splits = 1;
+  for (int x = 1; x <= 64 && (x == 1 || (x * partial <= 67108864.0 && x * 4 <= tiles)); ++x) {
+    const double time = (double)((rest * x + sms - 1) / sms) * ((tiles + x - 1) / x * 1.6 + 4) + (x > 1 ? 4 + 2 * x * partial / 2.5e6 : 0);
+    if (time < best_time) {
+      best_time = time;
+      splits = x;
+    }
+  }
+  const int chunk = (tiles + splits - 1) / splits * tc::kBN;
+  splits = (a.max_len + chunk - 1) / chunk;
+  if (splits > 1) {
+    t.whole = whole;
+    t.cut = Cut{chunk, splits, rows};
+  }
   return t;
 }
 
@@ -564,7 +598,7 @@ bool paged_chunk_takes(const PagedArgs& a) { return a.c.D <= 128 && a.G * (int64
 Cut paged_chunk_cut(const PagedArgs& a) { return paged_tiling(a).cut; }
 int64_t paged_chunk_blocks(const PagedArgs& a) {
   const tc::Tiling t = paged_tiling(a);
-  return (int64_t)a.c.B * a.c.Hkv * t.groups * t.blocks * t.cut.splits;
+  return (int64_t)a.c.B * a.c.Hkv * t.groups * (t.whole + (int64_t)(t.blocks - t.whole) * t.cut.splits);
 }
 cudaError_t launch_paged_chunk(const PagedArgs& a, int dtype, cudaStream_t s) {
   return dtype == 1 ? chunk_t<__half>(a, s) : chunk_t<__nv_bfloat16>(a, s);

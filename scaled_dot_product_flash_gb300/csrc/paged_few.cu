@@ -30,7 +30,7 @@ struct Cfg {
   static constexpr int kBlk = kTile * 128;         // bytes of one block of a unit's keys or values
   static constexpr int kHalf = kCB * kBlk, kUnit = 2 * kHalf;
   static constexpr int kWarps = D == 256 ? 4 : 8;
-  static constexpr int kStages = kCB == 1 ? 4 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kRows = kTile * NT;
   static constexpr int kRing = kWarps * kStages * kUnit;
   static constexpr int kMerge = kWarps * kTile * (D + 4) * 4;  // one row tile of every warp's output
@@ -363,10 +363,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
       if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w))
         v = sum_apart<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M);
       if (cut.splits > 1) {
-        const int64_t at = row * cut.splits + blockIdx.x;
+        const int64_t at = part_of(cut, b, a.Hq, hq, i, blockIdx.x);
         *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;
         if (d == 0) {
-          float* ml = a.workspace + (int64_t)c.B * a.Hq * c.L * cut.splits * D + 2 * at;
+          float* ml = part_stats(a, cut) + 2 * at;
           ml[0] = M;
           ml[1] = sum;
         }
@@ -381,75 +381,89 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
   }
 }
 
-// Joins the chunks of one query row: D/4 threads a chunk, several chunks side by side.
-template <typename T, int D, int kThreads>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedArgs a, Cut cut) {
-  constexpr int U = D / 4, kSide = kThreads / U;
-  __shared__ float4 part[kSide][U];
-  __shared__ float red[kThreads / 32], sums[kThreads / 32];
+// Joins the chunks of a query row, kWarps warps a row, each the chunks x, x + kWarps, ...; 8 warps a block.
+constexpr int kJoinWarps = 8;
+template <typename T, int D, int kWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedArgs a, Cut cut) {
+  constexpr int U = D / 4, kMine = (U + 31) / 32;  // float4s of a row, and of a lane
+  __shared__ float4 part[kWarps > 1 ? kJoinWarps : 1][U];
+  __shared__ float stat[kWarps > 1 ? kJoinWarps : 1][2];
   const CacheArgs& c = a.c;
-  const int64_t row = blockIdx.x;
-  const int i = (int)(row % c.L), hq = (int)(row / c.L % a.Hq), b = (int)(row / c.L / a.Hq);
-  const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
-  const int n = (int)(((int64_t)rows.limit(i) + cut.chunk - 1) / cut.chunk);  // chunks that the row sees
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, side = warp % kWarps;
+  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / kWarps) + warp / kWarps;
+  const bool there = row < (int64_t)c.B * a.Hq * cut.rows;
+  const int i = (int)(row % cut.rows), hq = (int)(row / cut.rows % a.Hq), b = (int)(row / cut.rows / a.Hq);
+  int n = 0;  // chunks that the row sees
+  if (there) {
+    const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
+    n = (int)(((int64_t)rows.limit(i) + cut.chunk - 1) / cut.chunk);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float* ml = a.workspace + (int64_t)c.B * a.Hq * c.L * cut.splits * D + 2 * row * cut.splits;
+  if (kWarps == 1 && !there) return;
+  const float* ml = part_stats(a, cut) + 2 * row * cut.splits;
+  const float* from = a.workspace + row * cut.splits * D;
   float M = minus_inf(), L = 0.f;
-  for (int x = threadIdx.x; x < n; x += kThreads) M = fmaxf(M, ml[2 * x]);
+  for (int x = lane; x < n; x += 32) M = fmaxf(M, ml[2 * x]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = M;
-  __syncthreads();
+  float4 v[kMine];
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, red[w]);
-  // (a chunk without a maximum has a sum of 0, or NaN and outputs of NaN)
-  for (int x = threadIdx.x; x < n; x += kThreads) L += ml[2 * x] == minus_inf() ? ml[2 * x + 1] : ml[2 * x + 1] * ex2(ml[2 * x] - M);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-  if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = L;
-  const int side = threadIdx.x / U, d = threadIdx.x % U * 4;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (side < kSide) {
+  for (int u = 0; u < kMine; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int x = side; x < n; x += kSide) {
-      const float mx = ml[2 * x], w = mx == minus_inf() ? 1.f : ex2(mx - M);
-      const float4 y = *reinterpret_cast<const float4*>(a.workspace + (row * cut.splits + x) * D + d);
-      v.x = fmaf(w, y.x, v.x);
-      v.y = fmaf(w, y.y, v.y);
-      v.z = fmaf(w, y.z, v.z);
-      v.w = fmaf(w, y.w, v.w);
-    }
-    part[side][d / 4] = v;
-  }
-  __syncthreads();
-  if (threadIdx.x >= U) return;
-  L = 0.f;
+  for (int x = side; x < n; x += kWarps) {
+    // (a chunk without a maximum has a sum of 0, or NaN and outputs of NaN)
+    const float mx = ml[2 * x], w = mx == minus_inf() ? 1.f : tc::ex2(mx - M);
+    L = fmaf(w, ml[2 * x + 1], L);
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) L += sums[w];
-  v = part[0][d / 4];
-  for (int x = 1; x < kSide; ++x) {
-    const float4 y = part[x][d / 4];
-    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+    for (int u = 0; u < kMine; ++u)
+      if (u * 32 + lane < U) {
+        const float4 y = reinterpret_cast<const float4*>(from + (int64_t)x * D)[u * 32 + lane];
+        v[u].x = fmaf(w, y.x, v[u].x);
+        v[u].y = fmaf(w, y.y, v[u].y);
+        v[u].z = fmaf(w, y.z, v[u].z);
+        v[u].w = fmaf(w, y.w, v[u].w);
+      }
+  }
+  if constexpr (kWarps > 1) {
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+      if (u * 32 + lane < U) part[warp][u * 32 + lane] = v[u];
+    if (lane == 0) stat[warp][0] = L;
+    __syncthreads();
+    if (side > 0 || !there) return;
+#pragma unroll
+    for (int y = 1; y < kWarps; ++y) {
+      L += stat[warp + y][0];
+#pragma unroll
+      for (int u = 0; u < kMine; ++u)
+        if (u * 32 + lane < U) {
+          const float4 z = part[warp + y][u * 32 + lane];
+          v[u].x += z.x; v[u].y += z.y; v[u].z += z.z; v[u].w += z.w;
+        }
+    }
   }
   const float fold = fold_sink(a.sinks, hq, M, L), inv = L == 0.f ? 0.f : fold / L;
-  T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
-  *reinterpret_cast<uint2*>(out) = make_uint2(tc::pack2<T>(v.x * inv, v.y * inv), tc::pack2<T>(v.z * inv, v.w * inv));
-  if (a.lse && d == 0) a.lse[row] = L == 0.f ? minus_inf() : (M + log2f(L)) * kLn2;
+  T* out = row_ptr<T>(a.out, a.lo, b, hq, i);
+#pragma unroll
+  for (int u = 0; u < kMine; ++u)
+    if (u * 32 + lane < U)
+      *reinterpret_cast<uint2*>(out + 4 * (u * 32 + lane)) = make_uint2(tc::pack2<T>(v[u].x * inv, v[u].y * inv), tc::pack2<T>(v[u].z * inv, v[u].w * inv));
+  if (a.lse && lane == 0) a.lse[((int64_t)b * a.Hq + hq) * c.L + i] = L == 0.f ? minus_inf() : (M + log2f(L)) * kLn2;
 }
 
 // ---- the weights of few rows.  A warp owns its units' tokens, so sums have one order and no atomics.
-template <int D>
+template <int D, int NT>
 struct WCfg {
-  static constexpr int kNT = D == 256 ? 1 : 2, kRows = kTile * kNT;
-  static constexpr int kWarps = 8, kStages = D == 256 ? 3 : 4;
+  static constexpr int kNT = NT, kRows = kTile * kNT;
+  static constexpr int kWarps = 4, kStages = 3;
   static constexpr int kUnit = (D + 63) / 64 * kTile * 128;
   static constexpr int kSmem = kWarps * kStages * kUnit + 1024;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(WCfg<D>::kWarps * 32) paged_weights_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, int chunk) {
-  using C = WCfg<D>;
-  constexpr int NT = C::kNT, kWarps = C::kWarps;
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(WCfg<D, NT>::kWarps * 32) paged_weights_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, int chunk) {
+  using C = WCfg<D, NT>;
+  constexpr int kWarps = C::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kWarps][C::kStages];
@@ -503,8 +517,16 @@ __global__ void __launch_bounds__(WCfg<D>::kWarps * 32) paged_weights_kernel(con
           for (int k8 = 0; k8 < 2; ++k8) qa[nt][ks][x + 2 * k8] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * k8) : 0u;
       }
     const int k_row = lane / 16 * 8 + lane % 8, k_piece = lane / 8 % 2;
+    // Lanes of the first four g write a token's weight each; what it was is read a unit ahead.
+    const int my_key = 8 * (g / 2) + 2 * t + g % 2;
+    auto was = [&](int u) {
+      const int key = ring.pos(u) + my_key;
+      return u < ring.units && g < 4 && key < end && !(first_pass && key >= fresh) ? weights[key] : 0.f;
+    };
+    float old = was(0);
     for (int u = 0; u < ring.units; ++u) {
       const int k0 = ring.pos(u);
+      const float next_old = was(u + 1);
       float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
       if (ring.wait(u, ok, wc)) {
         const uint32_t ks0 = tc::smem_u32(ring.base + u % C::kStages * C::kUnit);
@@ -545,12 +567,11 @@ __global__ void __launch_bounds__(WCfg<D>::kWarps * 32) paged_weights_kernel(con
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int off = 4; off <= 16; off <<= 1) sum[n][e] += __shfl_xor_sync(0xffffffffu, sum[n][e], off);
-          const int key = k0 + 8 * n + 2 * t + e;
-          if (g == 0 && key < end) weights[key] = (first_pass && key >= fresh ? 0.f : weights[key]) + sum[n][e];
-        }
+      if (g < 4 && k0 + my_key < end) weights[k0 + my_key] = old + (g & 2 ? (g & 1 ? sum[1][1] : sum[1][0]) : (g & 1 ? sum[0][1] : sum[0][0]));
+      old = next_old;
     }
     phase = ring.phase;
     __syncwarp();
@@ -577,6 +598,7 @@ Cut cut_few(const PagedArgs& a) {
   Cut cut;
   cut.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
   cut.splits = (a.max_len + cut.chunk - 1) / cut.chunk;
+  cut.rows = a.c.L;
   return cut;
 }
 
@@ -597,18 +619,33 @@ cudaError_t few_nt(const PagedArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, int D, int kThreads>
+template <typename T, int D, int NT>
+cudaError_t weights_nt(const PagedArgs& a, cudaStream_t s) {
+  using C = WCfg<D, NT>;
+  auto* kern = paged_weights_kernel<T, D, NT>;
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, C::kSmem, ready);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!make_tmap_pages(&map, a.c, kTile)) return cudaErrorInvalidValue;
+  const int chunk = 1024;
+  kern<<<dim3((a.max_len + chunk - 1) / chunk, a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, chunk);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int kWarps>
 cudaError_t join_t(const PagedArgs& a, const Cut& cut, cudaStream_t s) {
+  constexpr int kRows = kJoinWarps / kWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.c.B * a.Hq * a.c.L));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(((int64_t)a.c.B * a.Hq * cut.rows + kRows - 1) / kRows));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];  // its blocks may be placed while the last chunks are still running
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, kThreads>, a, cut);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, kWarps>, a, cut);
 }
 
 enum class Do { kAttn, kJoin, kWeights };
@@ -617,19 +654,11 @@ template <typename T, int D>
 cudaError_t run_d(const PagedArgs& a, Do what, cudaStream_t s) {
   if (what == Do::kJoin) {
     const Cut cut = cut_of(a);
-    return cut.splits > 16 ? join_t<T, D, 512>(a, cut, s) : join_t<T, D, 128>(a, cut, s);
+    return cut.splits > 8 ? join_t<T, D, kJoinWarps>(a, cut, s) : join_t<T, D, 1>(a, cut, s);
   }
   if (what == Do::kWeights) {
-    using C = WCfg<D>;
-    auto* kern = paged_weights_kernel<T, D>;
-    static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_smem(kern, C::kSmem, ready);
-    if (e != cudaSuccess) return e;
-    CUtensorMap map;
-    if (!make_tmap_pages(&map, a.c, kTile)) return cudaErrorInvalidValue;
-    const int chunk = 1024;
-    kern<<<dim3((a.max_len + chunk - 1) / chunk, a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, chunk);
-    return cudaGetLastError();
+    if constexpr (D == 256) return weights_nt<T, D, 1>(a, s);
+    else return rows_a_block(a) == kTile ? weights_nt<T, D, 1>(a, s) : weights_nt<T, D, 2>(a, s);
   }
   if constexpr (D == 256) return few_nt<T, D, 1>(a, s);
   else return rows_a_block(a) == kTile ? few_nt<T, D, 1>(a, s) : few_nt<T, D, 2>(a, s);
@@ -659,7 +688,7 @@ bool paged_attn_launchable(const PagedArgs& a) {
 }
 size_t paged_attn_workspace(const PagedArgs& a) {
   const Cut cut = cut_of(a);
-  return cut.splits == 1 ? 0 : (size_t)a.c.B * a.Hq * a.c.L * cut.splits * (a.c.D + 2) * sizeof(float);
+  return cut.splits == 1 ? 0 : (size_t)a.c.B * a.Hq * cut.rows * cut.splits * (a.c.D + 2) * sizeof(float);
 }
 cudaError_t launch_paged_attn(const PagedArgs& a, int dtype, cudaStream_t s) {
   return paged_chunk_takes(a) ? launch_paged_chunk(a, dtype, s) : run(a, dtype, Do::kAttn, s);

@@ -15,6 +15,7 @@ struct Tiling {
   int heads, tokens;  // of a Q tile
   int groups;         // of heads: G / heads
   int blocks;         // of two Q tiles (one for D = 256): queries of a sequence
+  int whole;          // of those, from the last one on: not cut
   int box;            // tokens of a box of keys
   Cut cut;
 };
@@ -27,14 +28,16 @@ constexpr bool kIsBf16 = std::is_same<T, __nv_bfloat16>::value;
 struct Box {
   int page, place;
 };
+// What the page table says about position pos (-1 past its end), which may be read before the length is known.
+__device__ __forceinline__ Box entry_at(const CacheArgs& c, const int* table, int pos) {
+  const int slot = pos / c.page_size;
+  return Box{slot < c.pages_per_seq ? table[slot] : -1, pos - slot * c.page_size};
+}
+__device__ __forceinline__ Box box_of(const CacheArgs& c, const Box& entry, int pos, int end) {
+  return pos < end && (unsigned)entry.page < (unsigned)c.num_pages ? entry : Box{c.num_pages, 0};
+}
 __device__ __forceinline__ Box box_at(const CacheArgs& c, const int* table, int pos, int end) {
-  Box x{c.num_pages, 0};
-  if (pos < end) {
-    const int slot = pos / c.page_size, page = table[slot];
-    x.place = pos - slot * c.page_size;
-    if ((unsigned)page < (unsigned)c.num_pages) x.page = page;
-  }
-  return x;
+  return pos < end ? box_of(c, entry_at(c, table, pos), pos, end) : Box{c.num_pages, 0};
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
