@@ -189,7 +189,7 @@ __device__ __forceinline__ float exponentials(const uint32_t (&sv)[kBN], uint32_
 }
 
 // One row's state at the end: writes its output into the staging tile (or its partial result
-// into the workspace) and its logsumexp.
+// into the workspace) and its logsumexp.  (The staging tile is the Q tile, which nobody reads any more.)
 template <typename T, int D>
 __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, const Tiling& t, const Rows& rows, const Span& span, int r, uint32_t o_addr,
                                            uint8_t* stage, float m, float l, bool any) {
@@ -515,6 +515,311 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---- one Q tile a block
+//
+// Head dim 256, whose O takes 256 columns of tensor memory (beside two S buffers, so that S of the
+// next keys is there while this tile's softmax runs), and calls whose rows all fit in one Q tile
+// (drafts, short chunks): then two blocks share an SM, with one S buffer each, and each other's
+// waits.  Keys are handed back in blocks of 64 columns and values in halves of 64 tokens, as soon as
+// the product that reads them is done with that piece.  Warps 0-3: softmax; warp 4 loads, its first half
+// the queries and keys, its second half the values; warp 5 issues S, and PV too where S has one
+// buffer (the two take turns then); warp 6 issues PV where it has two.
+// `exact`: every tile takes P as head and remainder, so that few rows, whose tiles are bound by the
+// bytes of the cache, come out as they do in paged_few.cu.
+template <int D>
+struct OneLayout {
+  static constexpr int kCB = (D + 63) / 64;
+  static constexpr int kTileBytes = 128 * kCB * 128;
+  static constexpr int kS = D == 256 ? 2 : 1;        // S buffers
+  static constexpr int kStages = D <= 64 ? 2 : 1;    // of K tiles and of V tiles
+  static constexpr int kKOff = kTileBytes, kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kBytes = kVOff + kStages * kTileBytes + 1024;
+  static constexpr int kColumns = D == 256 ? 512 : 256, kO = 128 * kS;
+  static constexpr int kThreads = D == 256 ? 256 : 192, kBlocks = D == 256 ? 1 : 2;
+};
+
+template <int kCB, int kStages, int kS>
+struct OneBars {
+  uint64_t q_full, k_full[kStages][kCB], k_empty[kStages][kCB], v_full[kStages][2], v_empty[kStages][2];
+  uint64_t s_full[kS], p_full[kS], pv_done[kS], fin, scanned;
+  uint32_t tmem_base;
+  int abort, bad_pages;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
+    paged_one_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkv, const __grid_constant__ CUtensorMap to,
+                     PagedArgs a, Tiling t, bool exact) {
+  using L = OneLayout<D>;
+  constexpr int kCB = L::kCB, kS = L::kS, kStages = L::kStages;
+  constexpr uint32_t kIdS = idesc_f16(kBM, kBN, kIsBf16<T>, false, false);
+  constexpr uint32_t kIdO = idesc_f16(kBM, D, kIsBf16<T>, false, true);
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ OneBars<kCB, kStages, kS> bars;
+  const CacheArgs& c = a.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const Work work = work_of(a, t, t.tokens);
+  const int* table = c.pages + work.b * c.pages_stride;
+  // Lanes 0-15 of the loading warp: box `lane` of each column block of a K tile.  Lanes 16-31: of each
+  // half of a V tile, box (lane − 16) / kCB, column block (lane − 16) % kCB.
+  const bool loads_k = lane < 16;
+  const int box = loads_k ? lane : (lane - 16) / kCB;
+  const bool mine = box < (loads_k ? kBN : kBN / 2) / t.box;
+  Box entry[2] = {{-1, 0}, {-1, 0}};  // the first K tile's, or both halves' of the first V tile
+  if (warp == 4 && mine) {
+    entry[0] = entry_at(c, table, work.k_lo + box * t.box);
+    if (!loads_k) entry[1] = entry_at(c, table, work.k_lo + kBN / 2 + box * t.box);
+  }
+  const Rows rows = rows_of(c, work.b, a.causal, a.max_len, kKidPagedAttn);
+  const Span span = span_of(rows, t, work.i0, work);
+  const int n = tiles_in(span, work.k_lo), end = span.end;
+  if (n == 0 && work.cut) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    return;
+  }
+  if (threadIdx.x == 0) {
+    bars.abort = 0;
+    mbar_init(&bars.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      for (int x = 0; x < kCB; ++x) {
+        mbar_init(&bars.k_full[s][x], 1);
+        mbar_init(&bars.k_empty[s][x], 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&bars.v_full[s][x], 1);
+        mbar_init(&bars.v_empty[s][x], 1);
+      }
+    }
+    for (int x = 0; x < kS; ++x) {
+      mbar_init(&bars.s_full[x], 1);
+      mbar_init(&bars.p_full[x], kBM);
+      mbar_init(&bars.pv_done[x], 1);
+    }
+    mbar_init(&bars.fin, kS);  // one commit an issuer
+    mbar_init(&bars.scanned, 1);
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(&bars.tmem_base, L::kColumns);
+    tmem_relinquish();
+  }
+  clear_unused<kCB>(sm, t);
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bars.tmem_base;
+  const WaitCtx wc{&bars.abort, 0, a.wait_limit_ns, c.err, kKidPagedAttn};
+  const auto few = [&](int j) { return exact || (j == 0 && split_tile(span, work.k_lo)); };
+
+  if (warp == 4) {
+    const unsigned half = loads_k ? 0x0000ffffu : 0xffff0000u;
+    const bool first = lane % 16 == 0;
+    bool ok = true;
+    int issued = 0;  // pieces
+    if (lane == 0) {
+      prefetch_tmap(&tq);
+      prefetch_tmap(&tkv);
+      prefetch_tmap(&to);
+      mbar_arrive_expect_tx(&bars.q_full, kCB * t.heads * t.tokens * 128);
+      for (int cb = 0; cb < kCB; ++cb) tma_load_4d(sm + cb * 16384, &tq, &bars.q_full, cb * 64, work.h * a.G + work.group * t.heads, work.i0, work.b);
+    }
+    __syncwarp();
+    if (loads_k) {
+      Box at = box_of(c, entry[0], work.k_lo + box * t.box, mine ? end : 0);
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = j % kStages;
+        const Box next = box_at(c, table, work.k_lo + (j + 1) * kBN + box * t.box, mine ? end : 0);
+        for (int cb = 0; cb < kCB; ++cb) {
+          if (!(ok = __all_sync(half, mbar_wait(&bars.k_empty[s][cb], ((j / kStages) & 1) ^ 1, wc)))) break;
+          if (first) mbar_arrive_expect_tx(&bars.k_full[s][cb], kBN * 128);
+          __syncwarp(half);
+          if (mine)
+            tma_load_4d(sm + L::kKOff + s * L::kTileBytes + cb * 16384 + box * t.box * 128, &tkv, &bars.k_full[s][cb], cb * 64, at.place, work.h, at.page);
+          ++issued;
+        }
+        at = next;
+      }
+      if (!ok || bars.abort)  // copies still in flight land before the block exits
+        for (int x = max(0, issued - kStages * kCB); x < issued; ++x) drain_wait(&bars.k_full[x / kCB % kStages][x % kCB], (x / kCB / kStages) & 1);
+    } else {
+      const int cb = (lane - 16) % kCB;
+      Box at[2];
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) at[hr] = box_of(c, entry[hr], work.k_lo + hr * (kBN / 2) + box * t.box, mine ? end : 0);
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = j % kStages;
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const Box next = box_at(c, table, work.k_lo + (j + 1) * kBN + hr * (kBN / 2) + box * t.box, mine ? end : 0);
+          if (ok && (ok = __all_sync(half, mbar_wait(&bars.v_empty[s][hr], ((j / kStages) & 1) ^ 1, wc)))) {
+            if (first) mbar_arrive_expect_tx(&bars.v_full[s][hr], L::kTileBytes / 2);
+            __syncwarp(half);
+            if (mine)
+              tma_load_4d(sm + L::kVOff + s * L::kTileBytes + cb * 16384 + (hr * (kBN / 2) + box * t.box) * 128, &tkv, &bars.v_full[s][hr], cb * 64, at[hr].place,
+                          c.Hkv + work.h, at[hr].page);
+            ++issued;
+          }
+          at[hr] = next;
+        }
+      }
+      if (!ok || bars.abort)
+        for (int x = max(0, issued - kStages * 2); x < issued; ++x) drain_wait(&bars.v_full[x / 2 % kStages][x % 2], (x / 2 / kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 5 || (kS == 2 && warp == 6)) {
+    const bool s_issuer = __shfl_sync(kAll, warp, 0) == 5, pv_issuer = kS == 1 || !s_issuer;
+    if (s_issuer) {
+      const bool bad = pages_bad(c, table, work.k_lo, end);
+      if (lane == 0) {
+        bars.bad_pages = bad;
+        mbar_arrive(&bars.scanned);
+      }
+    }
+    bool ok = __all_sync(kAll, mbar_wait(&bars.q_full, 0, wc));
+    tc_fence_after();
+    const uint64_t qd = sdesc_sw128(smem_u32(sm), 16, 1024);
+    auto scores = [&](int j) {
+      const int s = j % kStages, buf = j % kS;
+      const uint64_t kd = sdesc_sw128(smem_u32(sm + L::kKOff + s * L::kTileBytes), 16, 1024);
+#pragma unroll
+      for (int cb = 0; cb < kCB; ++cb) {
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.k_full[s][cb], (j / kStages) & 1, wc)))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+          if (cb * 4 + k4 < D / 16) mma_ss_w(tbase + 128 * buf, sdesc_advance(qd, cb * 16384 + k4 * 32), sdesc_advance(kd, cb * 16384 + k4 * 32), kIdS, cb + k4 > 0);
+        mma_commit_w(&bars.k_empty[s][cb]);
+      }
+      mma_commit_w(&bars.s_full[buf]);
+    };
+    auto values = [&](int j) {
+      const int s = j % kStages, buf = j % kS;
+      if (!(ok = __all_sync(kAll, mbar_wait(&bars.p_full[buf], (j / kS) & 1, wc)))) return;
+      const uint64_t vd = sdesc_sw128(smem_u32(sm + L::kVOff + s * L::kTileBytes), 16384, 1024);
+      const uint32_t p_tm = tbase + 128 * buf;
+      const bool split = few(j);
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.v_full[s][hr], (j / kStages) & 1, wc)))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 4 * hr; kk < 4 * hr + 4; ++kk) mma_ts_w(tbase + L::kO, p_tm + kk * 8, sdesc_advance(vd, kk * 2048), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+        if (split) {
+#pragma unroll
+          for (int kk = 4 * hr; kk < 4 * hr + 4; ++kk) mma_ts_w(tbase + L::kO, p_tm + 64 + kk * 8, sdesc_advance(vd, kk * 2048), kIdO, 1u);
+        }
+        mma_commit_w(&bars.v_empty[s][hr]);
+      }
+      mma_commit_w(&bars.pv_done[buf]);
+    };
+    if constexpr (kS == 1) {
+      if (ok && n > 0) scores(0);
+      for (int j = 0; ok && j < n; ++j) {
+        values(j);
+        if (!ok || j + 1 == n) break;
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[0], j & 1, wc)))) break;  // P(j) consumed
+        tc_fence_after();
+        scores(j + 1);
+      }
+    } else {
+      for (int j = 0; ok && j < n; ++j) {
+        if (pv_issuer) {
+          values(j);
+        } else {
+          if (j >= 2 && !(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[j % 2], ((j - 2) / 2) & 1, wc)))) break;
+          tc_fence_after();
+          scores(j);
+        }
+      }
+    }
+    mma_commit_w(&bars.fin);
+    drain_wait(&bars.fin, 0);
+  } else if (warp < 4) {
+    const int r = warp * 32 + lane;
+    const uint32_t o_addr = tmem_addr(tbase, warp * 32, L::kO);
+    const int i = span.i0 + r / t.heads;
+    const int limit = r < t.heads * t.tokens && i < span.i1 ? rows.limit(i) : 0;
+    const bool live = __any_sync(kAll, limit > 0);  // a warp without a row only keeps the barriers going
+    float m = minus_inf(), l = 0.f;
+    bool ok = __all_sync(kAll, mbar_wait(&bars.scanned, 0, wc));
+    const bool bad_pages = bars.bad_pages;
+    for (int j = 0; ok && j < n; ++j) {
+      const int k0 = work.k_lo + j * kBN, buf = j % kS;
+      if (!(ok = __all_sync(kAll, mbar_wait(&bars.s_full[buf], (j / kS) & 1, wc)))) break;
+      tc_fence_after();
+      if (k0 + kBN > rows.len) {  // values behind the last token
+        const int s = j % kStages;
+        // (V(j-1) has landed once PV(j-1) is done: a barrier tells only its last two phases apart)
+        if (j > 0 && !(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(j - 1) % kS], ((j - 1) / kS) & 1, wc)))) break;
+        if (!(ok = __all_sync(kAll, mbar_wait(&bars.v_full[s][warp / 2], (j / kStages) & 1, wc)))) break;
+        clear_behind<kCB>(sm + L::kVOff + s * L::kTileBytes, r, k0, rows.len);
+      }
+      if (live) {
+        const uint32_t s_addr = tmem_addr(tbase, warp * 32, 128 * buf);
+        uint32_t sv[kBN];
+#pragma unroll
+        for (int q4 = 0; q4 < kBN / 32; ++q4) tmem_ld32(s_addr + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q4]));
+        tmem_ld_wait(sv);
+        const bool cut = k0 + kBN > span.least;
+        const int lim = min(limit - k0, kBN);
+        float cs = a.scale_log2;
+        if (bad_pages) cs = hide_bad_pages(sv, c, table, k0, end, cs);
+        const float top = cut ? row_max<true>(sv, cs, lim) : row_max<false>(sv, cs, lim);
+        const float m_new = fmaxf(m, top);
+        const bool up = m_new > m + kRescale;
+        const float alpha = up ? ex2(m - m_new) : 1.f;
+        if (up) {
+          l *= alpha;
+          m = m_new;
+        }
+        if (j > 0 && __any_sync(kAll, up)) {  // rescale O once PV(j-1) has landed
+          if (!(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(j - 1) % kS], ((j - 1) / kS) & 1, wc)))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c32 = 0; c32 < D / 32; ++c32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c32 * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(o_addr + c32 * 32, o);
+          }
+          tmem_st_wait();
+        }
+        const float neg_m = m == minus_inf() ? 0.f : -m;
+        if (few(j)) l += exponentials<T, true, true>(sv, s_addr, cs, neg_m, lim, nullptr);
+        else if (cut) l += exponentials<T, true, false>(sv, s_addr, cs, neg_m, lim, nullptr);
+        else l += exponentials<T, false, false>(sv, s_addr, cs, neg_m, lim, nullptr);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(&bars.p_full[buf]);
+    }
+    if (ok && n > 0) ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, wc));
+    if (ok) ok = __all_sync(kAll, mbar_wait(&bars.q_full, 0, wc));
+    if (ok) {
+      tc_fence_after();
+      finish_row<T, D>(a, work, t, rows, span, r, o_addr, sm, m, l, n > 0);
+      fence_async_smem();
+    }
+    if (named_sync_and(1, kBM, ok) && r == 0 && !work.cut) {
+      for (int cb = 0; cb < kCB; ++cb) tma_store_4d(&to, sm + cb * 16384, cb * 64, work.h * a.G + work.group * t.heads, work.i0, work.b);
+      bulk_commit();
+      bulk_wait_read();
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tmem_dealloc(tbase, L::kColumns);
+  }
+}
+
 // ---- host
 
 template <typename T, int D>
@@ -522,12 +827,24 @@ cudaError_t chunk_d(const PagedArgs& a, cudaStream_t s) {
   const Tiling t = paged_tiling(a);
   CUtensorMap tq, tkv, to;
   if (!make_tmap_rows(&tq, a.q, a, a.lq, t) || !make_tmap_rows(&to, a.out, a, a.lo, t) || !make_tmap_pages(&tkv, a.c, t.box)) return cudaErrorInvalidValue;
+  if (t.tiles == 1) {
+    using L = OneLayout<D>;
+    auto* kern = paged_one_kernel<T, D>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(kern, L::kBytes, ready);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)paged_chunk_blocks(a), L::kThreads, L::kBytes, s>>>(tq, tkv, to, a, t, a.G * (int64_t)a.c.L <= 32);
+    return cudaGetLastError();
+  }
+  if constexpr (D <= 128) {
   auto* kern = paged_chunk_kernel<T, D>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(kern, Layout128<D>::kBytes, ready);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)paged_chunk_blocks(a), kThreads, Layout128<D>::kBytes, s>>>(tq, tkv, to, a, t);
   return cudaGetLastError();
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>
@@ -537,6 +854,7 @@ cudaError_t chunk_t(const PagedArgs& a, cudaStream_t s) {
     case 64: return chunk_d<T, 64>(a, s);
     case 96: return chunk_d<T, 96>(a, s);
     case 128: return chunk_d<T, 128>(a, s);
+    case 256: return chunk_d<T, 256>(a, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -559,20 +877,23 @@ tc::Tiling paged_tiling(const PagedArgs& a) {
     }
   }
   t.groups = a.G / t.heads;
-  const int queries = (a.c.D == 256 ? 1 : 2) * t.tokens;
+  t.tiles = a.c.D == 256 || (t.groups == 1 && a.c.L <= t.tokens) ? 1 : 2;
+  const int queries = t.tiles * t.tokens;
   t.blocks = (a.c.L + queries - 1) / queries;
-  t.box = a.c.D == 256 ? 64 : 128;
+  t.box = t.tiles == 1 ? 64 : 128;
   while (a.c.page_size % t.box) t.box /= 2;
   t.whole = t.blocks;
   t.cut = Cut{1 << 30, 1, 0};
   // What does not fill a wave of blocks (one an SM) is cut into chunks of keys, if that is expected
   // to pay: in microseconds, a pair of tiles takes 1.6 a KV tile, a block 4 more, and the join 4 and
-  // its bytes at 2.5 TB/s.  Where queries differ much in what they see, whole waves end evenly anyway.
-  const int64_t units = (int64_t)a.c.B * a.c.Hkv * t.groups, all = units * t.blocks, sms = a.c.num_sms > 0 ? a.c.num_sms : 1;
+  // its bytes at 2.5 TB/s.  Where the causal mask lets queries differ much in what they see, whole waves
+  // end evenly anyway.  (The size of the workspace goes by this, and is asked for without the mask.)
+  const int64_t units = (int64_t)a.c.B * a.c.Hkv * t.groups, all = units * t.blocks;
+  const int64_t sms = (a.c.num_sms > 0 ? a.c.num_sms : 1) * (t.tiles == 1 && a.c.D <= 128 ? 2 : 1);
   const int tiles = (a.max_len + tc::kBN - 1) / tc::kBN;
-  const bool even = !a.causal || (int64_t)2 * (a.max_len - a.c.L + queries) >= a.max_len;
+  const bool even = (int64_t)2 * (a.max_len - a.c.L + queries) >= a.max_len;
   if (all >= sms && !even) return t;
-  const int whole = (int)(all / sms * sms / units);
+  const int whole = t.blocks == 1 ? 0 : (int)(all / sms * sms / units);
   const int64_t rest = units * (t.blocks - whole);
   const int rows = min(a.c.L, (t.blocks - whole) * queries);
   const double partial = (double)a.c.B * a.Hq * rows * (a.c.D + 2) * sizeof(float);
@@ -594,7 +915,7 @@ tc::Tiling paged_tiling(const PagedArgs& a) {
   return t;
 }
 
-bool paged_chunk_takes(const PagedArgs& a) { return a.c.D <= 128 && a.G * (int64_t)a.c.L > 32; }
+bool paged_chunk_takes(const PagedArgs& a) { return a.G * (int64_t)a.c.L > (a.c.D == 256 ? 16 : 32); }
 Cut paged_chunk_cut(const PagedArgs& a) { return paged_tiling(a).cut; }
 int64_t paged_chunk_blocks(const PagedArgs& a) {
   const tc::Tiling t = paged_tiling(a);

@@ -2,12 +2,13 @@
 // chunks of a sequence (conventions in include/sdpa.h).
 //
 // Rows.  The G·L query rows of a KV head (row r = query r / G of head r % G of the group) are cut
-// into blocks of 16·NT; a block takes one of them and one chunk of the sequence, and its warps
-// take units of 16 tokens of that chunk in turn, each with a running maximum, sum and output of its
-// own, merged at the end.  Chunks are joined by a second kernel, placed while the first still runs.
+// into blocks of one or two tiles of 16; a block takes one of them and one chunk of the sequence.  It has
+// several rings, which take units of 16 tokens of that chunk in turn, and a warp a ring and row
+// tile, each with a running maximum, sum and output of its own, merged at the end.  Chunks are
+// joined by a second kernel, placed while the first still runs.
 //
 // Bound: the bytes of the cache, 4·D a token and KV head, each read once.  So a unit's keys and
-// values come by bulk tensor loads into a ring of the warp's own, a few units ahead, without a block
+// values come by bulk tensor loads into a ring, a few units ahead, without a block
 // barrier (16 tokens never cross a page, whose size is a multiple of 16); the products are warp-level
 // MMAs, m16n8k16, S = Q·K^T and O += P·V, whose accumulator of the first is the operand of the second.
 // P enters O as two 16-bit numbers, head and remainder, so that O is as exact as with fp32 weights: the
@@ -24,17 +25,21 @@ using tc::ex2;
 
 constexpr float kRescale = 8.f;
 
-template <int D, int NT>
+// RT: row tiles of 16 rows, a warp each for every ring; kSlots: rings of a block.
+template <int D, int RT, int kSlots>
 struct Cfg {
   static constexpr int kCB = (D + 63) / 64;        // 64-element blocks of a row
   static constexpr int kBlk = kTile * 128;         // bytes of one block of a unit's keys or values
   static constexpr int kHalf = kCB * kBlk, kUnit = 2 * kHalf;
-  static constexpr int kWarps = D == 256 ? 4 : 8;
+  static constexpr int kWarps = RT * kSlots;
   static constexpr int kStages = 3;
-  static constexpr int kRows = kTile * NT;
-  static constexpr int kRing = kWarps * kStages * kUnit;
-  static constexpr int kMerge = kWarps * kTile * (D + 4) * 4;  // one row tile of every warp's output
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
+  static constexpr int kBlocks = kSlots == 4 && D <= 128 ? 2 : 1;  // an SM
+  static constexpr int kRows = kTile * RT;
+  static constexpr int kRing = kSlots * kStages * kUnit;
+  static constexpr int kMerge = kWarps * kTile * (D + 4) * 4;  // every warp's output
+  static constexpr bool kQSmem = RT > 1;                       // query fragments in shared memory: 128 registers a thread
+  static constexpr int kQ = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSmem = kQ + (kQSmem ? RT * (D / 16) * 512 : 0) + 1024;
 };
 
 template <typename T>
@@ -63,8 +68,9 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// The ring of one warp: units of 16 tokens of one KV head, keys and (kBoth) values, loaded ahead.
-template <int D, int kWarps, int kStages, bool kBoth>
+// A ring of units of 16 tokens of one KV head, keys and (kBoth) values, loaded ahead; slot `slot` of kSlots.
+// Every warp that reads it follows its state; the lead one loads.
+template <int D, int kSlots, int kStages, bool kBoth>
 struct Ring {
   static constexpr int kCB = (D + 63) / 64, kBlk = kTile * 128, kHalf = kCB * kBlk;
   static constexpr int kUnit = kBoth ? 2 * kHalf : kHalf;
@@ -73,11 +79,12 @@ struct Ring {
   const int* table;
   uint8_t* base;
   uint64_t* full;
-  int h, start, end, warp, lane, units;  // units: of this warp
+  int h, start, end, slot, lane, units;  // units: of this ring
+  bool lead;
   int issued, entry, base_unit;          // entry: page of unit base_unit + lane
   uint32_t there, phase;                 // stages that hold a unit; the parity to wait for
 
-  __device__ __forceinline__ int pos(int u) const { return start + (warp + u * kWarps) * kTile; }
+  __device__ __forceinline__ int pos(int u) const { return start + (slot + u * kSlots) * kTile; }
   // This lane's entry of the page table, and whether it is a page.
   __device__ __forceinline__ void look(int u0, unsigned kid) {
     base_unit = u0;
@@ -91,15 +98,16 @@ struct Ring {
       }
     }
   }
-  // Starts the loads of the warp's next unit (all lanes).
+  // Starts the loads of the next unit (all lanes).
   __device__ __forceinline__ void issue(unsigned kid) {
     const int u = issued++, s = u % kStages;
+    there &= ~(1u << s);
     if (u >= units) return;
     if (u - base_unit >= 32) look(u, kid);
     const int page = __shfl_sync(0xffffffffu, entry, u - base_unit);
-    there &= ~(1u << s);
     if (page < 0) return;
     there |= 1u << s;
+    if (!lead) return;
     if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], kUnit);
     __syncwarp();
     if (lane < kUnit / kBlk) {
@@ -115,10 +123,9 @@ struct Ring {
     if (ok) phase ^= 1u << s;
     return ok;
   }
-  // Lets loads still in flight land (after the wait for unit u gave up).
-  __device__ __forceinline__ void drain(int u) {
-    for (int x = u; x < issued && x < units; ++x) {
-      const int s = x % kStages;
+  // Lets loads still in flight land (after a wait that gave up): of every stage, its last.
+  __device__ __forceinline__ void drain() {
+    for (int s = 0; s < kStages; ++s) {
       if (!(there >> s & 1u)) continue;
       const uint64_t t0 = tc::globaltimer();
       while (!tc::mbar_try_wait(&full[s], phase >> s & 1u) && tc::globaltimer() - t0 < 100000000ull) {
@@ -127,20 +134,20 @@ struct Ring {
   }
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
-    paged_few_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, Cut cut, int row_tiles) {
-  using C = Cfg<D, NT>;
-  constexpr int kWarps = C::kWarps;
+template <typename T, int D, int RT, int kSlots>
+__global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kSlots>::kBlocks)
+    paged_few_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, Cut cut, int row_blocks) {
+  using C = Cfg<D, RT, kSlots>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kWarps][C::kStages];
-  __shared__ float stat[kWarps][C::kRows][2];
+  __shared__ uint64_t full[kSlots][C::kStages];
+  __shared__ float stat[kSlots][C::kRows][2];
   __shared__ int abort_flag;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int b = blockIdx.z, h = blockIdx.y / row_tiles, rt = blockIdx.y % row_tiles;
-  const int R = a.G * c.L, row0 = rt * C::kRows;
+  const int slot = warp / RT, rt = warp % RT;  // the warps of a ring lie side by side
+  const int b = blockIdx.z, h = blockIdx.y / row_blocks, rb = blockIdx.y % row_blocks;
+  const int R = a.G * c.L, row0 = rb * C::kRows;
   const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
   const int i_last = (min(R, row0 + C::kRows) - 1) / a.G, i_first = max(row0 / a.G, rows.first);
   const int least = rows.limit(i_first), most = i_first <= i_last ? rows.limit(i_last) : 0;
@@ -149,7 +156,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     return;
   }
-  if (lane < C::kStages) tc::mbar_init(&full[warp][lane], 1);
+  if (rt == 0 && lane < C::kStages) tc::mbar_init(&full[slot][lane], 1);
   if (threadIdx.x == 0) abort_flag = 0;
   if (lane == 0) {
     tc::fence_mbar_init();
@@ -158,67 +165,73 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
   __syncthreads();
   const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidPagedAttn};
   const int all = (end - start + kTile - 1) / kTile;
-  Ring<D, kWarps, C::kStages, true> ring{&map, &c, c.pages + b * c.pages_stride, smem + warp * C::kStages * C::kUnit, full[warp], h, start, end,
-                                         warp, lane, all > warp ? (all - warp + kWarps - 1) / kWarps : 0, 0, -1, 0, 0u, 0u};
+  Ring<D, kSlots, C::kStages, true> ring{&map, &c, c.pages + b * c.pages_stride, smem + slot * C::kStages * C::kUnit, full[slot], h, start, end,
+                                         slot, lane, all > slot ? (all - slot + kSlots - 1) / kSlots : 0, rt == 0, 0, -1, 0, 0u, 0u};
   ring.look(0, kKidPagedAttn);
 #pragma unroll
   for (int s = 0; s < C::kStages; ++s) ring.issue(kKidPagedAttn);
 
   // Query rows as MMA operands; rows that are not there are zeros.
-  uint32_t qa[NT][D / 16][4];
-  int lim[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = row0 + kTile * nt + 8 * x + g, i = r / a.G;
-      lim[nt][x] = r < R ? rows.limit(i) : 0;
-      const bool real = r < R && i >= rows.first;
-      const T* q = real ? row_ptr<T>(a.q, a.lq, b, h * a.G + r % a.G, i) + 2 * t : nullptr;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-        for (int k8 = 0; k8 < 2; ++k8) qa[nt][ks][x + 2 * k8] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * k8) : 0u;
-    }
-
-  float o[NT][D / 8][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.f;
+  uint32_t qa[C::kQSmem ? 1 : D / 16][4];
+  uint4* const q_frag = reinterpret_cast<uint4*>(smem + C::kQ) + rt * (D / 16) * 32 + lane;  // [D / 16][lane]
+  int lim[2];
+  {
+    const T* q[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      m[nt][x] = minus_inf();
-      l[nt][x] = 0.f;
+      const int r = row0 + kTile * rt + 8 * x + g, i = r / a.G;
+      lim[x] = r < R ? rows.limit(i) : 0;
+      q[x] = r < R && i >= rows.first ? row_ptr<T>(a.q, a.lq, b, h * a.G + r % a.G, i) + 2 * t : nullptr;
     }
+    if (!C::kQSmem || slot == 0) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = q[e % 2] ? *reinterpret_cast<const uint32_t*>(q[e % 2] + 16 * ks + 8 * (e / 2)) : 0u;
+        if constexpr (C::kQSmem) {
+          q_frag[ks * 32] = make_uint4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qa[ks][e] = f[e];
+        }
+      }
+    }
+    if constexpr (C::kQSmem) __syncthreads();
   }
+
+  float o[D / 8][4], m[2] = {minus_inf(), minus_inf()}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
   const float c2 = a.scale_log2;
   // ldmatrix rows: keys for S (matrices: keys 0-7 and 8-15, each two 8-element pieces), keys for O.
   const int k_row = lane / 16 * 8 + lane % 8, k_piece = lane / 8 % 2, v_row = lane % 16, v_piece = lane / 16;
   bool ok = true;
   for (int u = 0; u < ring.units; ++u) {
     if (ring.wait(u, ok, wc)) {
-      const uint8_t* unit = ring.base + u % C::kStages * C::kUnit;
+      uint8_t* unit = ring.base + u % C::kStages * C::kUnit;
       const uint32_t ks0 = tc::smem_u32(unit), vs0 = ks0 + C::kHalf;
       const int k0 = ring.pos(u);
-      float s[NT][2][4];
+      float s[2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t kb[4];
+        uint32_t kb[4], f[4];
         ldsm(kb, ks0 + ks / 4 * C::kBlk + tc::sw128_off(k_row, ks % 4 * 2 + k_piece));
+        if constexpr (C::kQSmem) {
+          const uint4 x = q_frag[ks * 32];
+          f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        } else {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma<T>(s[nt][0], qa[nt][ks], kb[0], kb[1]);
-          mma<T>(s[nt][1], qa[nt][ks], kb[2], kb[3]);
+          for (int e = 0; e < 4; ++e) f[e] = qa[ks][e];
         }
+        mma<T>(s[0], f, kb[0], kb[1]);
+        mma<T>(s[1], f, kb[2], kb[3]);
       }
       // A unit that some row sees only in part: hidden scores are -inf; values that no row sees
       // become 0, since what lies there may be anything.
@@ -226,158 +239,134 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
       if (k0 + kTile > most) {
         for (int x = lane; x < kTile * C::kCB * 8; x += 32) {
           const int row = x / (C::kCB * 8), piece = x % (C::kCB * 8);
-          if (k0 + row >= most)
-            *reinterpret_cast<uint4*>(const_cast<uint8_t*>(unit) + C::kHalf + piece / 8 * C::kBlk + tc::sw128_off(row, piece % 8)) = make_uint4(0, 0, 0, 0);
+          if (k0 + row >= most) *reinterpret_cast<uint4*>(unit + C::kHalf + piece / 8 * C::kBlk + tc::sw128_off(row, piece % 8)) = make_uint4(0, 0, 0, 0);
         }
         tc::fence_async_smem();  // before the stage's next load
         __syncwarp();
       }
+      float top[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float top[2];
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = s[nt][n][e] * c2;
-            if (cut_unit && k0 + 8 * n + 2 * t + e % 2 >= lim[nt][e / 2]) v = minus_inf();
-            s[nt][n][e] = v;
-          }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) top[x] = fmaxf(fmaxf(s[nt][0][2 * x], s[nt][0][2 * x + 1]), fmaxf(s[nt][1][2 * x], s[nt][1][2 * x + 1]));
-        if (__any_sync(0xffffffffu, top[0] > m[nt][0] + kRescale || top[1] > m[nt][1] + kRescale)) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float v = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            const float up = fmaxf(m[nt][x], v);
-            const float f = up == minus_inf() ? 1.f : ex2(m[nt][x] - up);
-            m[nt][x] = up;
-            l[nt][x] *= f;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-              o[nt][d][2 * x] *= f;
-              o[nt][d][2 * x + 1] *= f;
-            }
-          }
+        for (int e = 0; e < 4; ++e) {
+          float v = s[n][e] * c2;
+          if (cut_unit && k0 + 8 * n + 2 * t + e % 2 >= lim[e / 2]) v = minus_inf();
+          s[n][e] = v;
         }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) top[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+      if (__any_sync(0xffffffffu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float shift = m[nt][x] == minus_inf() ? 0.f : m[nt][x];
+          float v = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+          const float up = fmaxf(m[x], v);
+          const float f = up == minus_inf() ? 1.f : ex2(m[x] - up);
+          m[x] = up;
+          l[x] *= f;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p = ex2(s[nt][n][2 * x + e] - shift);
-              s[nt][n][2 * x + e] = p;
-              l[nt][x] += p;
-            }
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][2 * x] *= f;
+            o[d][2 * x + 1] *= f;
+          }
         }
       }
-      uint32_t hi[NT][4], lo[NT][4];  // P and what its rounding leaves, as operands
+      uint32_t hi[4], lo[4];  // P and what its rounding leaves, as operands
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < 2; ++x) {
+        const float shift = m[x] == minus_inf() ? 0.f : m[x];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float p0 = s[nt][n][2 * x], p1 = s[nt][n][2 * x + 1];
-            const uint32_t w = tc::pack2<T>(p0, p1);
-            float h0, h1;
-            tc::unpack2<T>(w, h0, h1);
-            hi[nt][2 * n + x] = w;
-            lo[nt][2 * n + x] = tc::pack2<T>(p0 - h0, p1 - h1);
-          }
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = ex2(s[n][2 * x] - shift), p1 = ex2(s[n][2 * x + 1] - shift);
+          l[x] += p0 + p1;
+          const uint32_t w = tc::pack2<T>(p0, p1);
+          float h0, h1;
+          tc::unpack2<T>(w, h0, h1);
+          hi[2 * n + x] = w;
+          lo[2 * n + x] = tc::pack2<T>(p0 - h0, p1 - h1);
+        }
+      }
 #pragma unroll
       for (int dd = 0; dd < D / 16; ++dd) {
         uint32_t vb[4];
         ldsm_t(vb, vs0 + dd / 4 * C::kBlk + tc::sw128_off(v_row, dd % 4 * 2 + v_piece));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma<T>(o[nt][2 * dd], hi[nt], vb[0], vb[1]);
-          mma<T>(o[nt][2 * dd + 1], hi[nt], vb[2], vb[3]);
-          mma<T>(o[nt][2 * dd], lo[nt], vb[0], vb[1]);
-          mma<T>(o[nt][2 * dd + 1], lo[nt], vb[2], vb[3]);
-        }
+        mma<T>(o[2 * dd], hi, vb[0], vb[1]);
+        mma<T>(o[2 * dd + 1], hi, vb[2], vb[3]);
+        mma<T>(o[2 * dd], lo, vb[0], vb[1]);
+        mma<T>(o[2 * dd + 1], lo, vb[2], vb[3]);
       }
     }
-    if (!ok) {
-      ring.drain(u);
-      break;
-    }
-    __syncwarp();
+    // The ring's warps are done with the unit; all of them go on, or none.
+    if constexpr (RT > 1) ok = tc::named_sync_and(1 + slot, 32 * RT, ok);
+    else __syncwarp();
+    if (!ok) break;
     ring.issue(kKidPagedAttn);
   }
+  if (!ok) ring.drain();
 
-  // ---- the warps' results, one row tile after the other
+  // ---- the warps' results
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 1);
-      l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], 2);
-      if (lim[nt][x] == 0) {  // a row that sees nothing
-        m[nt][x] = minus_inf();
-        l[nt][x] = 0.f;
-      }
-      if (t == 0) {
-        stat[warp][kTile * nt + 8 * x + g][0] = m[nt][x];
-        stat[warp][kTile * nt + 8 * x + g][1] = l[nt][x];
-      }
+  for (int x = 0; x < 2; ++x) {
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    if (lim[x] == 0) {  // a row that sees nothing
+      m[x] = minus_inf();
+      l[x] = 0.f;
     }
+    if (t == 0) {
+      stat[slot][kTile * rt + 8 * x + g][0] = m[x];
+      stat[slot][kTile * rt + 8 * x + g][1] = l[x];
+    }
+  }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
-  float* red = reinterpret_cast<float*>(smem);  // [warp][16][D + 4]
+  float* red = reinterpret_cast<float*>(smem);  // [slot][row][D + 4]
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int x = 0; x < 2; ++x) {
+    const int q = kTile * rt + 8 * x + g;
+    float M = minus_inf();
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float M = minus_inf();
+    for (int w = 0; w < kSlots; ++w) M = fmaxf(M, stat[w][q][0]);
+    // (a warp that saw nothing but NaN has no maximum and a sum of NaN)
+    const float wgt = m[x] == minus_inf() ? 1.f : ex2(m[x] - M);
+    float* to = red + (slot * C::kRows + q) * (D + 4) + 2 * t;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][kTile * nt + 8 * x + g][0]);
-      // (a warp that saw nothing but NaN has no maximum and a sum of NaN)
-      const float wgt = m[nt][x] == minus_inf() ? 1.f : ex2(m[nt][x] - M);
-      float* to = red + (warp * kTile + 8 * x + g) * (D + 4) + 2 * t;
+    for (int d = 0; d < D / 8; ++d)
+      *reinterpret_cast<float2*>(to + 8 * d) = lim[x] == 0 ? make_float2(0.f, 0.f) : make_float2(o[d][2 * x] * wgt, o[d][2 * x + 1] * wgt);
+  }
+  __syncthreads();
+  for (int y = threadIdx.x; y < C::kRows * (D / 4); y += C::kWarps * 32) {
+    const int q = y / (D / 4), d = y % (D / 4) * 4, r = row0 + q;
+    if (r >= R) continue;
+    float M = minus_inf(), sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int d = 0; d < D / 8; ++d)
-        *reinterpret_cast<float2*>(to + 8 * d) =
-            lim[nt][x] == 0 ? make_float2(0.f, 0.f) : make_float2(o[nt][d][2 * x] * wgt, o[nt][d][2 * x + 1] * wgt);
+    for (int w = 0; w < kSlots; ++w) M = fmaxf(M, stat[w][q][0]);
+#pragma unroll
+    for (int w = 0; w < kSlots; ++w) {
+      const float mw = stat[w][q][0], lw = stat[w][q][1];
+      sum += mw == minus_inf() ? lw : lw * ex2(mw - M);
+      const float4 z = *reinterpret_cast<const float4*>(red + (w * C::kRows + q) * (D + 4) + d);
+      v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
     }
-    __syncthreads();
-    for (int y = threadIdx.x; y < kTile * (D / 4); y += kWarps * 32) {
-      const int q = y / (D / 4), d = y % (D / 4) * 4, r = row0 + kTile * nt + q;
-      if (r >= R) continue;
-      float M = minus_inf(), sum = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w][kTile * nt + q][0]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = stat[w][kTile * nt + q][0], lw = stat[w][kTile * nt + q][1];
-        sum += mw == minus_inf() ? lw : lw * ex2(mw - M);
-        const float4 z = *reinterpret_cast<const float4*>(red + (w * kTile + q) * (D + 4) + d);
-        v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
+    const int hq = h * a.G + r % a.G, i = r / a.G;
+    const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
+    if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w))
+      v = sum_apart<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M);
+    if (cut.splits > 1) {
+      const int64_t at = part_of(cut, b, a.Hq, hq, i, blockIdx.x);
+      *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;
+      if (d == 0) {
+        float* ml = part_stats(a, cut) + 2 * at;
+        ml[0] = M;
+        ml[1] = sum;
       }
-      const int hq = h * a.G + r % a.G, i = r / a.G;
-      const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
-      if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w))
-        v = sum_apart<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M);
-      if (cut.splits > 1) {
-        const int64_t at = part_of(cut, b, a.Hq, hq, i, blockIdx.x);
-        *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;
-        if (d == 0) {
-          float* ml = part_stats(a, cut) + 2 * at;
-          ml[0] = M;
-          ml[1] = sum;
-        }
-      } else {
-        const float fold = fold_sink(a.sinks, hq, M, sum), inv = sum == 0.f ? 0.f : fold / sum;
-        T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
-        *reinterpret_cast<uint2*>(out) = make_uint2(tc::pack2<T>(v.x * inv, v.y * inv), tc::pack2<T>(v.z * inv, v.w * inv));
-        if (a.lse && d == 0) a.lse[row] = sum == 0.f ? minus_inf() : (M + log2f(sum)) * kLn2;
-      }
+    } else {
+      const float fold = fold_sink(a.sinks, hq, M, sum), inv = sum == 0.f ? 0.f : fold / sum;
+      T* out = row_ptr<T>(a.out, a.lo, b, hq, i) + d;
+      *reinterpret_cast<uint2*>(out) = make_uint2(tc::pack2<T>(v.x * inv, v.y * inv), tc::pack2<T>(v.z * inv, v.w * inv));
+      if (a.lse && d == 0) a.lse[row] = sum == 0.f ? minus_inf() : (M + log2f(sum)) * kLn2;
     }
-    __syncthreads();
   }
 }
 
@@ -491,7 +480,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kWarps * 32) paged_weights_kernel
     const int end = min(start + chunk, first_pass ? rows.len : rows.limit(i_last));
     const int all = end > start ? (end - start + kTile - 1) / kTile : 0;
     Ring<D, kWarps, C::kStages, false> ring{&map, &c, c.pages + b * c.pages_stride, smem + warp * C::kStages * C::kUnit, full[warp], h, start, end,
-                                            warp, lane, all > warp ? (all - warp + kWarps - 1) / kWarps : 0, 0, -1, 0, 0u, phase};
+                                            warp, lane, all > warp ? (all - warp + kWarps - 1) / kWarps : 0, true, 0, -1, 0, 0u, phase};
     ring.look(0, kKidPagedWeights);
 #pragma unroll
     for (int s = 0; s < C::kStages; ++s) ring.issue(kKidPagedWeights);
@@ -559,7 +548,7 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kWarps * 32) paged_weights_kernel
             }
       }
       if (!ok) {
-        ring.drain(u);
+        ring.drain();
         break;
       }
       __syncwarp();
@@ -580,23 +569,31 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kWarps * 32) paged_weights_kernel
 
 // ---- host
 
-int row_tiles_of(const PagedArgs& a, int rows) { return (a.G * a.c.L + rows - 1) / rows; }
+// Rows of a block (of the weights: of a pass).
 int rows_a_block(const PagedArgs& a) { return a.c.D == 256 || a.G * a.c.L <= kTile ? kTile : 2 * kTile; }
+int row_blocks_of(const PagedArgs& a) { return (a.G * a.c.L + rows_a_block(a) - 1) / rows_a_block(a); }
+// Rings of a block: 4, and two blocks an SM, or 8 for a sequence that one block reads alone (200 tokens,
+// D = 64: 6.3 us instead of 8.3).
+int slots_of(const PagedArgs& a) { return a.c.D < 256 && rows_a_block(a) == kTile && a.max_len <= 512 ? 8 : 4; }
 
-// How a call's sequences are cut into chunks.
+// How a call's sequences are cut into chunks: for few pairs of a sequence and head into one wave of
+// blocks, of at least 128 tokens (2048 tokens, 8 heads: 10.3 us, of 256 12.3, of 512 14.4); for many into
+// chunks of 2048 at most, so that unequal sequences share the SMs (32 of 256 to 8192 tokens, 32 rows: 125 us,
+// of 1024 131, of 512 162); none where one block's warps read the sequence in what a join costs.
 Cut cut_few(const PagedArgs& a) {
-  const int64_t slots = a.c.num_sms > 0 ? a.c.num_sms : 1;
-  const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * row_tiles_of(a, rows_a_block(a));
-  const int step = 256;
+  constexpr int kStep = 64;  // tokens: a unit a ring
+  const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (a.c.D == 256 ? 1 : 2);
+  const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * row_blocks_of(a);
   const int64_t want = max((int64_t)1, slots / pairs);
   int64_t chunk = (a.max_len + want - 1) / want;
   if (pairs * 4 > slots) chunk = min(chunk, (int64_t)2048);
-  chunk = a.max_len <= 512 ? a.max_len : max(chunk, (int64_t)step);
+  chunk = a.max_len <= 512 ? a.max_len : max(chunk, (int64_t)128);
+  // Partial results take at most 64 MiB.
   const int64_t partial = (int64_t)a.c.B * a.Hq * a.c.L * (a.c.D + 2) * (int64_t)sizeof(float);
   const int64_t most = max((int64_t)1, ((int64_t)64 << 20) / partial);
   chunk = max(chunk, (a.max_len + most - 1) / most);
   Cut cut;
-  cut.chunk = (int)min((chunk + step - 1) / step * step, (int64_t)1 << 30);
+  cut.chunk = (int)min((chunk + kStep - 1) / kStep * kStep, (int64_t)1 << 30);
   cut.splits = (a.max_len + cut.chunk - 1) / cut.chunk;
   cut.rows = a.c.L;
   return cut;
@@ -604,18 +601,18 @@ Cut cut_few(const PagedArgs& a) {
 
 Cut cut_of(const PagedArgs& a) { return paged_chunk_takes(a) ? paged_chunk_cut(a) : cut_few(a); }
 
-template <typename T, int D, int NT>
-cudaError_t few_nt(const PagedArgs& a, cudaStream_t s) {
-  using C = Cfg<D, NT>;
-  auto* kern = paged_few_kernel<T, D, NT>;
+template <typename T, int D, int RT, int kSlots>
+cudaError_t few_t(const PagedArgs& a, cudaStream_t s) {
+  using C = Cfg<D, RT, kSlots>;
+  auto* kern = paged_few_kernel<T, D, RT, kSlots>;
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(kern, C::kSmem, ready);
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   if (!make_tmap_pages(&map, a.c, kTile)) return cudaErrorInvalidValue;
   const Cut cut = cut_few(a);
-  const int tiles = row_tiles_of(a, C::kRows);
-  kern<<<dim3(cut.splits, tiles * a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, cut, tiles);
+  const int blocks = row_blocks_of(a);
+  kern<<<dim3(cut.splits, blocks * a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, cut, blocks);
   return cudaGetLastError();
 }
 
@@ -660,8 +657,9 @@ cudaError_t run_d(const PagedArgs& a, Do what, cudaStream_t s) {
     if constexpr (D == 256) return weights_nt<T, D, 1>(a, s);
     else return rows_a_block(a) == kTile ? weights_nt<T, D, 1>(a, s) : weights_nt<T, D, 2>(a, s);
   }
-  if constexpr (D == 256) return few_nt<T, D, 1>(a, s);
-  else return rows_a_block(a) == kTile ? few_nt<T, D, 1>(a, s) : few_nt<T, D, 2>(a, s);
+  if constexpr (D == 256) return few_t<T, D, 1, 4>(a, s);
+  else if (rows_a_block(a) > kTile) return few_t<T, D, 2, 4>(a, s);
+  else return slots_of(a) == 8 ? few_t<T, D, 1, 8>(a, s) : few_t<T, D, 1, 4>(a, s);
 }
 
 template <typename T>
@@ -684,7 +682,7 @@ cudaError_t run(const PagedArgs& a, int dtype, Do what, cudaStream_t s) {
 
 bool paged_attn_launchable(const PagedArgs& a) {
   if (paged_chunk_takes(a)) return paged_chunk_blocks(a) <= 0x7fffffff;
-  return (int64_t)a.c.Hkv * row_tiles_of(a, rows_a_block(a)) <= 65535;
+  return (int64_t)a.c.Hkv * row_blocks_of(a) <= 65535;
 }
 size_t paged_attn_workspace(const PagedArgs& a) {
   const Cut cut = cut_of(a);

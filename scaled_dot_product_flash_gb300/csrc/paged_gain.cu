@@ -4,9 +4,9 @@
 // The product is transposed, S^T = K·Q^T with keys as its 128 rows, so that a thread has one key
 // and its sum over the queries never leaves the thread: no shuffles, no atomics, one order.  A block
 // has KT tiles of 128 keys of one KV head in shared memory for good and streams the Q tiles that see
-// them (rows as in paged_tc.cuh) and their logsumexps through a ring.  Four warps a key tile take
-// 2^(c·s − lse) from two TMEM buffers a tile, filled in turn; warp 8 loads Q, warp 9 issues the MMAs,
-// warp 10 fetches the logsumexps, negated and in units of log2.  Where there are few blocks a
+// them (rows as in paged_tc.cuh) and their logsumexps through a ring.  Eight warps a key tile take
+// 2^(c·s − lse) from two TMEM buffers a tile, filled in turn; three more load Q, issue the MMAs, and
+// fetch the logsumexps, negated and in units of log2.  Where there are few blocks a
 // cluster shares the Q tiles of its keys and adds its sums up in the order of its ranks.
 //
 // Rows without weight (padding, an lse of −inf, rows that a tile does not fill) have a logsumexp
@@ -21,8 +21,6 @@ namespace {
 using namespace tc;
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 352;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10;
 
 template <int D>
 struct GainLayout {
@@ -31,6 +29,9 @@ struct GainLayout {
   static constexpr int KT = D == 256 ? 1 : 2;      // key tiles of a block
   static constexpr int kStages = D == 256 ? 2 : 4;  // Q tiles in the ring
   static constexpr int kRingOff = KT * kTileBytes;
+  // Eight warps a key tile: four of its keys' quarters, twice, for the halves of the rows.
+  static constexpr int kLoadWarp = 8 * KT, kMmaWarp = kLoadWarp + 1, kLseWarp = kLoadWarp + 2;
+  static constexpr int kThreads = 32 * (kLoadWarp + 3);
   static constexpr int kBytes = kRingOff + kStages * kTileBytes + 1024;
 };
 
@@ -40,9 +41,22 @@ struct GainBars {
   uint64_t acc_full[KT][2], acc_empty[KT][2], mma_done;
   alignas(16) float lse[kStages][kBM];  // −lse·log2(e) of the rows, −inf for those without weight
   int dead[kStages];        // bit p: rows [32p, 32p + 32) hold some of those
-  float sums[KT][kBN];
+  float sums[KT][2][kBN];   // of each half of the rows
   uint32_t tmem_base;
   int abort;
+};
+
+// A Q tile: its first query and its group of heads; each role steps through the block's tiles by itself.
+struct Tile {
+  int i0, group, step_i, step_group;
+  __device__ __forceinline__ void next(const Tiling& t) {
+    i0 += step_i;
+    group += step_group;
+    if (group >= t.groups) {
+      group -= t.groups;
+      i0 += t.tokens;
+    }
+  }
 };
 
 // Σ 2^(c·s + x) over 32 rows of one key; rows e < from are hidden.
@@ -66,7 +80,7 @@ __device__ __forceinline__ void add_weights(uint64_t (&acc)[2], const uint32_t (
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(GainLayout<D>::kThreads, 1)
     paged_gain_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkv, PagedArgs a, Tiling t) {
   using L = GainLayout<D>;
   constexpr int kCB = L::kCB, KT = L::KT, kStages = L::kStages;
@@ -90,8 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t_first = i_first / t.tokens, t_last = (c.L - 1) / t.tokens;
   const int n_all = (t_last - t_first + 1) * t.groups;
   const int n = n_all > me ? (n_all - me + cl - 1) / cl : 0;  // of this block: me, me + cl, ...
-  auto tile_i0 = [&](int x) { return (t_first + (me + x * cl) / t.groups) * t.tokens; };
-  auto tile_group = [&](int x) { return (me + x * cl) % t.groups; };
+  Tile tile{(t_first + me / t.groups) * t.tokens, me % t.groups, cl / t.groups * t.tokens, cl % t.groups};
 
   if (threadIdx.x == 0) {
     bars.abort = 0;
@@ -101,16 +114,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.q_full[s], 1);
       mbar_init(&bars.q_empty[s], 1);
       mbar_init(&bars.lse_full[s], 32);
-      mbar_init(&bars.lse_empty[s], 4 * KT);
+      mbar_init(&bars.lse_empty[s], 8 * KT);
     }
     for (int w = 0; w < KT; ++w)
       for (int x = 0; x < 2; ++x) {
         mbar_init(&bars.acc_full[w][x], 1);
-        mbar_init(&bars.acc_empty[w][x], 4);
+        mbar_init(&bars.acc_empty[w][x], 8);
       }
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp) {
     tmem_alloc(&bars.tmem_base, 512);
     tmem_relinquish();
   }
@@ -123,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int* table = c.pages + b * c.pages_stride;
   const WaitCtx wc{&bars.abort, 0, a.wait_limit_ns, c.err, kKidPagedWeights};
 
-  if (warp == kLoadWarp) {
+  if (warp == L::kLoadWarp) {
     if (lane == 0) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tkv);
@@ -146,14 +159,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_expect_tx(&bars.q_full[s], kCB * t.heads * t.tokens * 128);
       __syncwarp();
       if (lane < kCB)
-        tma_load_4d(sm + L::kRingOff + s * L::kTileBytes + lane * 16384, &tq, &bars.q_full[s], lane * 64, h * a.G + tile_group(x) * t.heads, tile_i0(x), b);
+        tma_load_4d(sm + L::kRingOff + s * L::kTileBytes + lane * 16384, &tq, &bars.q_full[s], lane * 64, h * a.G + tile.group * t.heads, tile.i0, b);
+      tile.next(t);
       issued = x + 1;
     }
     if (!ok || bars.abort) {
       drain_wait(&bars.k_full, 0);
       for (int x = max(0, issued - kStages); x < issued; ++x) drain_wait(&bars.q_full[x % kStages], (x / kStages) & 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == L::kMmaWarp) {
     bool ok = __all_sync(kAll, mbar_wait(&bars.k_full, 0, wc));
     tc_fence_after();
     const uint64_t kd = sdesc_sw128(smem_u32(sm), 16, 1024);
@@ -178,18 +192,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mma_commit_w(&bars.mma_done);
     drain_wait(&bars.mma_done, 0);
-  } else if (warp == kLseWarp) {
+  } else if (warp == L::kLseWarp) {
     // Four rows a lane; the next tile's are fetched while this one's wait for their stage.
     float v[kBM / 32];
-    auto fetch = [&](int x) {
+    int token[kBM / 32];
+    const float* from[kBM / 32];  // the row's logsumexps, of the first tile's group and query 0
+#pragma unroll
+    for (int e = 0; e < kBM / 32; ++e) {
+      const int r = 32 * e + lane;
+      token[e] = r < t.heads * t.tokens ? r / t.heads : c.L;
+      from[e] = a.lse + ((int64_t)b * a.Hq + h * a.G + r % t.heads) * c.L;
+    }
+    auto fetch = [&] {
 #pragma unroll
       for (int e = 0; e < kBM / 32; ++e) {
-        const int r = 32 * e + lane, i = tile_i0(x) + r / t.heads;
-        const bool real = r < t.heads * t.tokens && i < c.L && i >= rows.first;
-        v[e] = real ? a.lse[((int64_t)b * a.Hq + h * a.G + tile_group(x) * t.heads + r % t.heads) * c.L + i] : minus_inf();
+        const int i = tile.i0 + token[e];
+        v[e] = i < c.L && i >= rows.first ? from[e][(int64_t)tile.group * t.heads * c.L + i] : minus_inf();
       }
+      tile.next(t);
     };
-    if (n > 0) fetch(0);
+    if (n > 0) fetch();
     bool ok = true;
     for (int x = 0; ok && x < n; ++x) {
       const int s = x % kStages;
@@ -201,21 +223,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         y[e] = none ? minus_inf() : -v[e] * kLog2e;
         dead |= __any_sync(kAll, none) ? 1 << e : 0;
       }
-      if (x + 1 < n) fetch(x + 1);
+      if (x + 1 < n) fetch();
       if (!(ok = __all_sync(kAll, mbar_wait(&bars.lse_empty[s], ((x / kStages) & 1) ^ 1, wc)))) break;
 #pragma unroll
       for (int e = 0; e < kBM / 32; ++e) bars.lse[s][32 * e + lane] = y[e];
       if (lane == 0) bars.dead[s] = dead;
       mbar_arrive(&bars.lse_full[s]);
     }
-  } else if (warp < 4 * KT) {
-    const int w = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+  } else {
+    const int w = warp / 8, half = warp / 4 % 2, quarter = warp % 4, r = quarter * 32 + lane;
     const int key = k0 + w * kBN + r;
     const uint32_t at = tmem_addr(tbase, quarter * 32, 2 * w * kBM);
     uint64_t acc[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
     bool ok = true;
     for (int x = 0; x < n; ++x) {
-      const int s = x % kStages, buf = x % 2, i0 = tile_i0(x);
+      const int s = x % kStages, buf = x % 2, i0 = tile.i0;
+      tile.next(t);
       ok = __all_sync(kAll, mbar_wait(&bars.lse_full[s], (x / kStages) & 1, wc) && mbar_wait(&bars.acc_full[w][buf], (x / 2) & 1, wc));
       if (!ok) break;
       tc_fence_after();
@@ -224,11 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int from = cut ? min(max(key - off - i0, 0), kBM) * t.heads : 0;
       const int dead = bars.dead[s];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
+      for (int x2 = 0; x2 < 2; ++x2) {
+        const int p = 2 * half + x2;  // rows [32p, 32p + 32)
         uint32_t sv[32];
         tmem_ld32(at + buf * kBM + 32 * p, sv);
         tmem_ld_wait(sv);
-        if (p == 3) {  // the scores are in registers: the buffer may be filled again
+        if (x2 == 1) {  // the scores are in registers: the buffer may be filled again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.acc_empty[w][buf]);
@@ -244,17 +268,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     float p0, p1, p2, p3;
     f2unpack(acc[0], p0, p1);
     f2unpack(acc[1], p2, p3);
-    bars.sums[w][r] = (p0 + p1) + (p2 + p3);
+    bars.sums[w][half][r] = (p0 + p1) + (p2 + p3);
   }
   tc_fence_before();
   cluster.sync();  // (a cluster of one: the block's barrier)
-  if (warp == kMmaWarp) tmem_dealloc(tbase, 512);
+  if (warp == L::kMmaWarp) tmem_dealloc(tbase, 512);
   if (me == 0)
-    for (int x = threadIdx.x; x < KT * kBN; x += kThreads) {
+    for (int x = threadIdx.x; x < KT * kBN; x += L::kThreads) {
       const int key = k0 + x;
       if (key >= rows.len) break;
       float sum = 0.f;
-      for (int p = 0; p < cl; ++p) sum += cluster.map_shared_rank(&bars.sums[0][0], p)[x];
+      for (int p = 0; p < cl; ++p) {
+        const float* y = cluster.map_shared_rank(&bars.sums[x / kBN][0][x % kBN], p);
+        sum += y[0] + y[kBN];
+      }
       if ((unsigned)table[key / c.page_size] >= (unsigned)c.num_pages) sum = 0.f;  // its page is bad
       float* to = a.weights + b * a.w_batch + h * a.w_head + key;
       *to = (key >= off + rows.first ? 0.f : *to) + sum;
@@ -274,11 +301,13 @@ cudaError_t gain_d(const PagedArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.c.B * a.c.Hkv, blocks = (a.max_len + L::KT * kBN - 1) / (L::KT * kBN);
   const int64_t q_tiles = (int64_t)t.groups * ((a.c.L + t.tokens - 1) / t.tokens);
+  // Blocks for three waves and more, so that under the causal mask, where the first keys have the most
+  // rows, they end together; at least 8 Q tiles each.
   int cl = 1;
-  while (cl < 8 && units * blocks * cl * 2 <= a.c.num_sms && cl * 4 <= q_tiles) cl *= 2;
+  while (cl < 8 && units * blocks * cl < 2 * (int64_t)a.c.num_sms && cl * 16 <= q_tiles) cl *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cl), (unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

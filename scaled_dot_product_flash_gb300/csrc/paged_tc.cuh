@@ -14,7 +14,8 @@ constexpr int kBN = 128;  // keys of a KV tile
 struct Tiling {
   int heads, tokens;  // of a Q tile
   int groups;         // of heads: G / heads
-  int blocks;         // of two Q tiles (one for D = 256): queries of a sequence
+  int tiles;          // Q tiles of a block: 2, or 1 (head dim 256, and calls of one tile a KV head)
+  int blocks;         // of a sequence's queries
   int whole;          // of those, from the last one on: not cut
   int box;            // tokens of a box of keys
   Cut cut;

@@ -332,6 +332,27 @@ def test_sequences_of_several_chunks(dtype, G, L, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,L,n,D", [(4, 1, 10240, 10240, 32), (8, 2, 5200, 5300, 64), (32, 8, 1500, 9000, 128), (2, 1, 3000, 20000, 256)])
+def test_long_chunks_agree_with_the_dense_kernel(Hq, Hkv, L, n, D, causal):
+    """Whole waves of blocks and what is left over of them, at sizes that are too large for the oracle.
+    Both kernels' outputs lie within half·|o| + half·A of the exact ones (paged_util.check), A at most
+    sqrt(sum w^2)-fold less than max|v| here: values are N(0, 1), outputs of n >= 1000 visible tokens
+    below 0.5 and A below 1; rows that see fewer tokens are left to the other tests."""
+    rng = np.random.default_rng(42)
+    cache, table, _, _ = fill(rng, [n], Hkv, D, 64, "bf16")
+    rows = cache[table[0].long().cuda()].permute(1, 2, 0, 3, 4).flatten(2, 3)[:, :, :n].unsqueeze(1)
+    q = draw_rows(rng, (1, Hq, L, D), "bf16").cuda()
+    out, lse = api.paged_attention(q, cache, table.cuda(), ints([n]).cuda(), need_lse=True, is_causal="bottom_right" if causal else False)
+    want, want_lse = api.attention_forward(q, rows[0].contiguous(), rows[1].contiguous(), is_causal="bottom_right" if causal else False)
+    api.poll_status()
+    first = max(0, 1000 - (n - L))
+    half = 2.0**-9
+    assert (out - want)[:, :, first:].float().abs().max() <= 2 * half * (0.5 + 1.0)
+    assert (lse - want_lse).abs().max() <= 2.0**-15
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("L", [2, 50])
 def test_layouts_and_another_stream(L):
     rng = np.random.default_rng(43)
