@@ -21,43 +21,49 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWriteThreads = 256, kWriteEach = 4;
+constexpr int kWriteEach = 4;
 
+// Grid: (blocks of rows · keys and values of each head, sequences); `per` rows are moved at a time.
 template <int D>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(CacheArgs c) {
+__global__ void __launch_bounds__(256) paged_write_kernel(CacheArgs c, int per, int chunks, Divider by_page) {
   constexpr int U = D / 8;  // 16-byte pieces of a row
-  const int b = blockIdx.y;
-  const int table = c.pages_per_seq * c.page_size;
-  const int len = cache_len(c, b, table, kKidPagedWrite);
+  const int b = blockIdx.y, head = blockIdx.x / chunks, which = head >= c.Hkv, h = head - which * c.Hkv;
+  const int row = threadIdx.x / U, piece = threadIdx.x % U, i0 = (blockIdx.x - head * chunks) * per * kWriteEach + row;
+  const int len = cache_len(c, b, c.pages_per_seq * c.page_size, kKidPagedWrite);
   // (a sequence whose length lies past the table's end keeps its rows' positions)
-  const int n = max(c.lens[b], 0);
-  const int count = c.counts ? min(max(c.counts[b], 0), c.L) : c.L;
-  const int rows = 2 * c.Hkv * c.L;
+  const int64_t first = (int64_t)max(c.lens[b], 0) - c.L;
+  const int pad = c.counts ? c.L - min(max(c.counts[b], 0), c.L) : 0;
+  if (row >= per) return;
+  const uint16_t* from = row_ptr<uint16_t>(which ? c.v : c.k, which ? c.lv : c.lk, b, h, 0) + 8 * piece;
+  const int64_t stride = which ? c.lv.sl : c.lk.sl;
+  const int* table = c.pages + b * c.pages_stride;
   uint4 x[kWriteEach];
-  uint4* to[kWriteEach];
+  int page[kWriteEach], place[kWriteEach];
 #pragma unroll
   for (int e = 0; e < kWriteEach; ++e) {
-    const int64_t p = ((int64_t)blockIdx.x * kWriteEach + e) * kWriteThreads + threadIdx.x;
-    const int row = (int)min(p / U, (int64_t)rows), piece = (int)(p % U);
-    to[e] = nullptr;
-    if (row >= rows) continue;
-    const int i = row % c.L, which = row / c.L / c.Hkv, h = row / c.L % c.Hkv;
-    const int64_t pos = (int64_t)n - c.L + i;
-    if (i < c.L - count || pos < 0 || pos >= len) continue;
-    const int page = cache_page(c, b, (int)pos, kKidPagedWrite);
-    if (page < 0) continue;
-    x[e] = reinterpret_cast<const uint4*>(row_ptr<uint16_t>(which ? c.v : c.k, which ? c.lv : c.lk, b, h, i))[piece];
-    to[e] = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(c.data) + paged_row(c, page, which, h, (int)pos % c.page_size)) + piece;
+    const int i = i0 + e * per;
+    const int64_t pos = first + i;
+    page[e] = -1;
+    if (i >= c.L || i < pad || pos < 0 || pos >= len) continue;
+    const int slot = by_page((int)pos);
+    page[e] = table[slot];
+    place[e] = (int)pos - slot * c.page_size;
+    x[e] = *reinterpret_cast<const uint4*>(from + i * stride);
   }
 #pragma unroll
-  for (int e = 0; e < kWriteEach; ++e)
-    if (to[e]) *to[e] = x[e];
+  for (int e = 0; e < kWriteEach; ++e) {
+    if ((unsigned)page[e] < (unsigned)c.num_pages)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(c.data) + paged_row(c, page[e], which, h, place[e]) + 8 * piece) = x[e];
+    else if (i0 + e * per < c.L && i0 + e * per >= pad && first + i0 + e * per >= 0 && first + i0 + e * per < len)
+      report_error(c.err, kDevErrIndex, kKidPagedWrite);
+  }
 }
 
 template <int D>
 cudaError_t write_d(const CacheArgs& c, cudaStream_t s) {
-  const int64_t pieces = (int64_t)2 * c.Hkv * c.L * (D / 8), each = kWriteThreads * kWriteEach;
-  paged_write_kernel<D><<<dim3((unsigned)((pieces + each - 1) / each), c.B), kWriteThreads, 0, s>>>(c);
+  const int per = min(c.L, 256 / (D / 8)), threads = (per * (D / 8) + 31) / 32 * 32;
+  const int chunks = (c.L + per * kWriteEach - 1) / (per * kWriteEach);
+  paged_write_kernel<D><<<dim3((unsigned)(2 * (int64_t)c.Hkv * chunks), c.B), threads, 0, s>>>(c, per, chunks, divider(c.page_size));
   return cudaGetLastError();
 }
 
