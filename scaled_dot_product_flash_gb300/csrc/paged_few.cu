@@ -85,19 +85,16 @@ struct Ring {
   uint32_t there, phase;                 // stages that hold a unit; the parity to wait for
 
   __device__ __forceinline__ int pos(int u) const { return start + (slot + u * kSlots) * kTile; }
-  // This lane's entry of the page table, and whether it is a page.
-  __device__ __forceinline__ void look(int u0, unsigned kid) {
+  // Takes the page table's entry for unit u0 + lane, if there is such a unit and it is a page.
+  __device__ __forceinline__ void take(int u0, int found, unsigned kid) {
     base_unit = u0;
     entry = -1;
-    const int p = u0 + lane < units ? pos(u0 + lane) : end;
-    if (p < end) {
-      entry = table[p / c->page_size];
-      if ((unsigned)entry >= (unsigned)c->num_pages) {
-        report_error(c->err, kDevErrIndex, kid);
-        entry = -1;
-      }
+    if (u0 + lane < units) {
+      if ((unsigned)found < (unsigned)c->num_pages) entry = found;
+      else report_error(c->err, kDevErrIndex, kid);
     }
   }
+  __device__ __forceinline__ void look(int u0, unsigned kid) { take(u0, u0 + lane < units ? table[pos(u0 + lane) / c->page_size] : -1, kid); }
   // Starts the loads of the next unit (all lanes).
   __device__ __forceinline__ void issue(unsigned kid) {
     const int u = issued++, s = u % kStages;
@@ -148,6 +145,10 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
   const int slot = warp / RT, rt = warp % RT;  // the warps of a ring lie side by side
   const int b = blockIdx.z, h = blockIdx.y / row_blocks, rb = blockIdx.y % row_blocks;
   const int R = a.G * c.L, row0 = rb * C::kRows;
+  // The page table's entries of the first units are on their way while the length is; it says which count.
+  const int* table = c.pages + b * c.pages_stride;
+  const int64_t guess = ((int64_t)blockIdx.x * cut.chunk + (slot + lane * kSlots) * kTile) / c.page_size;
+  const int found = guess < c.pages_per_seq ? table[guess] : -1;
   const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
   const int i_last = (min(R, row0 + C::kRows) - 1) / a.G, i_first = max(row0 / a.G, rows.first);
   const int least = rows.limit(i_first), most = i_first <= i_last ? rows.limit(i_last) : 0;
@@ -165,9 +166,9 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
   __syncthreads();
   const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidPagedAttn};
   const int all = (end - start + kTile - 1) / kTile;
-  Ring<D, kSlots, C::kStages, true> ring{&map, &c, c.pages + b * c.pages_stride, smem + slot * C::kStages * C::kUnit, full[slot], h, start, end,
+  Ring<D, kSlots, C::kStages, true> ring{&map, &c, table, smem + slot * C::kStages * C::kUnit, full[slot], h, start, end,
                                          slot, lane, all > slot ? (all - slot + kSlots - 1) / kSlots : 0, rt == 0, 0, -1, 0, 0u, 0u};
-  ring.look(0, kKidPagedAttn);
+  ring.take(0, found, kKidPagedAttn);
 #pragma unroll
   for (int s = 0; s < C::kStages; ++s) ring.issue(kKidPagedAttn);
 
