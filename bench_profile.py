@@ -9,8 +9,10 @@ timing.  Every launch goes through the C ABI exactly as in normal use.
 --L is Lq (and Lkv unless --Lkv is given).  --mask padding passes a boolean key-padding
 mask [B, 1, 1, Lkv] hiding the last 10% of the keys; --mask additive passes one N(0, 1)
 [Lq, Lkv] mask in the element type, shared by every batch and head (seed 6).  The cache
-operations work on sequences of --Lkv tokens in pages of --page tokens, in random order, and
-on the last --L rows of each; rotary turns q and k of --L rows by positions that end at --Lkv.
+operations, of the 4-bit cache and of 16-bit pages, work on sequences of --Lkv tokens in pages of
+--page tokens, in random order, and on the last --L rows of each; paged_evict keeps --L tokens of
+them, an eighth of those the last ones; rotary turns q and k of --L rows by positions that end at
+--Lkv.
 Prints the mean CUDA-event time per call (after one warm-up call).
 """
 from __future__ import annotations
@@ -57,6 +59,8 @@ def serving_op(a):
     pages = torch.randperm(a.B * per, generator=torch.Generator().manual_seed(7))
     pages = pages.to(torch.int32).view(a.B, per).cuda()
     lens = torch.full((a.B,), n, dtype=torch.int32, device="cuda")
+    if a.op.startswith("paged"):
+        return paged_op(a, q, k, v, pages, lens)
     cache = api.cache_empty(a.B * per, a.Hkv, a.page, a.D, q.dtype)
     gen = torch.Generator(device="cuda").manual_seed(8)
     for at in range(0, n, 4096):  # fill it
@@ -75,10 +79,32 @@ def serving_op(a):
             row * n * 1.25 + 2 * es * q.numel())
 
 
+def paged_op(a, q, k, v, pages, lens):
+    """serving_op of the operations on 16-bit pages."""
+    n, row, es = a.Lkv or a.L, a.B * a.Hkv * a.D, q.element_size()
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    cache = api.paged_empty(pages.numel(), a.Hkv, a.page, a.D, q.dtype)
+    cache.copy_(torch.randn(cache.shape, generator=gen, device="cuda", dtype=q.dtype))
+    if a.op == "paged_write":
+        return lambda: api.paged_write(cache, k, v, pages, lens), 4 * es * row * a.L
+    weights = torch.rand((a.B, a.Hkv, n), generator=gen, device="cuda")
+    if a.op == "paged_evict":
+        out = dict(new_lens=torch.empty_like(lens), new_weights=torch.empty_like(weights))
+        return (lambda: api.paged_evict(cache, pages, lens, weights, a.L, a.L // 8, **out),
+                4 * es * row * a.L)
+    out, lse = api.paged_attention(q, cache, pages, lens, need_lse=True)
+    if a.op == "paged_weights":
+        return (lambda: api.paged_weights(q, cache, pages, lens, lse, weights),
+                row * n * es + es * q.numel() + 8 * weights.numel())
+    return (lambda: api.paged_attention(q, cache, pages, lens, out=out),
+            2 * es * row * n + 2 * es * q.numel())
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", choices=["fwd", "bwd", "step", "rotary", "cache_write",
-                                     "cache_read", "cache_attn"], default="fwd")
+                                     "cache_read", "cache_attn", "paged_write", "paged_attn",
+                                     "paged_weights", "paged_evict"], default="fwd")
     ap.add_argument("--B", type=int, default=2)
     ap.add_argument("--Hq", type=int, default=32)
     ap.add_argument("--Hkv", type=int, default=8)

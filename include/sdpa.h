@@ -403,8 +403,9 @@ int sdpa_paged_write(const sdpa_cache_t* cache, const void* k, const void* v,
  * Attention of q [B,Hq,Lq,D] over the cached keys and values, as sdpa_cache_attn has it (sinks,
  * lse, is_causal, max_len, workspace), for one token or a few a sequence and for chunks of
  * thousands.  Rows that are not real see nothing, whatever is in them.  A token that a row does not
- * see leaves no trace in it, whatever its key and value; a NaN in one that it sees makes the row's
- * outputs NaN.
+ * see leaves no trace in it, whatever its key and value.  Of one that it sees, a NaN in the key makes
+ * the row NaN, a NaN in the value that column of its output, and an infinite value makes it infinite
+ * or (where the weight is next to nothing) NaN.
  */
 size_t sdpa_paged_attn_workspace_size(const sdpa_cache_t* cache, int B, int Hq, int Lq, int max_len);
 int sdpa_paged_attn(const sdpa_cache_t* cache, const void* q, void* out, float* lse,
@@ -440,7 +441,8 @@ int sdpa_paged_weights(const sdpa_cache_t* cache, const void* q, const float* ls
  *   weights     fp32 [B][Hkv][slots], read; new_weights the same shape, written: the kept
  *               tokens' weights, 0 in the slots past them; may be weights itself.
  *               weight_strides: (batch, head) of weights, then of new_weights.
- * Sequences of at most `budget` tokens keep all of them.  A token whose page is bad, or
+ * Sequences of at most `budget` tokens keep all of them; one longer than slots is reported and taken
+ * as slots long.  A token whose page is bad, or
  * whose new place's is, is not moved (reported).  Two tokens must not share a place.
  */
 int sdpa_paged_evict(const sdpa_cache_t* cache, const float* weights, float* new_weights,

@@ -131,28 +131,44 @@ __device__ __forceinline__ int64_t paged_row(const CacheArgs& c, int page, int w
   return ((((int64_t)page * 2 + which) * c.Hkv + h) * c.page_size + place) * c.D;
 }
 
-// Columns d..d+3 of Σ exp2(c·q·k_j − M)·v_j over the tokens [from, to) of sequence b that query
-// (hq, i) of KV head h sees, product by product in fp32: the way out for outputs that came out NaN,
-// where a value that the row does not see, or the remainder of a weight times an infinite one, gave 0·∞.
+// For columns d..d+3 of an output o of query (hq, i) of KV head h over the tokens [from, to) of
+// sequence b, some of which came out NaN without a reason in the row's scores: those whose values
+// are not all finite are infinite or NaN accordingly; others have met a value that the row does not
+// see, under a weight of 0, and are Σ exp2(c·q·k_j − M)·v_j once more, product by product in fp32.
 template <typename T, int D>
-__device__ __noinline__ float4 sum_apart(const PagedArgs& a, int b, int h, int hq, int i, int d, int from, int to, float M) {
+__device__ __noinline__ float4 mend_output(const PagedArgs& a, int b, int h, int hq, int i, int d, int from, int to, float M, float4 o) {
   const CacheArgs& c = a.c;
   const T* q = row_ptr<T>(a.q, a.lq, b, hq, i);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = from; j < to; ++j) {
-    const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
-    if ((unsigned)page >= (unsigned)c.num_pages) continue;
-    const T* k = reinterpret_cast<const T*>(c.data) + paged_row(c, page, 0, h, place);
-    const T* v = reinterpret_cast<const T*>(c.data) + paged_row(c, page, 1, h, place) + d;
-    float s = 0.f;
-    for (int x = 0; x < D; ++x) s = fmaf(Elem<T>::to_f(q[x]), Elem<T>::to_f(k[x]), s);
-    const float p = tc::ex2(s * a.scale_log2 - M);
-    o.x = fmaf(p, Elem<T>::to_f(v[0]), o.x);
-    o.y = fmaf(p, Elem<T>::to_f(v[1]), o.y);
-    o.z = fmaf(p, Elem<T>::to_f(v[2]), o.z);
-    o.w = fmaf(p, Elem<T>::to_f(v[3]), o.w);
+  const T* data = reinterpret_cast<const T*>(c.data);
+  float x[4] = {o.x, o.y, o.z, o.w}, seen[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int j = from; j < to; ++j) {
+      const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
+      if ((unsigned)page >= (unsigned)c.num_pages) continue;
+      const T* v = data + paged_row(c, page, 1, h, place) + d;
+      float p = 0.f;
+      if (pass == 1) {
+        const T* k = data + paged_row(c, page, 0, h, place);
+        float s = 0.f;
+        for (int y = 0; y < D; ++y) s = fmaf(Elem<T>::to_f(q[y]), Elem<T>::to_f(k[y]), s);
+        p = tc::ex2(s * a.scale_log2 - M);
+      }
+      for (int y = 0; y < 4; ++y) {
+        const float z = Elem<T>::to_f(v[y]);
+        if (pass == 1) sum[y] = fmaf(p, z, sum[y]);
+        else if (!(fabsf(z) < __builtin_huge_valf())) seen[y] += z;  // inf - inf: NaN
+      }
+    }
+    bool again = false;
+    for (int y = 0; y < 4; ++y)
+      if (x[y] != x[y]) {
+        if (pass == 1 && seen[y] == 0.f) x[y] = sum[y];
+        else if (pass == 0 && seen[y] != 0.f) x[y] = seen[y];  // (a NaN stays one)
+        again |= seen[y] == 0.f;
+      }
+    if (!again) break;
   }
-  return o;
+  return make_float4(x[0], x[1], x[2], x[3]);
 }
 
 }  // namespace sdpa

@@ -15,7 +15,7 @@
 // second MMA is hidden behind the copies.
 // The running maximum is raised only when a score passes it by 2^8: one vote a unit, no shuffles.
 // An output that is NaN without a reason in its row's scores has met a value that is not finite,
-// perhaps one that its row does not see: it is summed anew, one product after the other.
+// perhaps one that its row does not see: mend_output looks.
 #include "paged.h"
 
 namespace sdpa {
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
     const int hq = h * a.G + r % a.G, i = r / a.G;
     const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
     if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w))
-      v = sum_apart<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M);
+      v = mend_output<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M, v);
     if (cut.splits > 1) {
       const int64_t at = part_of(cut, b, a.Hq, hq, i, blockIdx.x);
       *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;

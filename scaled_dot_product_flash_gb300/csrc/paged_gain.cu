@@ -163,10 +163,9 @@ __global__ void __launch_bounds__(GainLayout<D>::kThreads, 1)
       tile.next(t);
       issued = x + 1;
     }
-    if (!ok || bars.abort) {
-      drain_wait(&bars.k_full, 0);
-      for (int x = max(0, issued - kStages); x < issued; ++x) drain_wait(&bars.q_full[x % kStages], (x / kStages) & 1);
-    }
+    // No copy is in flight when the block exits, whatever its other warps met.
+    drain_wait(&bars.k_full, 0);
+    for (int x = max(0, issued - kStages); x < issued; ++x) drain_wait(&bars.q_full[x % kStages], (x / kStages) & 1);
   } else if (warp == L::kMmaWarp) {
     bool ok = __all_sync(kAll, mbar_wait(&bars.k_full, 0, wc));
     tc_fence_after();

@@ -171,6 +171,66 @@ def test_bad_pages_and_lengths():
     assert torch.equal(cache.view(torch.int16), good.view(torch.int16))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("scale", [0.1, 0.0, -0.1])
+@pytest.mark.parametrize("L", [4, 20, 70, 200])
+def test_bad_pages_in_chunks(L, scale, D):
+    """Tokens 16..31 and 112..127 lie on pages that do not exist, for attention and weights alike."""
+    rng = np.random.default_rng(6)
+    n, gone = 260, [*range(16, 32), *range(112, 128)]
+    cache, table, ks, vs = fill(rng, [n], 1, D, 16, "bf16")
+    q = draw_rows(rng, (1, 4, L, D), "bf16")
+    broken = table.clone()
+    broken[0, 1], broken[0, 7] = -1, cache.shape[0]
+    out, lse = api.paged_attention(q.cuda(), cache, broken.cuda(), ints([n]).cuda(), need_lse=True, scale=scale)
+    with pytest.raises(_lib.SdpaError) as e:
+        api.poll_status()
+    assert e.value.status == INDEX
+    # Query i sees the tokens that are there up to its own; those before the first query lie before all rows.
+    kept = np.delete(np.arange(n), gone)
+    assert n - L >= 128 or L == 200
+    if L <= 130:
+        check(out, lse, q, [np.delete(ks[0], gone, 1)], [np.delete(vs[0], gone, 1)], scale, True, "bf16")
+    else:
+        late = kept[kept >= n - L].size                                          # rows of whose own tokens are there
+        rows = np.searchsorted(np.arange(n - L, n), kept[kept >= n - L])
+        check(out[:, :, rows], lse[:, :, rows].contiguous(), q[:, :, rows], [ks[0][:, kept]], [vs[0][:, kept]], scale, True, "bf16", few=False)
+        assert late == rows.size
+    w = torch.zeros(1, 1, n, device="cuda")
+    api.paged_weights(q.cuda(), cache, broken.cuda(), ints([n]).cuda(), lse, w, scale=scale)
+    with pytest.raises(_lib.SdpaError):
+        api.poll_status()
+    assert not w[0, 0, gone].any() and abs(w.sum().item() - 4 * L) < 1e-2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,L,D", [(4, 60, 64), (4, 300, 128), (2, 40, 256), (4, 8, 64), (4, 1, 128)])
+def test_nan_values_cost_little(G, L, D):
+    """A cache whose values are NaN throughout takes no more than 100 times as long (it is not
+    summed anew by hand), and everything that sees one is NaN."""
+    rng = np.random.default_rng(34)
+    n = 6000
+    cache, table, _, _ = fill(rng, [n], 2, D, 64, "bf16")
+    q = draw_rows(rng, (1, 2 * G, L, D), "bf16").cuda()
+    at, _ = on_device(table, [n])
+
+    def timed():
+        api.paged_attention(q, cache, *at)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        out, _ = api.paged_attention(q, cache, *at)
+        b.record()
+        b.synchronize()
+        return out, a.elapsed_time(b)
+
+    _, plain = timed()
+    cache[:, 1] = NAN
+    out, slow = timed()
+    api.poll_status()
+    assert out.isnan().all() and slow < 100 * max(plain, 0.05)
+
+
 CASES = [
     # dtype, Hq, Hkv, L, D, page, lens, counts
     ("bf16", 1, 1, 1, 64, 16, [1], None),
