@@ -131,44 +131,49 @@ __device__ __forceinline__ int64_t paged_row(const CacheArgs& c, int page, int w
   return ((((int64_t)page * 2 + which) * c.Hkv + h) * c.page_size + place) * c.D;
 }
 
-// For columns d..d+3 of an output o of query (hq, i) of KV head h over the tokens [from, to) of
-// sequence b, some of which came out NaN without a reason in the row's scores: those whose values
-// are not all finite are infinite or NaN accordingly; others have met a value that the row does not
-// see, under a weight of 0, and are Σ exp2(c·q·k_j − M)·v_j once more, product by product in fp32.
-template <typename T, int D>
-__device__ __noinline__ float4 mend_output(const PagedArgs& a, int b, int h, int hq, int i, int d, int from, int to, float M, float4 o) {
+// For columns [d, d + N) of an output o of query (hq, i) of KV head h over the tokens [from, to) of
+// sequence b, some of which came out NaN without a reason in the row's scores, since a product meets
+// every value of a tile, under a weight of 0 too.  Those with a value among the tokens that is not finite are
+// infinite or NaN accordingly; the others, where the value belongs to a token that the row does not
+// see, are Σ exp2(c·q·k_j − M)·v_j once more, product by product in fp32.
+template <typename T, int D, int N>
+__device__ __noinline__ void mend_columns(const PagedArgs& a, int b, int h, int hq, int i, int d, int from, int to, float M, float* o) {
   const CacheArgs& c = a.c;
   const T* q = row_ptr<T>(a.q, a.lq, b, hq, i);
   const T* data = reinterpret_cast<const T*>(c.data);
-  float x[4] = {o.x, o.y, o.z, o.w}, seen[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int j = from; j < to; ++j) {
-      const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
-      if ((unsigned)page >= (unsigned)c.num_pages) continue;
-      const T* v = data + paged_row(c, page, 1, h, place) + d;
-      float p = 0.f;
-      if (pass == 1) {
-        const T* k = data + paged_row(c, page, 0, h, place);
-        float s = 0.f;
-        for (int y = 0; y < D; ++y) s = fmaf(Elem<T>::to_f(q[y]), Elem<T>::to_f(k[y]), s);
-        p = tc::ex2(s * a.scale_log2 - M);
-      }
-      for (int y = 0; y < 4; ++y) {
-        const float z = Elem<T>::to_f(v[y]);
-        if (pass == 1) sum[y] = fmaf(p, z, sum[y]);
-        else if (!(fabsf(z) < __builtin_huge_valf())) seen[y] += z;  // inf - inf: NaN
-      }
+  uint32_t open = 0;  // columns whose NaN is not explained yet
+  for (int y = 0; y < N; ++y)
+    if (o[y] != o[y]) {
+      open |= 1u << y;
+      o[y] = 0.f;
     }
-    bool again = false;
-    for (int y = 0; y < 4; ++y)
-      if (x[y] != x[y]) {
-        if (pass == 1 && seen[y] == 0.f) x[y] = sum[y];
-        else if (pass == 0 && seen[y] != 0.f) x[y] = seen[y];  // (a NaN stays one)
-        again |= seen[y] == 0.f;
-      }
-    if (!again) break;
+  uint32_t nan = 0;
+  for (int j = from; j < to && (open & ~nan); ++j) {
+    const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
+    if ((unsigned)page >= (unsigned)c.num_pages) continue;
+    const T* v = data + paged_row(c, page, 1, h, place) + d;
+    for (uint32_t left = open & ~nan; left; left &= left - 1) {
+      const int y = __ffs(left) - 1;
+      const float z = Elem<T>::to_f(v[y]);
+      if (fabsf(z) < __builtin_huge_valf()) continue;
+      o[y] += z;  // (inf - inf is NaN)
+      if (o[y] != o[y]) nan |= 1u << y;
+    }
   }
-  return make_float4(x[0], x[1], x[2], x[3]);
+  for (int y = 0; y < N; ++y)
+    if (o[y] != 0.f) open &= ~(1u << y);
+  if (!open) return;
+  for (int j = from; j < to; ++j) {
+    const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
+    if ((unsigned)page >= (unsigned)c.num_pages) continue;
+    const T* k = data + paged_row(c, page, 0, h, place);
+    const T* v = data + paged_row(c, page, 1, h, place) + d;
+    float s = 0.f;
+    for (int y = 0; y < D; ++y) s = fmaf(Elem<T>::to_f(q[y]), Elem<T>::to_f(k[y]), s);
+    const float p = tc::ex2(s * a.scale_log2 - M);
+    for (int y = 0; y < N; ++y)
+      if (open >> y & 1u) o[y] = fmaf(p, Elem<T>::to_f(v[y]), o[y]);
+  }
 }
 
 }  // namespace sdpa

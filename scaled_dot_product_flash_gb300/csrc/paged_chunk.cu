@@ -8,9 +8,8 @@
 // box of the map of out stores them; rows that the split leaves over are zeros.
 // Keys.  A tile of 128 keys is put together from the pages: boxes of as many tokens as page size
 // and tile have in common (16 to 128), one lane each, at the place that the page table names; boxes
-// past the last key, or on a bad page, are loaded from outside the tensor, which fills zeros.  In tiles
-// that some row sees only in part the values are looked through in shared memory before they meet P:
-// those behind the last token and those that are not finite are cleared (struct Odd).
+// past the last key, or on a bad page, are loaded from outside the tensor, which fills zeros.  Values
+// behind the sequence's last token are cleared in shared memory before they meet P.
 //
 // The pipeline is that of the dense forward kernel: a block of 12 warps computes two Q tiles;
 // warps 0-3 / 4-7 are the softmax of tile 0 / 1, one thread a row; warp 8 loads; warps 9 / 10
@@ -121,56 +120,14 @@ __device__ __forceinline__ float hide_bad_pages(uint32_t (&sv)[kBN], const Cache
   return scale2 == 0.f ? 1.f : scale2;
 }
 
-// Values that are not finite, in KV tiles that some row sees only in part: their place in shared memory is
-// cleared, so that they cannot reach rows under a weight of 0, and the first token of each kind in
-// each column is kept here, for the rows that do see it.
-template <int D>
-struct Odd {
-  int first[3][D];  // +inf, -inf, NaN
-  int any;
-  __device__ __forceinline__ void clear() {
-    for (int x = threadIdx.x; x < 3 * D; x += blockDim.x) first[0][x] = 0x7fffffff;
-    if (threadIdx.x == 0) any = 0;
-  }
-};
-
-// Row `row` (this thread's) of a V tile, from token `from` on: cleared if it lies behind the last token,
-// else freed of what is not finite.
-template <typename T, int D>
-__device__ __noinline__ void clean_values(uint8_t* tile, int row, int k0, int from, int len, Odd<D>& odd) {
-  if (k0 + row < from) return;
-  constexpr uint32_t kExp = kIsBf16<T> ? 0x7f80u : 0x7c00u, kMant = kIsBf16<T> ? 0x7fu : 0x3ffu;
-#pragma unroll 4
-  for (int x = 0; x < (D + 63) / 64 * 8; ++x) {
-    uint4* at = reinterpret_cast<uint4*>(tile + x / 8 * 16384 + sw128_off(row, x % 8));
-    if (k0 + row >= len) {
-      *at = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const uint4 w = *at;
-    uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) bad |= (ws[e] & kExp) == kExp || (ws[e] & kExp << 16) == kExp << 16;
-    if (!bad) continue;
+// Clears row `row` (this thread's) of a V tile if it lies behind the last token.
+template <int kCB>
+__device__ __forceinline__ void clear_behind(uint8_t* tile, int row, int k0, int len) {
+  if (k0 + row >= len) {
 #pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-      uint16_t* one = reinterpret_cast<uint16_t*>(at) + e;
-      if ((*one & kExp) != kExp) continue;
-      atomicMin(&odd.first[*one & kMant ? 2 : *one >> 15][x * 8 + e], k0 + row);
-      *one = 0;
-    }
-    odd.any = 1;
+    for (int x = 0; x < kCB * 8; ++x) *reinterpret_cast<uint4*>(tile + x / 8 * 16384 + row * 128 + x % 8 * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
-}
-
-// What column d of an output is to a row that sees tokens [0, to), if it meets such values.
-template <int D>
-__device__ __forceinline__ float with_odd(const Odd<D>& odd, int d, int to, float o) {
-  const bool up = odd.first[0][d] < to, down = odd.first[1][d] < to;
-  if (odd.first[2][d] < to || (up && down)) return __int_as_float(0x7fffffff);
-  return up ? -minus_inf() : down ? minus_inf() : o;
 }
 
 // Maximum of c·s over the keys e < lim of a row of scores; -inf without any.
@@ -243,7 +200,7 @@ __device__ __forceinline__ float exponentials(const uint32_t (&sv)[kBN], uint32_
 // into the workspace) and its logsumexp.  (The staging tile is the Q tile, which nobody reads any more.)
 template <typename T, int D>
 __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, const Tiling& t, const Rows& rows, const Span& span, int r, uint32_t o_addr,
-                                           uint8_t* stage, float m, float l, bool any, const Odd<D>& odd) {
+                                           uint8_t* stage, float m, float l, bool any) {
   const int i = span.i0 + r / t.heads, hq = w.h * a.G + w.group * t.heads + r % t.heads;
   const bool there = r < t.heads * t.tokens && i < span.i1;
   const int lim = there ? rows.limit(i) : 0;
@@ -252,7 +209,7 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, co
     m = minus_inf();
     l = 0.f;
   }
-  const bool nothing = l == 0.f, some_odd = *reinterpret_cast<const volatile int*>(&odd.any) != 0;
+  const bool nothing = l == 0.f;
   const int64_t row = ((int64_t)w.b * a.Hq + hq) * a.c.L + i;
   float inv = 1.f, m_all = m, l_all = l;
   if (!w.cut && there) {
@@ -269,12 +226,19 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const Work& w, co
       tmem_ld32(o_addr + c32 * 32, o);
       tmem_ld_wait(o);
     }
+    bool odd = false;
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
+    for (int e = 0; e < 32; ++e) {
       if (nothing) o[e] = 0u;
-    if (some_odd) {
+      odd |= (o[e] & 0x7fffffffu) > 0x7f800000u;
+    }
+    if (odd && l == l) {  // see mend_columns
+      float x[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(with_odd(odd, c32 * 32 + e, to, __uint_as_float(o[e])));
+      for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]);
+      mend_columns<T, D, 32>(a, w.b, w.h, hq, i, c32 * 32, w.k_lo, to, m, x);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(x[e]);
     }
     __syncwarp();
     if (w.cut) {
@@ -311,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bars;
-  __shared__ Odd<D> odd;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Work work = work_of(a, t, 2 * t.tokens);
@@ -352,7 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   for (int w = 0; w < 2; ++w) clear_unused<kCB>(sm + L::kQOff + w * L::kTileBytes, t);
-  odd.clear();
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -510,17 +472,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
       }
-      const bool split = j == 0 && split_tile(sp, k0);
-      const int clean = split ? 0 : sp.least;  // (a remainder of P times an infinite value would be NaN)
-      if (k0 + quarter * 32 + 32 > clean) {  // before P is announced
+      if (k0 + kBN > rows.len) {  // values behind the last token
         const int itv = 2 * j + 1;
         if (!(ok = __all_sync(kAll, mbar_wait(&bars.kv_full[itv % kStages], (itv / kStages) & 1, wc)))) break;
-        clean_values<T, D>(sm + L::kRingOff + itv % kStages * L::kTileBytes, r, k0, clean, rows.len, odd);
-        __syncwarp();
+        clear_behind<kCB>(sm + L::kRingOff + itv % kStages * L::kTileBytes, r, k0, rows.len);
       }
       if (j < nboth && (w == 1 || j > 0))
         if (!(ok = __all_sync(kAll, mbar_wait(&bars.turn[w], (w == 1 ? j : j - 1) & 1, wc)))) break;
       const float neg_m = m == minus_inf() ? 0.f : -m;  // (nothing seen so far: P = 0 under any finite shift)
+      const bool split = j == 0 && split_tile(sp, k0);
       if (split) l += exponentials<T, true, true>(sv, s_addr, cs, neg_m, lim, nullptr);
       else if (cut) l += exponentials<T, true, false>(sv, s_addr, cs, neg_m, lim, &bars.p_half[w]);
       else l += exponentials<T, false, false>(sv, s_addr, cs, neg_m, lim, &bars.p_half[w]);
@@ -543,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* stage = sm + L::kQOff + w * L::kTileBytes;
       if (ok) {
         tc_fence_after();
-        finish_row<T, D>(a, work, t, rows, sp, r, o_addr, stage, m, l, mine > 0, odd);
+        finish_row<T, D>(a, work, t, rows, sp, r, o_addr, stage, m, l, mine > 0);
         fence_async_smem();
       }
       if (named_sync_and(1 + w, kBM, ok) && r == 0 && !work.cut) {
@@ -605,7 +565,6 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
   extern __shared__ unsigned char smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ OneBars<kCB, kStages, kS> bars;
-  __shared__ Odd<D> odd;
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Work work = work_of(a, t, t.tokens);
@@ -654,7 +613,6 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
     tmem_relinquish();
   }
   clear_unused<kCB>(sm, t);
-  odd.clear();
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -799,15 +757,12 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
       const int k0 = work.k_lo + j * kBN, buf = j % kS;
       if (!(ok = __all_sync(kAll, mbar_wait(&bars.s_full[buf], (j / kS) & 1, wc)))) break;
       tc_fence_after();
-      const bool cut = k0 + kBN > span.least;
-      const int clean = j == 0 && split_tile(span, k0) ? 0 : span.least;  // (a remainder of P times an infinite value would be NaN)
-      if (k0 + warp * 32 + 32 > clean) {  // before P is announced
+      if (k0 + kBN > rows.len) {  // values behind the last token
         const int s = j % kStages;
         // (V(j-1) has landed once PV(j-1) is done: a barrier tells only its last two phases apart)
         if (j > 0 && !(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(j - 1) % kS], ((j - 1) / kS) & 1, wc)))) break;
         if (!(ok = __all_sync(kAll, mbar_wait(&bars.v_full[s][warp / 2], (j / kStages) & 1, wc)))) break;
-        clean_values<T, D>(sm + L::kVOff + s * L::kTileBytes, r, k0, clean, rows.len, odd);
-        __syncwarp();
+        clear_behind<kCB>(sm + L::kVOff + s * L::kTileBytes, r, k0, rows.len);
       }
       if (live) {
         const uint32_t s_addr = tmem_addr(tbase, warp * 32, 128 * buf);
@@ -815,6 +770,7 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
 #pragma unroll
         for (int q4 = 0; q4 < kBN / 32; ++q4) tmem_ld32(s_addr + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q4]));
         tmem_ld_wait(sv);
+        const bool cut = k0 + kBN > span.least;
         const int lim = min(limit - k0, kBN);
         float cs = a.scale_log2;
         if (bad_pages) cs = hide_bad_pages(sv, c, table, k0, end, cs);
@@ -853,7 +809,7 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
     if (ok) ok = __all_sync(kAll, mbar_wait(&bars.q_full, 0, wc));
     if (ok) {
       tc_fence_after();
-      finish_row<T, D>(a, work, t, rows, span, r, o_addr, sm, m, l, n > 0, odd);
+      finish_row<T, D>(a, work, t, rows, span, r, o_addr, sm, m, l, n > 0);
       fence_async_smem();
     }
     if (named_sync_and(1, kBM, ok) && r == 0 && !work.cut) {

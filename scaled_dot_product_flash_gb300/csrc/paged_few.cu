@@ -15,7 +15,7 @@
 // second MMA is hidden behind the copies.
 // The running maximum is raised only when a score passes it by 2^8: one vote a unit, no shuffles.
 // An output that is NaN without a reason in its row's scores has met a value that is not finite,
-// perhaps one that its row does not see: mend_output looks.
+// perhaps one that its row does not see: mend_columns looks.
 #include "paged.h"
 
 namespace sdpa {
@@ -352,8 +352,11 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
     }
     const int hq = h * a.G + r % a.G, i = r / a.G;
     const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
-    if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w))
-      v = mend_output<T, D>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M, v);
+    if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w)) {
+      float x[4] = {v.x, v.y, v.z, v.w};
+      mend_columns<T, D, 4>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M, x);
+      v = make_float4(x[0], x[1], x[2], x[3]);
+    }
     if (cut.splits > 1) {
       const int64_t at = part_of(cut, b, a.Hq, hq, i, blockIdx.x);
       *reinterpret_cast<float4*>(a.workspace + at * D + d) = v;

@@ -483,13 +483,14 @@ def test_two_graphs_on_their_own_workspaces():
         q = draw_rows(rng, (1, 8, L, 64), "bf16").cuda()
         at, _ = on_device(table, [n])
         stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(stream):
             api.paged_attention(q, cache, *at)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=stream):
             out, lse = api.paged_attention(q, cache, *at, need_lse=True)
-        runs.append((graph, stream, q, out, lse, ks, vs))
+        runs.append((graph, stream, q, out, lse, ks, vs, cache, at))             # the graph reads cache and at
     for _ in range(3):
         for graph, stream, q, *_ in runs:
             q.copy_(draw_rows(rng, tuple(q.shape), "bf16"))
@@ -499,5 +500,5 @@ def test_two_graphs_on_their_own_workspaces():
                 graph.replay()
         torch.cuda.synchronize()
         api.poll_status()
-        for _, _, q, out, lse, ks, vs in runs:
+        for _, _, q, out, lse, ks, vs, *_ in runs:
             check(out, lse, q, ks, vs, 1 / 8, True, "bf16")
