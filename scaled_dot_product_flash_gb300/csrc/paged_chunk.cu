@@ -41,7 +41,7 @@ struct Layout128 {
 
 struct Bars {
   uint64_t q_full, kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], mma_done[2], turn[2], scanned;
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], mma_done[2], turn[2], scanned, tail_clean;
   uint32_t tmem_base;
   int abort, bad_pages;
 };
@@ -120,13 +120,12 @@ __device__ __forceinline__ float hide_bad_pages(uint32_t (&sv)[kBN], const Cache
   return scale2 == 0.f ? 1.f : scale2;
 }
 
-// Clears row `row` (this thread's) of a V tile if it lies behind the last token.
+// Clears the rows of a V tile from `row` on: those behind the last token, which may hold anything.  By the
+// lanes that loaded the tile, once it has landed; the issuers wait for it.
 template <int kCB>
-__device__ __forceinline__ void clear_behind(uint8_t* tile, int row, int k0, int len) {
-  if (k0 + row >= len) {
-#pragma unroll 1
-    for (int x = 0; x < kCB * 8; ++x) *reinterpret_cast<uint4*>(tile + x / 8 * 16384 + row * 128 + x % 8 * 16) = make_uint4(0, 0, 0, 0);
-  }
+__device__ __forceinline__ void clear_behind(uint8_t* tile, int row, int lane, int lanes) {
+  const int n = (kBN - row) * 8;
+  for (int x = lane; x < n * kCB; x += lanes) *reinterpret_cast<uint4*>(tile + x / n * 16384 + row * 128 + x % n * 16) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
 }
 
@@ -288,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Span span[2] = {span_of(rows, t, work.i0, work), span_of(rows, t, work.i0 + t.tokens, work)};
   const int nkv[2] = {tiles_in(span[0], work.k_lo), tiles_in(span[1], work.k_lo)};
   const int nmax = max(nkv[0], nkv[1]), end = max(span[0].end, span[1].end);
+  const bool tail = nmax > 0 && work.k_lo + nmax * kBN > rows.len;  // the last KV tile holds places behind the last token
   if (nmax == 0 && work.cut) {
     asm volatile("griddepcontrol.launch_dependents;");
     return;
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.turn[w], 4);  // one arrival a warp of the other warpgroup
     }
     mbar_init(&bars.scanned, 1);
+    mbar_init(&bars.tail_clean, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -353,6 +354,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       at = next;
     }
+    if (ok && tail) {
+      const int it = 2 * nmax - 1;
+      if (__all_sync(kAll, mbar_wait(&bars.kv_full[it % kStages], (it / kStages) & 1, wc))) {
+        clear_behind<kCB>(sm + L::kRingOff + it % kStages * L::kTileBytes, rows.len - work.k_lo - (nmax - 1) * kBN, lane, 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.tail_clean);
+      }
+    }
     // No copy is in flight when the block exits, whatever its other warps met.
     for (int it = max(0, issued - kStages); it < issued; ++it) drain_wait(&bars.kv_full[it % kStages], (it / kStages) & 1);
     drain_wait(&bars.q_full, 0);
@@ -393,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool act = j < nkv_w, split = act && j == 0 && few;
       if (!(ok = __all_sync(kAll, mbar_wait(&bars.kv_full[sv], (itv / kStages) & 1, wc)))) break;
       if (act) {
+        if (tail && j == nmax - 1 && !(ok = __all_sync(kAll, mbar_wait(&bars.tail_clean, 0, wc)))) break;
         if (!(ok = __all_sync(kAll, mbar_wait(split ? &bars.p_full[w] : &bars.p_half[w], j & 1, wc)))) break;
         tc_fence_after();
         values(sv, 0, s_tm, j == 0);
@@ -472,11 +482,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
       }
-      if (k0 + kBN > rows.len) {  // values behind the last token
-        const int itv = 2 * j + 1;
-        if (!(ok = __all_sync(kAll, mbar_wait(&bars.kv_full[itv % kStages], (itv / kStages) & 1, wc)))) break;
-        clear_behind<kCB>(sm + L::kRingOff + itv % kStages * L::kTileBytes, r, k0, rows.len);
-      }
       if (j < nboth && (w == 1 || j > 0))
         if (!(ok = __all_sync(kAll, mbar_wait(&bars.turn[w], (w == 1 ? j : j - 1) & 1, wc)))) break;
       const float neg_m = m == minus_inf() ? 0.f : -m;  // (nothing seen so far: P = 0 under any finite shift)
@@ -548,7 +553,7 @@ struct OneLayout {
 template <int kCB, int kStages, int kS>
 struct OneBars {
   uint64_t q_full, k_full[kStages][kCB], k_empty[kStages][kCB], v_full[kStages][2], v_empty[kStages][2];
-  uint64_t s_full[kS], p_full[kS], pv_done[kS], fin, scanned;
+  uint64_t s_full[kS], p_full[kS], pv_done[kS], fin, scanned, tail_clean;
   uint32_t tmem_base;
   int abort, bad_pages;
 };
@@ -582,6 +587,7 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
   const Rows rows = rows_of(c, work.b, a.causal, a.max_len, kKidPagedAttn);
   const Span span = span_of(rows, t, work.i0, work);
   const int n = tiles_in(span, work.k_lo), end = span.end;
+  const bool tail = n > 0 && work.k_lo + n * kBN > rows.len;  // the last KV tile holds places behind the last token
   if (n == 0 && work.cut) {
     asm volatile("griddepcontrol.launch_dependents;");
     return;
@@ -606,6 +612,7 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
     }
     mbar_init(&bars.fin, kS);  // one commit an issuer
     mbar_init(&bars.scanned, 1);
+    mbar_init(&bars.tail_clean, 1);
     fence_mbar_init();
   }
   if (warp == 5) {
@@ -673,6 +680,14 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
           at[hr] = next;
         }
       }
+      if (ok && tail) {
+        const int s = (n - 1) % kStages, ph = ((n - 1) / kStages) & 1;
+        if (__all_sync(half, mbar_wait(&bars.v_full[s][0], ph, wc) && mbar_wait(&bars.v_full[s][1], ph, wc))) {
+          clear_behind<kCB>(sm + L::kVOff + s * L::kTileBytes, rows.len - work.k_lo - (n - 1) * kBN, lane - 16, 16);
+          __syncwarp(half);
+          if (first) mbar_arrive(&bars.tail_clean);
+        }
+      }
       for (int x = max(0, issued - kStages * 2); x < issued; ++x) drain_wait(&bars.v_full[x / 2 % kStages][x % 2], (x / 2 / kStages) & 1);
     }
     __syncwarp();
@@ -708,6 +723,7 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
       const uint64_t vd = sdesc_sw128(smem_u32(sm + L::kVOff + s * L::kTileBytes), 16384, 1024);
       const uint32_t p_tm = tbase + 128 * buf;
       const bool split = few(j);
+      if (tail && j == n - 1 && !(ok = __all_sync(kAll, mbar_wait(&bars.tail_clean, 0, wc)))) return;
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
         if (!(ok = __all_sync(kAll, mbar_wait(&bars.v_full[s][hr], (j / kStages) & 1, wc)))) return;
@@ -757,13 +773,6 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
       const int k0 = work.k_lo + j * kBN, buf = j % kS;
       if (!(ok = __all_sync(kAll, mbar_wait(&bars.s_full[buf], (j / kS) & 1, wc)))) break;
       tc_fence_after();
-      if (k0 + kBN > rows.len) {  // values behind the last token
-        const int s = j % kStages;
-        // (V(j-1) has landed once PV(j-1) is done: a barrier tells only its last two phases apart)
-        if (j > 0 && !(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(j - 1) % kS], ((j - 1) / kS) & 1, wc)))) break;
-        if (!(ok = __all_sync(kAll, mbar_wait(&bars.v_full[s][warp / 2], (j / kStages) & 1, wc)))) break;
-        clear_behind<kCB>(sm + L::kVOff + s * L::kTileBytes, r, k0, rows.len);
-      }
       if (live) {
         const uint32_t s_addr = tmem_addr(tbase, warp * 32, 128 * buf);
         uint32_t sv[kBN];
