@@ -49,9 +49,10 @@
  *    return SDPA_ERR_INVALID_ARG or SDPA_ERR_UNSUPPORTED; a failed launch returns
  *    SDPA_ERR_CUDA.  Kernels never trap: a wait that runs out of its iteration limit sets
  *    the device error word and the kernel returns; sdpa_poll_status reports it.
- *  - Beside the attention the library has the rotary embedding of q and k (sdpa_rotary) and a
- *    paged cache of keys and values in 4 bits (sdpa_cache_*), each with its own rules below;
- *    what those read from device memory (pages, lengths, axes) is checked by the kernels.
+ *  - Beside the attention the library has the rotary embedding of q and k (sdpa_rotary) and
+ *    paged caches of keys and values, in 4 bits (sdpa_cache_*) and in 16 (sdpa_paged_*, with
+ *    the weights that tokens gather and eviction by them), each with its own rules below; what
+ *    those read from device memory (pages, lengths, axes) is checked by the kernels.
  *  - Supported: dtype in {SDPA_F32, SDPA_F16, SDPA_BF16}; D in {32, 64, 96, 128, 256}
  *    (fp16/bf16 run on tensor cores at every D, fp32 on the CUDA-core tiled kernels);
  *    B, Hq, Hkv, Lq, Lkv >= 1; Hq % Hkv == 0; Hq, B <= 65535; scale finite (0 allowed).

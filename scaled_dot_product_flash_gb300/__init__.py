@@ -5,8 +5,9 @@ declared in ``include/sdpa.h``).  This package is its thin Python binding:
 
 * ``_lib``: ctypes entry points under the C names (``sdpa_fwd``, ``sdpa_bwd``, ...).
 * ``api``: tensor-level calls that allocate outputs with PyTorch and pass raw pointers:
-  attention forward and backward, rotary positions, and a 4-bit paged cache of keys and
-  values (write, read back, attention over it).
+  attention forward and backward, rotary positions, a 4-bit paged cache of keys and values
+  (write, read back, attention over it), and a 16-bit one (write, attention for tokens and for
+  chunks of prompts, attention weights of its tokens, eviction by them).
 * ``autograd``: ``SDPAFunction`` (torch autograd over the forward and fused backward), a
   ``scaled_dot_product_attention`` drop-in for the cases the kernels cover, and
   ``rotary_embedding``.

@@ -13,11 +13,19 @@
 //
 // The pipeline is that of the dense forward kernel: a block of 12 warps computes two Q tiles;
 // warps 0-3 / 4-7 are the softmax of tile 0 / 1, one thread a row; warp 8 loads; warps 9 / 10
-// issue the MMAs of tile 0 / 1; warp 11 looks whether all pages are good.  S_w = Q_w·K^T goes to TMEM columns [128w, 128w + 128), P_w over its first
-// 64 as the A operand of O_w += P_w·V at columns [256 + 128w, +D), PV in two halves of 64 keys.  The two
-// softmax warpgroups take turns at the exponentials.  The running maximum is raised when a row's
-// maximum grows by 2^8.  Rows that see few keys take P as head and remainder (16 more bits), see split_tile.
-// With few blocks the keys are cut into chunks whose unnormalised results the join kernel adds up.
+// issue the MMAs of tile 0 / 1; warp 11 looks whether all pages are good.  S_w = Q_w·K^T goes to TMEM
+// columns [128w, 128w + 128), P_w over its first 64 as the A operand of O_w += P_w·V at columns
+// [256 + 128w, +D), PV in two halves of 64 keys.  The two softmax warpgroups take turns at the
+// exponentials.  The running maximum is raised when a row's maximum grows by 2^8.  Rows that see few keys
+// take P as head and remainder (16 more bits), see split_tile.  What does not fill a wave of blocks is cut
+// along the keys, and the join kernel adds the unnormalised results up.
+//
+// Bound: the tensor pipe, 1024 cycles a pair of tiles of 128 x 128 at D = 128; exponentials take half of that.
+// Measured (bf16, 32 query and 8 KV heads, D = 128, from a graph): 2 prompts of 4096 tokens 233 us, 1180
+// TFLOP/s, 0.61 of the measured rate (the dense kernel on the same shape 228); 2048 queries over 32768
+// tokens 784 us, 1365 TFLOP/s, 0.71.  A block's iteration takes some 3000 cycles for 2048 of the tensor
+// pipe, its start and end some 5 us.  The softmax loop is sensitive: clearing V's last rows in it, once
+// a block, cost 3%, looking values of cut tiles through 5 to 9%.
 #include "paged_tc.cuh"
 
 namespace sdpa {

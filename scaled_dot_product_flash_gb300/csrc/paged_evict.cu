@@ -1,7 +1,9 @@
 // Writing a 16-bit paged cache, and evicting the tokens that have gathered the least attention
 // weight (conventions in include/sdpa.h).
 //
-// Write: every thread moves four 16-byte pieces.  Bound: HBM for prompts, latency for tokens.
+// Write: every thread moves four 16-byte pieces.  Bound: HBM for prompts, latency for tokens: two prompts of
+// 4096 tokens, 8 heads, D = 128 8.3 us from a graph (67 MB in and out, half of it to L2), one token of 32
+// sequences 2.3.
 //
 // Evict, two kernels:
 //  - select: a cluster of blocks takes one row of weights (one sequence and KV head).  Weights are
@@ -12,6 +14,9 @@
 //    when all of its loads have landed never overwrites a row that is still to be read.  Rows are cut
 //    into slices of 32 bytes or more, one block each: slices do not touch one another, and there are
 //    enough of them to fill the device.
+//    Bound: HBM, twice the rows that move.  32 sequences of 2304 tokens to 2048, 8 heads, D = 128: 99 us
+//    with the selection (8 of them), 5.5 TB/s; looking places up a round ahead but waiting for it, 128.
+//    One of 32768 to 8192: 28.7 us, 12 of them the selection, whose cluster barriers cost 0.7 us each.
 #include <cooperative_groups.h>
 
 #include "paged.h"

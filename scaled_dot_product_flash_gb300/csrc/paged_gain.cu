@@ -12,6 +12,11 @@
 // Rows without weight (padding, an lse of −inf, rows that a tile does not fill) have a logsumexp
 // of +inf here; since their products may be NaN, the 32-row pieces that hold some are marked, and
 // there those terms are left out one by one.
+//
+// Bound: tensor pipe and exponential unit alike, 512 cycles a pair of 128 x 128 tiles at D = 128.  Measured
+// (bf16, 32 query and 8 KV heads, D = 128, from a graph): prompts of 4096 tokens 140 us, both units 44%
+// busy; with four warps a key tile 151, and 169 with divisions in the warp that fetches logsumexps, whose
+// steps the others wait for.
 #include <cooperative_groups.h>
 
 #include "paged_tc.cuh"
@@ -20,7 +25,6 @@ namespace sdpa {
 namespace {
 using namespace tc;
 namespace cg = cooperative_groups;
-
 
 template <int D>
 struct GainLayout {
