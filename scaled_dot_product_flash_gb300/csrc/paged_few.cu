@@ -167,10 +167,12 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
     asm volatile("griddepcontrol.launch_dependents;");
     return;
   }
-  if (rt == 0 && lane < C::kStages) tc::mbar_init(&full[slot][lane], 1);
-  if (threadIdx.x == 0) abort_flag = 0;
-  if (lane == 0) {
+  if (rt == 0 && lane < C::kStages) {
+    tc::mbar_init(&full[slot][lane], 1);
     tc::fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
     tc::prefetch_tmap(&map);
   }
   __syncthreads();
@@ -478,9 +480,11 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kWarps * 32) paged_weights_kernel
   if (rows.first >= c.L) return;  // no real row
   const int R = a.G * c.L, start = blockIdx.x * chunk;
   if (start >= rows.len) return;
-  if (lane < C::kStages) tc::mbar_init(&full[warp][lane], 1);
+  if (lane < C::kStages) {
+    tc::mbar_init(&full[warp][lane], 1);
+    tc::fence_mbar_init();
+  }
   if (threadIdx.x == 0) abort_flag = 0;
-  if (lane == 0) tc::fence_mbar_init();
   __syncthreads();
   const tc::WaitCtx wc{&abort_flag, 0, a.wait_limit_ns, c.err, kKidPagedWeights};
   const int fresh = rows.len - (c.L - rows.first);  // tokens from here on are the call's own

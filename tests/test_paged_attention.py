@@ -253,6 +253,16 @@ CASES = [
     ("f16", 2, 2, 257, 64, 80, [257, 400], None),
     ("bf16", 2, 1, 200, 256, 48, [200, 333], [200, 77]),
     ("bf16", 48, 1, 9, 64, 16, [9, 140], None),                    # 48 query heads a KV head
+    ("f16", 160, 1, 3, 64, 16, [50, 3], None),                     # more query heads than a tile has rows
+    ("bf16", 131, 1, 2, 32, 32, [70], None),                       # a prime number of them
+    ("bf16", 64, 1, 1, 128, 16, [200, 1], None),
+    ("f16", 17, 1, 1, 96, 16, [140, 0], None),
+    ("bf16", 4, 1, 10, 32, 16, [150, 10], None),                   # one tile of rows at every head dim
+    ("f16", 3, 1, 20, 96, 48, [170, 30], [20, 7]),
+    ("bf16", 8, 2, 25, 128, 64, [25, 190], None),
+    ("f16", 2, 1, 33, 256, 16, [133, 35], [33, 1]),
+    ("f16", 4, 2, 50, 32, 65536, [300, 50], None),                 # the largest pages
+    ("bf16", 2, 2, 1, 64, 65536, [77], None),
 ]
 
 

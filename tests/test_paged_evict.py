@@ -217,6 +217,26 @@ def test_evict(dtype, H, D, page, lens, budget, recent, in_place):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,budget,recent", [([700, 300], 200, 40), ([9000, 100], 3000, 2900)])
+def test_evict_rows_of_a_larger_tensor(lens, budget, recent):
+    """Weights with the heads outermost and rows off the 16-byte grid, in place and to another layout."""
+    rng = np.random.default_rng(23)
+    wide = torch.from_numpy(rng.random((3, 2, max(lens) + 20)).astype(np.float32)).cuda()
+    for in_place in (False, True):
+        cache, table, _, _ = fill(rng, lens, 3, 32, 16, "bf16")
+        weights, before = wide[..., 3:-1].transpose(0, 1), wide.clone()
+        want = evicted(cache, table, lens, weights, budget, recent)
+        at, _ = on_device(table, lens)
+        new = weights
+        if not in_place:
+            new = torch.full((2, 4, weights.shape[2] + 5), NAN, device="cuda")[:, 1:, 5:]
+        got = api.paged_evict(cache, *at, weights, budget, recent, new_weights=new)
+        api.poll_status()
+        same((cache, *got), want)
+        assert torch.equal(wide[..., :3], before[..., :3]) and torch.equal(wide[..., -1:], before[..., -1:])
+
+
+@pytest.mark.gpu
 def test_evict_numbers_of_every_kind():
     """NaN below all, zeros of both signs alike, infinities, subnormals, the largest and smallest."""
     rng = np.random.default_rng(21)
