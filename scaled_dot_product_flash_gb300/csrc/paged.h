@@ -131,6 +131,29 @@ __device__ __forceinline__ int64_t paged_row(const CacheArgs& c, int page, int w
   return ((((int64_t)page * 2 + which) * c.Hkv + h) * c.page_size + place) * c.D;
 }
 
+// P = 2^(c·s − base) meets V in T.  A row's base follows its scores lazily, since O has to be rescaled with
+// it: it rises where a tile's maximum passes the one it was set by by 2^8.  bf16 has fp32's exponents and takes
+// that maximum itself as the base.  fp16 ends below 2^16 and loses bits under 2^-14, so there the base lies 7
+// below it, and it sinks again where a tile's weights all lie under 2^-7, as they do behind a token that
+// outweighs the others.  A weight is off by 2^-25·2^base then, apart from its rounding to the type's bits: by at
+// most 2^-32 of the row's largest and 2^-18 of its tile's largest.  (Sums of 16 more bits per weight, for few rows, do not
+// help against the end of the exponents.)
+template <typename T>
+constexpr bool kNarrow = std::is_same<T, __half>::value;
+constexpr float kRescale = 8.f, kSink = 7.f, kBias = 7.f;
+constexpr float kExact = 4194304.f;  // 2^22: below it a base can lie 7 below a maximum with P still under 2^16
+
+template <typename T>
+__device__ __forceinline__ float bias_of(float x) { return kNarrow<T> && fabsf(x) < kExact ? kBias : 0.f; }
+// The base for a largest score of top.
+template <typename T>
+__device__ __forceinline__ float base_of(float top) { return top - bias_of<T>(top); }
+// The score past which it rises.
+template <typename T>
+__device__ __forceinline__ float base_high(float base) { return base + (kRescale + bias_of<T>(base)); }
+// (What lies 2^60 below the row's sum l adds nothing; O stays far from fp32's end.)
+__device__ __forceinline__ bool base_sinks(float base, float top, float l) { return top < base - kSink && l * tc::ex2(base - top) < 0x1p60f; }
+
 // For columns [d, d + N) of an output o of query (hq, i) of KV head h over the tokens [from, to) of
 // sequence b, some of which came out NaN without a reason in the row's scores, since a product meets
 // every value of a tile, under a weight of 0 too.  Those with a value among the tokens that is not finite are

@@ -16,7 +16,7 @@
 // issue the MMAs of tile 0 / 1; warp 11 looks whether all pages are good.  S_w = Q_w·K^T goes to TMEM
 // columns [128w, 128w + 128), P_w over its first 64 as the A operand of O_w += P_w·V at columns
 // [256 + 128w, +D), PV in two halves of 64 keys.  The two softmax warpgroups take turns at the
-// exponentials.  The running maximum is raised when a row's maximum grows by 2^8.  Rows that see few keys
+// exponentials.  The base of a row's exponents follows its scores lazily (paged.h).  Rows that see few keys
 // take P as head and remainder (16 more bits), see split_tile.  What does not fill a wave of blocks is cut
 // along the keys, and the join kernel adds the unnormalised results up.
 //
@@ -37,7 +37,6 @@ constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kScanWarp = 11;
 // The block is launched with 168 registers a thread: 128·56 + 256·224 = 384·168.
 constexpr int kRegsLow = 56, kRegsHigh = 224;
-constexpr float kRescale = 8.f;
 
 template <int D>
 struct Layout128 {
@@ -135,6 +134,27 @@ __device__ __forceinline__ void clear_behind(uint8_t* tile, int row, int lane, i
   const int n = (kBN - row) * 8;
   for (int x = lane; x < n * kCB; x += lanes) *reinterpret_cast<uint4*>(tile + x / n * 16384 + row * 128 + x % n * 16) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
+}
+
+// Whether a row's base (paged.h) may have to move for a tile's largest score; `high`: where it rises.
+template <typename T>
+__device__ __forceinline__ bool base_off(float m, float high, float top) { return top > high || (kNarrow<T> && top < m - kSink); }
+// Moves it to where that score wants it, the row's sum along; returns O's factor.  Only a warp that has such a
+// row asks (2048 queries over 32768 tokens: 764 us, all asking 778), in fp16 by a call (796 us, inlined 819).
+template <typename T>
+__device__ __forceinline__ float3 moved_base(float m, float l, float top) {
+  if (!(top > base_high<T>(m)) && !(kNarrow<T> && base_sinks(m, top, l))) return make_float3(m, l, 1.f);
+  const float to = base_of<T>(top), alpha = ex2(m - to);  // 0 when m was -inf
+  return make_float3(to, l * alpha, alpha);
+}
+__device__ __noinline__ float3 moved_base_half(float m, float l, float top) { return moved_base<__half>(m, l, top); }
+template <typename T>
+__device__ __forceinline__ float move_base(float& m, float& l, float& high, float top) {
+  const float3 x = kNarrow<T> ? moved_base_half(m, l, top) : moved_base<T>(m, l, top);
+  m = x.x;
+  l = x.y;
+  high = base_high<T>(m);
+  return x.z;
 }
 
 // Maximum of c·s over the keys e < lim of a row of scores; -inf without any.
@@ -453,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem_addr(tbase, quarter * 32, w * 128), o_addr = tmem_addr(tbase, quarter * 32, 256 + w * 128);
     const int i = sp.i0 + r / t.heads;
     const int limit = r < t.heads * t.tokens && i < sp.i1 ? rows.limit(i) : 0;
-    float m = minus_inf(), l = 0.f;
+    float m = minus_inf(), l = 0.f, high = minus_inf();
     bool ok = __all_sync(kAll, mbar_wait(&bars.scanned, 0, wc));
     const bool bad_pages = bars.bad_pages;
     for (int j = 0; ok && j < mine; ++j) {
@@ -469,26 +489,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       float cs = a.scale_log2;
       if (bad_pages) cs = hide_bad_pages(sv, c, table, k0, end, cs);
       const float top = cut ? row_max<true>(sv, cs, lim) : row_max<false>(sv, cs, lim);
-      const float m_new = fmaxf(m, top);
-      const bool up = m_new > m + kRescale;
-      const float alpha = up ? ex2(m - m_new) : 1.f;  // 0 when m was -inf
-      if (up) {
-        l *= alpha;
-        m = m_new;
-      }
-      if (j > 0 && __any_sync(kAll, up)) {  // rescale O once PV(j-1) has landed
-        if (!(ok = __all_sync(kAll, mbar_wait(&bars.o_done[w], (j - 1) & 1, wc)))) break;
-        tc_fence_after();
+      if (__any_sync(kAll, base_off<T>(m, high, top))) {
+        const float alpha = move_base<T>(m, l, high, top);
+        if (j > 0 && __any_sync(kAll, alpha != 1.f)) {  // rescale O once PV(j-1) has landed
+          if (!(ok = __all_sync(kAll, mbar_wait(&bars.o_done[w], (j - 1) & 1, wc)))) break;
+          tc_fence_after();
 #pragma unroll 1
-        for (int c32 = 0; c32 < D / 32; ++c32) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c32 * 32, o);
-          tmem_ld_wait(o);
+          for (int c32 = 0; c32 < D / 32; ++c32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c32 * 32, o);
+            tmem_ld_wait(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(o_addr + c32 * 32, o);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(o_addr + c32 * 32, o);
+          }
+          tmem_st_wait();
         }
-        tmem_st_wait();
       }
       if (j < nboth && (w == 1 || j > 0))
         if (!(ok = __all_sync(kAll, mbar_wait(&bars.turn[w], (w == 1 ? j : j - 1) & 1, wc)))) break;
@@ -774,7 +790,7 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
     const int i = span.i0 + r / t.heads;
     const int limit = r < t.heads * t.tokens && i < span.i1 ? rows.limit(i) : 0;
     const bool live = __any_sync(kAll, limit > 0);  // a warp without a row only keeps the barriers going
-    float m = minus_inf(), l = 0.f;
+    float m = minus_inf(), l = 0.f, high = minus_inf();
     bool ok = __all_sync(kAll, mbar_wait(&bars.scanned, 0, wc));
     const bool bad_pages = bars.bad_pages;
     for (int j = 0; ok && j < n; ++j) {
@@ -792,26 +808,22 @@ __global__ void __launch_bounds__(OneLayout<D>::kThreads, OneLayout<D>::kBlocks)
         float cs = a.scale_log2;
         if (bad_pages) cs = hide_bad_pages(sv, c, table, k0, end, cs);
         const float top = cut ? row_max<true>(sv, cs, lim) : row_max<false>(sv, cs, lim);
-        const float m_new = fmaxf(m, top);
-        const bool up = m_new > m + kRescale;
-        const float alpha = up ? ex2(m - m_new) : 1.f;
-        if (up) {
-          l *= alpha;
-          m = m_new;
-        }
-        if (j > 0 && __any_sync(kAll, up)) {  // rescale O once PV(j-1) has landed
-          if (!(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(j - 1) % kS], ((j - 1) / kS) & 1, wc)))) break;
-          tc_fence_after();
+        if (__any_sync(kAll, base_off<T>(m, high, top))) {
+          const float alpha = move_base<T>(m, l, high, top);
+          if (j > 0 && __any_sync(kAll, alpha != 1.f)) {  // rescale O once PV(j-1) has landed
+            if (!(ok = __all_sync(kAll, mbar_wait(&bars.pv_done[(j - 1) % kS], ((j - 1) / kS) & 1, wc)))) break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int c32 = 0; c32 < D / 32; ++c32) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + c32 * 32, o);
-            tmem_ld_wait(o);
+            for (int c32 = 0; c32 < D / 32; ++c32) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + c32 * 32, o);
+              tmem_ld_wait(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(o_addr + c32 * 32, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(o_addr + c32 * 32, o);
+            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
         }
         const float neg_m = m == minus_inf() ? 0.f : -m;
         if (few(j)) l += exponentials<T, true, true>(sv, s_addr, cs, neg_m, lim, nullptr);

@@ -11,9 +11,9 @@
 // values come by bulk tensor loads into a ring, a few units ahead, without a block
 // barrier (16 tokens never cross a page, whose size is a multiple of 16); the products are warp-level
 // MMAs, m16n8k16, S = Q·K^T and O += P·V, whose accumulator of the first is the operand of the second.
-// P enters O as two 16-bit numbers, head and remainder, so that O is as exact as with fp32 weights: the
-// second MMA is hidden behind the copies.
-// The running maximum is raised only when a score passes it by 2^8: one vote a unit, no shuffles.
+// P enters O as two 16-bit numbers, head and remainder, so that O is as exact as with fp32 weights (in fp16
+// down to what paged.h says of small ones): the second MMA is hidden behind the copies.
+// The base of a row's exponents moves only when its scores have left it far behind: one vote a unit, no shuffles.
 // An output that is NaN without a reason in its row's scores has met a value that is not finite,
 // perhaps one that its row does not see: mend_columns looks.
 //
@@ -32,8 +32,6 @@ namespace sdpa {
 namespace {
 
 using tc::ex2;
-
-constexpr float kRescale = 8.f;
 
 // RT: row tiles of 16 rows, a warp each for every ring; kSlots: rings of a block.
 template <int D, int RT, int kSlots>
@@ -213,7 +211,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
     if constexpr (C::kQSmem) __syncthreads();
   }
 
-  float o[D / 8][4], m[2] = {minus_inf(), minus_inf()}, l[2] = {0.f, 0.f};
+  float o[D / 8][4], m[2] = {minus_inf(), minus_inf()}, l[2] = {0.f, 0.f};  // m: the rows' bases (paged.h)
 #pragma unroll
   for (int d = 0; d < D / 8; ++d)
 #pragma unroll
@@ -268,12 +266,20 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
         }
 #pragma unroll
       for (int x = 0; x < 2; ++x) top[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-      if (__any_sync(0xffffffffu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale)) {
+      const bool rise = top[0] > base_high<T>(m[0]) || top[1] > base_high<T>(m[1]);
+      const bool sink = kNarrow<T> && (top[0] < m[0] - kSink || top[1] < m[1] - kSink);  // (by the lane's scores)
+      if (__any_sync(0xffffffffu, rise || sink)) {
+        const bool sinks = kNarrow<T> && __any_sync(0xffffffffu, sink);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float v = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          const float up = fmaxf(m[x], v);
+          float up = fmaxf(m[x], base_of<T>(v));
+          if (sinks) {
+            float sum = l[x] + __shfl_xor_sync(0xffffffffu, l[x], 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (base_sinks(m[x], v, sum)) up = base_of<T>(v);
+          }
           const float f = up == minus_inf() ? 1.f : ex2(m[x] - up);
           m[x] = up;
           l[x] *= f;

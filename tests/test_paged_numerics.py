@@ -1,0 +1,104 @@
+"""What attention over a 16-bit paged cache makes of weights, scores and values at the ends of their
+ranges, against the fp64 oracle."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from cache_util import TYPES, draw_rows, ints, make_table
+from oracle import paged as ref
+from paged_util import NAN, fill, on_device
+from scaled_dot_product_flash_gb300 import _lib, api
+from scaled_dot_product_flash_gb300.inputs import as_f64
+
+
+def put(ks, vs, page, dtype, rng):
+    """(cache, table) holding these keys and values [Hkv, n, D], NaN elsewhere."""
+    lens = [k.shape[1] for k in ks]
+    table, pages = make_table(rng, lens, page)
+    H, _, D = ks[0].shape
+    cache = torch.full((pages, 2, H, page, D), NAN, dtype=TYPES[dtype])
+    for b, n in enumerate(lens):
+        for j in range(0, n, page):
+            m = min(page, n - j)
+            cache[table[b, j // page], 0, :, :m] = ks[b][:, j:j + m]
+            cache[table[b, j // page], 1, :, :m] = vs[b][:, j:j + m]
+    return cache.cuda(), table
+
+
+# ---- weights far below a row's largest
+
+FORMS = [(64, 1, 1), (128, 4, 8), (64, 1, 60), (128, 2, 200), (256, 1, 1), (256, 1, 20), (256, 1, 50)]  # D, G, L: every kernel
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", [6, 12, 17.5, 20, 30, 60])
+@pytest.mark.parametrize("n,heavy", [(90, [0]), (4096, [0]), (2500, [3, 700, 1500, 2300])])
+@pytest.mark.parametrize("D,G,L", FORMS)
+def test_small_weights_are_kept(D, G, L, n, heavy, gap, dtype):
+    """A few tokens that score `gap` above all others and have a value of 0, as attention sinks do: what
+    comes out is what the others contribute.  Tolerances as in paged_util.check, and for what P in T keeps of
+    a weight (paged.h):
+      2^-25·max|v|   fp16: tokens in a heavy one's tile of at most 128 are off by 2^-32 of it each, and
+                     the heavy ones' weights together are 1 at most
+      2^-16·A        fp16: all others by 2^-18 of their tile's largest, which is at most e^1 = 2^1.45
+                     times a weight here"""
+    if n < L:
+        pytest.skip("rows past the first token")
+    rng = np.random.default_rng(int(10 * gap) + n + D)
+    k = torch.zeros(1, n, D, dtype=TYPES[dtype])
+    k[0, :, 0] = torch.from_numpy(rng.uniform(-0.4, 0.4, n)).to(k.dtype)
+    k[0, :, 1:] = draw_rows(rng, (n, D - 1), dtype)
+    v = draw_rows(rng, (1, n, D), dtype, 0.25) + 1
+    k[0, heavy, 0] = gap
+    v[0, heavy] = 0
+    cache, table = put([k], [v], 32, dtype, rng)
+    q = torch.zeros(1, G, L, D, dtype=TYPES[dtype])
+    q[..., 0] = 1                                                                # a score is a key's first element
+    at, _ = on_device(table, [n])
+    out, lse = api.paged_attention(q.cuda(), cache, *at, scale=1.0, need_lse=True)
+    api.poll_status()
+    o, want, A, S = ref.attention(as_f64(q), [as_f64(k)], [as_f64(v)], 1.0, True)
+    half, u = torch.finfo(TYPES[dtype]).eps / 2, 2.0**-24
+    ds = (D + 8) * u * S[..., None] + 2.0**-21
+    p = (2 * half**2 if G * L <= 32 else half) + (2.0**-16 if dtype == "f16" else 0)
+    floor = 2.0**-25 * (1 + as_f64(v).max()) if dtype == "f16" else 1e-38
+    tol = half * np.abs(o) + (p + 2 * ds + 2 * n * u) * A + floor
+    worst = (np.abs(as_f64(out) - o) / tol).max()
+    assert worst <= 1, f"out is {worst:.2f} of its tolerance"
+    off = np.abs(as_f64(lse) - want) / (ds[..., 0] + n * u + 2.0**-21 + 2.0**-22 * np.abs(want))
+    assert off.max() <= 1, f"lse is {off.max():.2f} of its tolerance"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("slope", [0.02, -0.02])
+@pytest.mark.parametrize("D,G,L", FORMS)
+def test_scores_that_rise_and_fall(D, G, L, slope, dtype):
+    """4000 scores on a line from 0 to 80, up or down: bases move every few tiles.  Tolerances as in
+    test_small_weights_are_kept; in fp16 2^-25·max|v| is for the tokens before a base moves on, 500 of them
+    at most (10 on a scale where the row's largest weight is 1), off by 2^-32 of the row's largest, which is a
+    fiftieth of its sum (1 / (1 - e^-0.02))."""
+    rng = np.random.default_rng(5)
+    n = 4000
+    k = torch.zeros(1, n, D, dtype=TYPES[dtype])
+    line = slope * np.arange(n)
+    k[0, :, 0] = torch.from_numpy(np.round(line)).to(k.dtype)                    # whole numbers to 80 are exact
+    k[0, :, 1] = torch.from_numpy(line - np.round(line)).to(k.dtype)
+    v = draw_rows(rng, (1, n, D), dtype)
+    cache, table = put([k], [v], 64, dtype, rng)
+    q = torch.zeros(1, G, L, D, dtype=TYPES[dtype])
+    q[..., :2] = 1
+    at, _ = on_device(table, [n])
+    out, lse = api.paged_attention(q.cuda(), cache, *at, scale=1.0, need_lse=True)
+    api.poll_status()
+    o, want, A, S = ref.attention(as_f64(q), [as_f64(k)], [as_f64(v)], 1.0, True)
+    half, u = torch.finfo(TYPES[dtype]).eps / 2, 2.0**-24
+    ds = (D + 8) * u * S[..., None] + 2.0**-21
+    p = 2 * half**2 if G * L <= 32 else half
+    tol = half * np.abs(o) + (p + 2 * ds + 2 * n * u) * A + 2.0**-25 * (1 + np.abs(as_f64(v)).max())
+    worst = (np.abs(as_f64(out) - o) / tol).max()
+    assert worst <= 1, f"out is {worst:.2f} of its tolerance"
+    assert (np.abs(as_f64(lse) - want) / (ds[..., 0] + n * u + 2.0**-21 + 2.0**-22 * np.abs(want))).max() <= 1
