@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
     const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
     if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w)) {
       float x[4] = {v.x, v.y, v.z, v.w};
-      mend_columns<T, D, 4>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M, x);
+      if (sum > 0.f) mend_columns<T, D, 4>(a, b, h, hq, i, d, start, min(end, rows.limit(i)), M, x);
+      else x[0] = x[1] = x[2] = x[3] = 0.f;  // nothing seen but scores of -inf
       v = make_float4(x[0], x[1], x[2], x[3]);
     }
     if (cut.splits > 1) {

@@ -102,3 +102,64 @@ def test_scores_that_rise_and_fall(D, G, L, slope, dtype):
     worst = (np.abs(as_f64(out) - o) / tol).max()
     assert worst <= 1, f"out is {worst:.2f} of its tolerance"
     assert (np.abs(as_f64(lse) - want) / (ds[..., 0] + n * u + 2.0**-21 + 2.0**-22 * np.abs(want))).max() <= 1
+
+
+# ---- values that are not finite
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("what", [NAN, float("inf")])
+@pytest.mark.parametrize("D,G,L", [f for f in FORMS if f[2] > 1] + [(64, 1, 2), (128, 1, 5), (256, 2, 4)])
+def test_a_hidden_value_where_every_score_is_minus_infinity(D, G, L, what, dtype):
+    """Rows that see nothing but scores of -inf rest at 0 and -inf, whatever a token that they do not see holds."""
+    rng = np.random.default_rng(9)
+    n = L + 5
+    k = torch.zeros(1, n, D, dtype=TYPES[dtype])
+    k[0, :-1, 0] = -math.inf
+    v = draw_rows(rng, (1, n, D), dtype)
+    v[0, -1] = what
+    cache, table = put([k], [v], 32, dtype, rng)
+    q = torch.zeros(1, G, L, D, dtype=TYPES[dtype])
+    q[..., 0] = 1
+    at, _ = on_device(table, [n])
+    out, lse = api.paged_attention(q.cuda(), cache, *at, scale=1.0, need_lse=True)
+    api.poll_status()
+    assert not out[:, :, :-1].any() and torch.isneginf(lse[:, :, :-1]).all()
+    assert not out[:, :, -1].isfinite().any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,G,L", FORMS)
+def test_some_values_that_are_not_finite(D, G, L, dtype):
+    """NaN and infinities strewn over the values, many in columns of their own, some with others: what a row
+    sees decides, column by column, over several chunks and pages.  Tolerance of the rest: paged_util.check's
+    terms, P to 2^-20 where a column was mended."""
+    rng = np.random.default_rng(10)
+    n = 3000
+    k = draw_rows(rng, (1, n, D), dtype, 0.5)
+    v = draw_rows(rng, (1, n, D), dtype)
+    bad = torch.zeros(n, D)
+    for j in [0, 17, 300, 1500, *range(n - 40, n, 3)]:
+        for x in rng.choice(D, 3, replace=False):
+            bad[j, x] = [NAN, math.inf, -math.inf][rng.integers(3)]
+    v[0] = torch.where(bad != 0, bad.to(v.dtype), v[0])
+    cache, table = put([k], [v], 48, dtype, rng)
+    q = draw_rows(rng, (1, G, L, D), dtype, 0.5)
+    at, _ = on_device(table, [n])
+    out, lse = api.paged_attention(q.cuda(), cache, *at, need_lse=True)
+    api.poll_status()
+    clean = torch.where(bad != 0, 0, v[0].double())[None].numpy()
+    o, want, A, S = ref.attention(as_f64(q), [as_f64(k)], [clean], D**-0.5, True)
+    marks = bad.double().numpy()
+    for i in range(L):
+        seen = marks[:n - L + i + 1]
+        nan, up, down = np.isnan(seen).any(0), (seen == np.inf).any(0), (seen == -np.inf).any(0)
+        o[:, :, i] = np.where(nan | (up & down), np.nan, np.where(up, np.inf, np.where(down, -np.inf, o[:, :, i])))
+    got = as_f64(out)
+    assert np.array_equal(np.isnan(got), np.isnan(o)) and np.array_equal(got[np.isinf(o)], o[np.isinf(o)])
+    half, u = torch.finfo(TYPES[dtype]).eps / 2, 2.0**-24
+    tol = half * np.abs(o) + (max(2.0**-20, 2 * half**2 if G * L <= 32 else half) + 2 * (D + 8) * u * S[..., None] + 2.0**-20 + 2 * n * u) * A + 2.0**-25
+    fine = np.isfinite(o)
+    assert (np.abs(got - o)[fine] <= tol[fine]).all() and torch.isfinite(lse).all()
