@@ -163,3 +163,33 @@ def test_some_values_that_are_not_finite(D, G, L, dtype):
     tol = half * np.abs(o) + (max(2.0**-20, 2 * half**2 if G * L <= 32 else half) + 2 * (D + 8) * u * S[..., None] + 2.0**-20 + 2 * n * u) * A + 2.0**-25
     fine = np.isfinite(o)
     assert (np.abs(got - o)[fine] <= tol[fine]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", [NAN, math.inf])
+@pytest.mark.parametrize("G,L,D", [(4, 60, 64), (4, 300, 128), (2, 40, 256), (4, 8, 64), (4, 2, 128)])
+def test_a_hidden_value_costs_little(G, L, D, what):
+    """One token of 16000 with values that are not finite, which all rows but the last do not see: no more
+    than 600 times a call's time."""
+    rng = np.random.default_rng(35)
+    n = 16000
+    cache, table, _, _ = fill(rng, [n], 2, D, 64, "bf16")
+    q = draw_rows(rng, (1, 2 * G, L, D), "bf16").cuda()
+    at, _ = on_device(table, [n])
+
+    def timed():
+        api.paged_attention(q, cache, *at)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        out, _ = api.paged_attention(q, cache, *at)
+        b.record()
+        b.synchronize()
+        return out, a.elapsed_time(b)
+
+    good, plain = timed()
+    cache[table[0, (n - 1) // 64], 1, :, (n - 1) % 64] = what
+    out, slow = timed()
+    api.poll_status()
+    assert not out[:, :, -1].isfinite().any()
+    assert (out[:, :, :-1].float() - good[:, :, :-1].float()).abs().max() <= 2.0**-8 * good.float().abs().max() + 2.0**-8
+    assert slow < 600 * max(plain, 0.05)
