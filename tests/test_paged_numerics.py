@@ -104,6 +104,37 @@ def test_scores_that_rise_and_fall(D, G, L, slope, dtype):
     assert (np.abs(as_f64(lse) - want) / (ds[..., 0] + n * u + 2.0**-21 + 2.0**-22 * np.abs(want))).max() <= 1
 
 
+# ---- scores up to 2^26
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("steps", [[0], [-32, 0], [0, -64, 0]])
+@pytest.mark.parametrize("D,G,L", FORMS)
+def test_large_scores(D, G, L, steps, dtype):
+    """Scores of 5.7e7, where fp32 counts in steps of 4 and of 8 once log2(e) is in: equal ones have equal
+    weights, whole steps less none.  Tolerance: the output's rounding, P's, the exponential's 2^-21 and the
+    sums' n·2^-23."""
+    rng = np.random.default_rng(8)
+    n = 1500
+    k = torch.zeros(1, n, D, dtype=TYPES[dtype])
+    for x, step in enumerate(steps):                                             # one part of the tokens each
+        k[0, n * x // len(steps):, 0] = 60224 + 32 * step
+    v = draw_rows(rng, (1, n, D), dtype, 0.2) + 1
+    cache, table = put([k], [v], 48, dtype, rng)
+    q = torch.zeros(1, G, L, D, dtype=TYPES[dtype])
+    q[..., 0] = 948
+    at, _ = on_device(table, [n])
+    out, lse = api.paged_attention(q.cuda(), cache, *at, scale=1.0, need_lse=True)
+    api.poll_status()
+    o, want, A, _ = ref.attention(as_f64(q), [as_f64(k)], [as_f64(v)], 1.0, True)
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    tol = half * np.abs(o) + ((2 * half**2 if G * L <= 32 else half) + 2.0**-21 + 2 * n * 2.0**-24) * A
+    worst = (np.abs(as_f64(out) - o) / tol).max()
+    assert worst <= 1, f"out is {worst:.2f} of its tolerance"
+    assert (np.abs(as_f64(lse) - want) <= 2.0**-22 * np.abs(want)).all()
+
+
 # ---- values that are not finite
 
 
