@@ -61,7 +61,8 @@ __device__ __forceinline__ void clear_unused(uint8_t* tile, const Tiling& t) {
 tc::Tiling paged_tiling(const PagedArgs& a);
 // Map of q or out: boxes of `heads` heads of `tokens` rows.
 inline bool make_tmap_rows(CUtensorMap* map, const void* base, const PagedArgs& a, const Layout& l, const tc::Tiling& t) {
-  const int64_t dims[4] = {a.c.D, a.Hq, a.c.L, a.c.B}, strides[3] = {l.sh, l.sl, l.sb};
+  // (a single head's, row's or batch's stride means nothing, and may be more than a map takes)
+  const int64_t D = a.c.D, dims[4] = {D, a.Hq, a.c.L, a.c.B}, strides[3] = {a.Hq > 1 ? l.sh : D, a.c.L > 1 ? l.sl : D, a.c.B > 1 ? l.sb : D};
   const int box[4] = {64, t.heads, t.tokens, 1};
   return make_tmap_box(map, base, dims, strides, box);
 }

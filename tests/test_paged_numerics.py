@@ -8,7 +8,7 @@ import torch
 
 from cache_util import TYPES, draw_rows, ints, make_table
 from oracle import paged as ref
-from paged_util import NAN, fill, on_device
+from paged_util import NAN, check, fill, on_device
 from scaled_dot_product_flash_gb300 import _lib, api
 from scaled_dot_product_flash_gb300.inputs import as_f64
 
@@ -224,3 +224,30 @@ def test_a_hidden_value_costs_little(G, L, D, what):
     assert not out[:, :, -1].isfinite().any()
     assert (out[:, :, :-1].float() - good[:, :, :-1].float()).abs().max() <= 2.0**-8 * good.float().abs().max() + 2.0**-8
     assert slow < 600 * max(plain, 0.05)
+
+
+# ---- forms and arguments that other tests do not reach
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [1, 60, 200])
+def test_strides_of_single_dimensions_do_not_matter(L):
+    """The largest batch stride that is valid, of a batch of one."""
+    rng = np.random.default_rng(14)
+    cache, table, ks, vs = fill(rng, [250], 1, 64, 16, "bf16")
+    q = draw_rows(rng, (1, 1, L, 64), "bf16").cuda()
+    out = torch.empty_like(q)
+    lse = torch.empty(1, 1, L, device="cuda")
+    at, _ = on_device(table, [250])
+    c, far = api._paged(cache, *at, 1), 1 << 40
+    need = _lib.sdpa_paged_attn_workspace_size(c, 1, 1, L, 0)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    lay = _lib.Int64x6(far, far, 64, far, far, 64)
+    assert _lib.sdpa_paged_attn(c, q.data_ptr(), out.data_ptr(), lse.data_ptr(), None, lay, None, 1, 1, L, 0.125, 2, 0, ws.data_ptr(), need, stream) == 0
+    w = torch.zeros(1, 1, 250, device="cuda")
+    strides = api._pack2(far, far)
+    assert _lib.sdpa_paged_weights(c, q.data_ptr(), lse.data_ptr(), w.data_ptr(), strides, 250, _lib.Int64x3(far, far, 64), None, 1, 1, L, 0.125, 2, 0, stream) == 0
+    api.poll_status()
+    check(out, lse, q, ks, vs, 0.125, True, "bf16")
+    assert abs(w.sum().item() - L) < 1e-3
