@@ -1,8 +1,8 @@
 // Attention over a 16-bit paged cache for few query rows a KV head, and the kernel that joins the
 // chunks of a sequence (conventions in include/sdpa.h).
 //
-// Rows.  The G·L query rows of a KV head (row r = query r / G of head r % G of the group) are cut
-// into blocks of one or two tiles of 16; a block takes one of them and one chunk of the sequence.  It has
+// Rows.  The G·L query rows of a KV head (row r = query r / G of head r % G of the group), at most 32 (16 at
+// D = 256), are one or two tiles of 16.  A block takes them and one chunk of the sequence.  It has
 // several rings, which take units of 16 tokens of that chunk in turn, and a warp a ring and row
 // tile, each with a running maximum, sum and output of its own, merged at the end.  Chunks are
 // joined by a second kernel, placed while the first still runs.
@@ -141,7 +141,7 @@ struct Ring {
 
 template <typename T, int D, int RT, int kSlots>
 __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kSlots>::kBlocks)
-    paged_few_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, Cut cut, int row_blocks) {
+    paged_few_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, Cut cut) {
   using C = Cfg<D, RT, kSlots>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -151,15 +151,13 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
   const CacheArgs& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int slot = warp / RT, rt = warp % RT;  // the warps of a ring lie side by side
-  const int b = blockIdx.z, h = blockIdx.y / row_blocks, rb = blockIdx.y % row_blocks;
-  const int R = a.G * c.L, row0 = rb * C::kRows;
+  const int b = blockIdx.z, h = blockIdx.y, R = a.G * c.L;
   // The page table's entries of the first units are on their way while the length is; it says which count.
   const int* table = c.pages + b * c.pages_stride;
   const int64_t guess = ((int64_t)blockIdx.x * cut.chunk + (slot + lane * kSlots) * kTile) / c.page_size;
   const int found = guess < c.pages_per_seq ? table[guess] : -1;
   const Rows rows = rows_of(c, b, a.causal, a.max_len, kKidPagedAttn);
-  const int i_last = (min(R, row0 + C::kRows) - 1) / a.G, i_first = max(row0 / a.G, rows.first);
-  const int least = rows.limit(i_first), most = i_first <= i_last ? rows.limit(i_last) : 0;
+  const int least = rows.limit(rows.first), most = rows.first < c.L ? rows.limit(c.L - 1) : 0;
   const int start = (int)min((int64_t)blockIdx.x * cut.chunk, (int64_t)most), end = (int)min((int64_t)start + cut.chunk, (int64_t)most);
   if (start >= end && cut.splits > 1) {
     asm volatile("griddepcontrol.launch_dependents;");
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
     const T* q[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int r = row0 + kTile * rt + 8 * x + g, i = r / a.G;
+      const int r = kTile * rt + 8 * x + g, i = r / a.G;
       lim[x] = r < R ? rows.limit(i) : 0;
       q[x] = r < R && i >= rows.first ? row_ptr<T>(a.q, a.lq, b, h * a.G + r % a.G, i) + 2 * t : nullptr;
     }
@@ -355,8 +353,8 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
   }
   __syncthreads();
   for (int y = threadIdx.x; y < C::kRows * (D / 4); y += C::kWarps * 32) {
-    const int q = y / (D / 4), d = y % (D / 4) * 4, r = row0 + q;
-    if (r >= R) continue;
+    const int q = y / (D / 4), d = y % (D / 4) * 4;
+    if (q >= R) continue;
     float M = minus_inf(), sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
       const float4 z = *reinterpret_cast<const float4*>(red + (w * C::kRows + q) * (D + 4) + d);
       v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
     }
-    const int hq = h * a.G + r % a.G, i = r / a.G;
+    const int hq = h * a.G + q % a.G, i = q / a.G;
     const int64_t row = ((int64_t)b * a.Hq + hq) * c.L + i;
     if (sum == sum && (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w)) {
       float x[4] = {v.x, v.y, v.z, v.w};
@@ -594,9 +592,8 @@ __global__ void __launch_bounds__(WCfg<D, NT>::kWarps * 32) paged_weights_kernel
 
 // ---- host
 
-// Rows of a block (of the weights: of a pass).
+// Rows of a block, which holds all of a KV head (of the weights: of a pass).
 int rows_a_block(const PagedArgs& a) { return a.c.D == 256 || a.G * a.c.L <= kTile ? kTile : 2 * kTile; }
-int row_blocks_of(const PagedArgs& a) { return (a.G * a.c.L + rows_a_block(a) - 1) / rows_a_block(a); }
 // Rings of a block: 4, and two blocks an SM, or 8 for a sequence that one block reads alone (200 tokens,
 // D = 64: 6.3 us instead of 8.3).
 int slots_of(const PagedArgs& a) { return a.c.D < 256 && rows_a_block(a) == kTile && a.max_len <= 512 ? 8 : 4; }
@@ -608,7 +605,7 @@ int slots_of(const PagedArgs& a) { return a.c.D < 256 && rows_a_block(a) == kTil
 Cut cut_few(const PagedArgs& a) {
   constexpr int kStep = 64;  // tokens: a unit a ring
   const int64_t slots = (int64_t)(a.c.num_sms > 0 ? a.c.num_sms : 1) * (a.c.D == 256 ? 1 : 2);
-  const int64_t pairs = (int64_t)a.c.B * a.c.Hkv * row_blocks_of(a);
+  const int64_t pairs = (int64_t)a.c.B * a.c.Hkv;
   const int64_t want = max((int64_t)1, slots / pairs);
   int64_t chunk = (a.max_len + want - 1) / want;
   if (pairs * 4 > slots) chunk = min(chunk, (int64_t)2048);
@@ -636,8 +633,7 @@ cudaError_t few_t(const PagedArgs& a, cudaStream_t s) {
   CUtensorMap map;
   if (!make_tmap_pages(&map, a.c, kTile)) return cudaErrorInvalidValue;
   const Cut cut = cut_few(a);
-  const int blocks = row_blocks_of(a);
-  kern<<<dim3(cut.splits, blocks * a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, cut, blocks);
+  kern<<<dim3(cut.splits, a.c.Hkv, a.c.B), C::kWarps * 32, C::kSmem, s>>>(map, a, cut);
   return cudaGetLastError();
 }
 
@@ -705,10 +701,7 @@ cudaError_t run(const PagedArgs& a, int dtype, Do what, cudaStream_t s) {
 
 }  // namespace
 
-bool paged_attn_launchable(const PagedArgs& a) {
-  if (paged_chunk_takes(a)) return paged_chunk_blocks(a) <= 0x7fffffff;
-  return (int64_t)a.c.Hkv * row_blocks_of(a) <= 65535;
-}
+bool paged_attn_launchable(const PagedArgs& a) { return !paged_chunk_takes(a) || paged_chunk_blocks(a) <= 0x7fffffff; }
 size_t paged_attn_workspace(const PagedArgs& a) {
   const Cut cut = cut_of(a);
   return cut.splits == 1 ? 0 : (size_t)a.c.B * a.Hq * cut.rows * cut.splits * (a.c.D + 2) * sizeof(float);
