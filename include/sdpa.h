@@ -402,9 +402,12 @@ int sdpa_paged_write(const sdpa_cache_t* cache, const void* k, const void* v,
 
 /*
  * Attention of q [B,Hq,Lq,D] over the cached keys and values, as sdpa_cache_attn has it (sinks,
- * lse, is_causal, max_len, workspace; but scaled scores stay below 2^26), for one token or a few a
- * sequence and for chunks of thousands.  Rows that are not real see nothing, whatever is in them.  A token that a row does not
- * see leaves no trace in it, whatever its key and value.  Of one that it sees, a NaN in the key makes
+ * lse, is_causal, max_len, workspace), for one token or a few a sequence and for chunks of
+ * thousands.  Scaled scores stay below 2^26, and values times the tokens of a sequence below 2^119.
+ * Weights enter the sums rounded to dtype, up to 32 rows a KV head (Hq/Hkv·Lq) to twice its bits; in fp16
+ * they are off by another 2^-32 of the row's largest at most.
+ * Rows that are not real see nothing, whatever is in them (so their lse is −inf, or the sink).  A
+ * token that a row does not see leaves no trace in it, whatever its key and value.  Of one that it sees, a NaN in the key makes
  * the row NaN, a NaN in the value that column of its output, and an infinite value makes it infinite
  * or (where the weight is next to nothing) NaN.
  */

@@ -555,7 +555,9 @@ def paged_attention(q, cache, pages, lens, scale=None, is_causal="bottom_right",
 
     For one token or a few a sequence as for chunks of a prompt (write their rows first).
     counts int32 [B]: only the last counts[b] rows are real; the others of a padded batch give
-    0 (lse -inf).  The other arguments as in ``cache_attention``.
+    0 (lse -inf, or the sink where there is one).  The other arguments as in ``cache_attention``.
+    How work is cut over the device goes by max_len, or the width of ``pages``: bound it where the
+    table is much wider than the sequences.
     """
     if stream is not None and stream != torch.cuda.current_stream():
         with torch.cuda.stream(stream):

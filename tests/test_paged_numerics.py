@@ -11,6 +11,7 @@ from oracle import paged as ref
 from paged_util import NAN, check, fill, on_device
 from scaled_dot_product_flash_gb300 import _lib, api
 from scaled_dot_product_flash_gb300.inputs import as_f64
+from test_paged_evict import check_weights
 
 
 def put(ks, vs, page, dtype, rng):
@@ -226,7 +227,69 @@ def test_a_hidden_value_costs_little(G, L, D, what):
     assert slow < 600 * max(plain, 0.05)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,size", [("bf16", 2.0**100), ("f16", 60000.0)])
+@pytest.mark.parametrize("D,G,L", FORMS)
+def test_large_values(D, G, L, dtype, size):
+    """Values whose sum over 4000 tokens is far from fp32's end in bf16, and near fp16's largest number.
+    Tolerance: paged_util.check's terms; A is at most `size`."""
+    rng = np.random.default_rng(11)
+    n = 4000
+    k = draw_rows(rng, (1, n, D), dtype, 0.5)
+    v = torch.from_numpy(size * rng.choice([1, -0.5], (1, n, D))).to(k.dtype)
+    v[..., 0] = size
+    cache, table = put([k], [v], 48, dtype, rng)
+    q = draw_rows(rng, (1, G, L, D), dtype, 0.5)
+    at, _ = on_device(table, [n])
+    out, _ = api.paged_attention(q.cuda(), cache, *at)
+    api.poll_status()
+    o, _, A, S = ref.attention(as_f64(q), [as_f64(k)], [as_f64(v)], D**-0.5, True)
+    half, u = torch.finfo(TYPES[dtype]).eps / 2, 2.0**-24
+    tol = half * np.abs(o) + ((2 * half**2 if G * L <= 32 else half) + 2 * (D + 8) * u * S[..., None] + 2.0**-20 + 2 * n * u) * A
+    assert (np.abs(as_f64(out) - o) <= tol).all()
+
+
 # ---- forms and arguments that other tests do not reach
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,Hq,Hkv,L,page,lens,counts", [
+    ("bf16", 4, 1, 5, 16, [300, 9, 5], [5, 2, 0]),
+    ("f16", 17, 1, 1, 48, [700, 1], None),
+    ("bf16", 8, 2, 8, 64, [129, 500], [8, 3]),
+    ("f16", 2, 1, 16, 32, [1300, 16, 40], [16, 16, 7]),
+])
+def test_17_to_32_rows_at_head_dim_256(dtype, Hq, Hkv, L, page, lens, counts, causal):
+    """One tile of rows, head and remainder of P in every tile; weights in two passes over the rows."""
+    rng = np.random.default_rng(12 + L)
+    cache, table, ks, vs = fill(rng, lens, Hkv, 256, page, dtype)
+    q = draw_rows(rng, (len(lens), Hq, L, 256), dtype, 1.5)
+    at, dev_counts = on_device(table, lens, counts)
+    how = dict(is_causal="bottom_right" if causal else False, counts=dev_counts)
+    out, lse = api.paged_attention(q.cuda(), cache, *at, need_lse=True, **how)
+    check(out, lse, q, ks, vs, 1 / 16, causal, dtype, counts)
+    old = torch.from_numpy(rng.random((len(lens), Hkv, max(lens) + 5))).float()
+    got = api.paged_weights(q.cuda(), cache, *at, lse, old.cuda(), **how)
+    api.poll_status()
+    check_weights(got, q, ks, vs, lse, old, 1 / 16, causal, counts)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,counts", [(70, [70, 33]), (33, None)])
+def test_weights_under_a_table_of_8_million_tokens(L, counts):
+    """More blocks of keys than a grid's second dimension: the kernel for few rows, in several passes over them."""
+    rng = np.random.default_rng(13)
+    lens = [300, 71]
+    cache, table, ks, vs = fill(rng, lens, 1, 32, 65536, "bf16", width=129)
+    q = draw_rows(rng, (2, 2, L, 32), "bf16")
+    at, dev_counts = on_device(table, lens, counts)
+    out, lse = api.paged_attention(q.cuda(), cache, *at, need_lse=True, counts=dev_counts, max_len=300)
+    old = torch.rand(2, 1, 8454144, generator=torch.Generator().manual_seed(1))
+    got = api.paged_weights(q.cuda(), cache, *at, lse, old.cuda(), counts=dev_counts)
+    api.poll_status()
+    assert torch.equal(got[:, :, 300:].cpu(), old[:, :, 300:])
+    check_weights(got[:, :, :320], q, ks, vs, lse, old[:, :, :320], 32**-0.5, True, counts)
 
 
 @pytest.mark.gpu
