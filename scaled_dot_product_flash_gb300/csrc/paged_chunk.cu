@@ -21,11 +21,12 @@
 // along the keys, and the join kernel adds the unnormalised results up.
 //
 // Bound: the tensor pipe, 1024 cycles a pair of tiles of 128 x 128 at D = 128; exponentials take half of that.
-// Measured (bf16, 32 query and 8 KV heads, D = 128, from a graph): 2 prompts of 4096 tokens 233 us, 1180
-// TFLOP/s, 0.61 of the measured rate (the dense kernel on the same shape 228); 2048 queries over 32768
-// tokens 784 us, 1365 TFLOP/s, 0.71.  A block's iteration takes some 3000 cycles for 2048 of the tensor
-// pipe, its start and end some 5 us.  The softmax loop is sensitive: clearing V's last rows in it, once
-// a block, cost 3%, looking values of cut tiles through 5 to 9%.
+// Measured (bf16, 32 query and 8 KV heads, D = 128, from a graph): 2 prompts of 4096 tokens 230 us, 1195
+// TFLOP/s, 0.62 of the measured rate (the dense kernel on the same shape 228); 2048 queries over 32768
+// tokens 765 us, 1400 TFLOP/s, 0.73; in fp16 236 to 240 and 780 to 800.  A block's iteration takes some 3000
+// cycles for 2048 of the tensor pipe, its start and end some 5 us.  The softmax loop is sensitive: clearing V's
+// last rows in it, once a block, cost 3%, looking values of cut tiles through 5 to 9%, rounding c·s before
+// the base is taken off it 4%.
 #include "paged_tc.cuh"
 
 namespace sdpa {
@@ -873,12 +874,12 @@ cudaError_t chunk_d(const PagedArgs& a, cudaStream_t s) {
     return cudaGetLastError();
   }
   if constexpr (D <= 128) {
-  auto* kern = paged_chunk_kernel<T, D>;
-  static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(kern, Layout128<D>::kBytes, ready);
-  if (e != cudaSuccess) return e;
-  kern<<<(unsigned)paged_chunk_blocks(a), kThreads, Layout128<D>::kBytes, s>>>(tq, tkv, to, a, t);
-  return cudaGetLastError();
+    auto* kern = paged_chunk_kernel<T, D>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(kern, Layout128<D>::kBytes, ready);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)paged_chunk_blocks(a), kThreads, Layout128<D>::kBytes, s>>>(tq, tkv, to, a, t);
+    return cudaGetLastError();
   }
   return cudaErrorInvalidValue;
 }

@@ -16,7 +16,8 @@
 //    enough of them to fill the device.
 //    Bound: HBM, twice the rows that move.  32 sequences of 2304 tokens to 2048, 8 heads, D = 128: 99 us
 //    with the selection (8 of them), 5.5 TB/s; looking places up a round ahead but waiting for it, 128.
-//    One of 32768 to 8192: 28.7 us, 12 of them the selection, whose cluster barriers cost 0.7 us each.
+//    One of 32768 to 8192: 28.6 us, 12 of them the selection, whose cluster barriers cost 0.7 us each; eight
+//    rounds of 1024 rows in slices of 32 bytes.
 #include <cooperative_groups.h>
 
 #include "paged.h"

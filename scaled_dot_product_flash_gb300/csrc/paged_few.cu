@@ -23,7 +23,7 @@
 //
 // Measured (bf16, 32 query and 8 KV heads, D = 128, calls replayed from a graph): 32 sequences of 256 to
 // 8192 tokens 90.8 us, 554 MB, 6.0 TB/s with the join; one of 131072 tokens 91 us, 5.9 TB/s; 200 tokens,
-// D = 64, 4.7 us.  Blocks of 8 rings, one an SM, took 94.5 us for the batch, of 4 rings, two an SM, 91 to 94.
+// D = 64, in fp16 4.9 us.  Blocks of 8 rings, one an SM, took 94.5 us for the batch, of 4 rings, two an SM, 91 to 94.
 // The weights of the batch, keys alone, 48.5 us, 5.9 TB/s: blocks of 4 warps with rings of 3 units, four an
 // SM (8 warps 68 us, rings of 4 55), what a token's weight was being read a unit ahead (97 us without).
 #include "paged.h"
@@ -598,7 +598,9 @@ int rows_a_block(const PagedArgs& a) { return a.c.D == 256 || a.G * a.c.L <= kTi
 // D = 64: 6.3 us instead of 8.3).
 int slots_of(const PagedArgs& a) { return a.c.D < 256 && rows_a_block(a) == kTile && a.max_len <= 512 ? 8 : 4; }
 
-// How a call's sequences are cut into chunks: for few pairs of a sequence and head into one wave of
+// How a call's sequences are cut into chunks, by the longest one that the call admits (max_len, or the
+// table's width; a bound far above the sequences costs: one of 2048 tokens takes 7.2 us, under a table of 131072
+// without a max_len 34.5): for few pairs of a sequence and head into one wave of
 // blocks, of at least 128 tokens (2048 tokens, 8 heads: 10.3 us, of 256 12.3, of 512 14.4); for many into
 // chunks of 2048 at most, so that unequal sequences share the SMs (32 of 256 to 8192 tokens, 32 rows: 125 us,
 // of 1024 131, of 512 162); none where one block's warps read the sequence in what a join costs.

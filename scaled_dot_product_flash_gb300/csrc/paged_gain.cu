@@ -304,7 +304,7 @@ cudaError_t gain_d(const PagedArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.c.B * a.c.Hkv, blocks = (a.max_len + L::KT * kBN - 1) / (L::KT * kBN);
   const int64_t q_tiles = (int64_t)t.groups * ((a.c.L + t.tokens - 1) / t.tokens);
-  // Blocks for three waves and more, so that under the causal mask, where the first keys have the most
+  // Blocks for two waves and more, so that under the causal mask, where the first keys have the most
   // rows, they end together; at least 8 Q tiles each.
   int cl = 1;
   while (cl < 8 && units * blocks * cl < 2 * (int64_t)a.c.num_sms && cl * 16 <= q_tiles) cl *= 2;
