@@ -405,7 +405,7 @@ int sdpa_paged_write(const sdpa_cache_t* cache, const void* k, const void* v,
  * lse, is_causal, max_len, workspace), for one token or a few a sequence and for chunks of
  * thousands.  Scaled scores stay below 2^26, and values times the tokens of a sequence below 2^119.
  * Weights enter the sums rounded to dtype, up to 32 rows a KV head (Hq/Hkv·Lq) to twice its bits; in fp16
- * they are off by another 2^-32 of the row's largest at most.
+ * they are off by another 2^-32 of the row's largest at most (2^-25 where scores pass 2^21).
  * Rows that are not real see nothing, whatever is in them (so their lse is −inf, or the sink).  A
  * token that a row does not see leaves no trace in it, whatever its key and value.  Of one that it sees, a NaN in the key makes
  * the row NaN, a NaN in the value that column of its output, and an infinite value makes it infinite

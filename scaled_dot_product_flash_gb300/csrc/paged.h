@@ -134,13 +134,13 @@ __device__ __forceinline__ int64_t paged_row(const CacheArgs& c, int page, int w
 // P = 2^(c·s − base) meets V in T.  A row's base follows its scores lazily, since O has to be rescaled with
 // it: it rises where a tile's maximum passes the one it was set by by 2^8.  bf16 has fp32's exponents and takes
 // that maximum itself as the base.  fp16 ends below 2^16 and loses bits under 2^-14, so there the base lies 7
-// below it, and it sinks again where a tile's weights all lie under 2^-7, as they do behind a token that
+// below it, and it falls again where a tile's weights all lie under 2^-7, as they do behind a token that
 // outweighs the others.  A weight is off by 2^-25·2^base then, apart from its rounding to the type's bits: by at
 // most 2^-32 of the row's largest and 2^-18 of its tile's largest.  (Sums of 16 more bits per weight, for few rows, do not
 // help against the end of the exponents.)
 template <typename T>
 constexpr bool kNarrow = std::is_same<T, __half>::value;
-constexpr float kRescale = 8.f, kSink = 7.f, kBias = 7.f;
+constexpr float kRescale = 8.f, kFall = 7.f, kBias = 7.f;
 constexpr float kExact = 4194304.f;  // 2^22: below it a base can lie 7 below a maximum with P still under 2^16
 
 template <typename T>
@@ -152,17 +152,17 @@ __device__ __forceinline__ float base_of(float top) { return top - bias_of<T>(to
 template <typename T>
 __device__ __forceinline__ float base_high(float base) { return base + (kRescale + bias_of<T>(base)); }
 // (What lies 2^60 below the row's sum l adds nothing; O stays far from fp32's end.)
-__device__ __forceinline__ bool base_sinks(float base, float top, float l) { return top < base - kSink && l * tc::ex2(base - top) < 0x1p60f; }
+__device__ __forceinline__ bool base_falls(float base, float top, float l) { return top < base - kFall && l * tc::ex2(base - top) < 0x1p60f; }
 
 // For columns [d, d + N) of an output o of query (hq, i) of KV head h over the tokens [from, to) of
 // sequence b, some of which came out NaN without a reason in the row's scores, since a product meets
 // every value of a tile, under a weight of 0 too.  Those with a value among the tokens that is not finite are
 // infinite or NaN accordingly; the others, where the value belongs to a token that the row does not
 // see, are Σ exp2(c·q·k_j − M)·v_j once more, product by product in fp32, one thread a row.
-// A value that is not finite in the last token of 60 queries over 16384 tokens, D = 128, costs 26 ms so in bf16 and 80 in
-// fp16, element by element, of eight of them for one or two tokens 0.4.  What the loops of paged_chunk.cu take
-// depends on what this function looks like: the dot product in pieces of 8 costs fp16 prompts 3% and bf16 ones
-// nothing; four tokens at a time, 4 ms here, 7%; warp-level MMAs, 1 to 2 ms here, 25%.
+// A value that is not finite in the last token of 60 queries over 16384 tokens costs 20 ms so in bf16 and at
+// D = 256, 78 in fp16 at D = 128, element by element, and one at the end of 16384 for one or two queries 0.4.  What
+// the loops of paged_chunk.cu take depends on what this function looks like: pieces of 8 cost fp16 prompts 3% and
+// bf16 ones nothing; the sums in registers, 4 ms here, 7%; warp-level MMAs, 1 to 2 ms here, 25%.
 template <typename T, int D, int N>
 __device__ __noinline__ void mend_columns(const PagedArgs& a, int b, int h, int hq, int i, int d, int from, int to, float M, float* o) {
   const CacheArgs& c = a.c;
@@ -190,32 +190,42 @@ __device__ __noinline__ void mend_columns(const PagedArgs& a, int b, int h, int 
   for (int y = 0; y < N; ++y)
     if (o[y] != 0.f) open &= ~(1u << y);
   if (!open) return;
-  for (int j = from; j < to; ++j) {
+  constexpr int kStep = D == 256 || (!kNarrow<T> && N == 32) ? 4 : 1;  // tokens at a time, of one page
+  for (int j = from; j < to; j += kStep) {
     const int page = c.pages[b * c.pages_stride + j / c.page_size], place = j % c.page_size;
     if ((unsigned)page >= (unsigned)c.num_pages) continue;
     const T* k = data + paged_row(c, page, 0, h, place);
     const T* v = data + paged_row(c, page, 1, h, place) + d;
-    float s = 0.f;
-    if constexpr (kNarrow<T> && N == 32) {
-      for (int y = 0; y < D; ++y) s = fmaf(Elem<T>::to_f(q[y]), Elem<T>::to_f(k[y]), s);
+    float s[kStep] = {};
+    if constexpr (kNarrow<T> && N == 32 && D < 256) {
+      for (int y = 0; y < D; ++y) s[0] = fmaf(Elem<T>::to_f(q[y]), Elem<T>::to_f(k[y]), s[0]);
     } else {
 #pragma unroll 2
       for (int y = 0; y < D; y += 8) {
-        const uint4 x4 = *reinterpret_cast<const uint4*>(q + y), z4 = *reinterpret_cast<const uint4*>(k + y);
-        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, z[4] = {z4.x, z4.y, z4.z, z4.w};
+        const uint4 x4 = *reinterpret_cast<const uint4*>(q + y);
+        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float x0, x1, z0, z1;
-          tc::unpack2<T>(x[u], x0, x1);
-          tc::unpack2<T>(z[u], z0, z1);
-          s = fmaf(x0, z0, s);
-          s = fmaf(x1, z1, s);
+        for (int n = 0; n < kStep; ++n) {
+          const uint4 z4 = *reinterpret_cast<const uint4*>(k + n * D + y);
+          const uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x0, x1, z0, z1;
+            tc::unpack2<T>(x[u], x0, x1);
+            tc::unpack2<T>(z[u], z0, z1);
+            s[n] = fmaf(x0, z0, s[n]);
+            s[n] = fmaf(x1, z1, s[n]);
+          }
         }
       }
     }
-    const float p = tc::ex2(s * a.scale_log2 - M);
-    for (int y = 0; y < N; ++y)
-      if (open >> y & 1u) o[y] = fmaf(p, Elem<T>::to_f(v[y]), o[y]);
+#pragma unroll
+    for (int n = 0; n < kStep; ++n) {
+      if (j + n >= to) break;
+      const float p = tc::ex2(s[n] * a.scale_log2 - M);
+      for (int y = 0; y < N; ++y)
+        if (open >> y & 1u) o[y] = fmaf(p, Elem<T>::to_f(v[n * D + y]), o[y]);
+    }
   }
 }
 

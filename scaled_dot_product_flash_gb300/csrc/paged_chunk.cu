@@ -139,12 +139,12 @@ __device__ __forceinline__ void clear_behind(uint8_t* tile, int row, int lane, i
 
 // Whether a row's base (paged.h) may have to move for a tile's largest score; `high`: where it rises.
 template <typename T>
-__device__ __forceinline__ bool base_off(float m, float high, float top) { return top > high || (kNarrow<T> && top < m - kSink); }
+__device__ __forceinline__ bool base_off(float m, float high, float top) { return top > high || (kNarrow<T> && top < m - kFall); }
 // Moves it to where that score wants it, the row's sum along; returns O's factor.  Only a warp that has such a
 // row asks (2048 queries over 32768 tokens: 764 us, all asking 778), in fp16 by a call (796 us, inlined 819).
 template <typename T>
 __device__ __forceinline__ float3 moved_base(float m, float l, float top) {
-  if (!(top > base_high<T>(m)) && !(kNarrow<T> && base_sinks(m, top, l))) return make_float3(m, l, 1.f);
+  if (!(top > base_high<T>(m)) && !(kNarrow<T> && base_falls(m, top, l))) return make_float3(m, l, 1.f);
   const float to = base_of<T>(top), alpha = ex2(m - to);  // 0 when m was -inf
   return make_float3(to, l * alpha, alpha);
 }

@@ -265,18 +265,18 @@ __global__ void __launch_bounds__(Cfg<D, RT, kSlots>::kWarps * 32, Cfg<D, RT, kS
 #pragma unroll
       for (int x = 0; x < 2; ++x) top[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
       const bool rise = top[0] > base_high<T>(m[0]) || top[1] > base_high<T>(m[1]);
-      const bool sink = kNarrow<T> && (top[0] < m[0] - kSink || top[1] < m[1] - kSink);  // (by the lane's scores)
-      if (__any_sync(0xffffffffu, rise || sink)) {
-        const bool sinks = kNarrow<T> && __any_sync(0xffffffffu, sink);
+      const bool fall = kNarrow<T> && (top[0] < m[0] - kFall || top[1] < m[1] - kFall);  // (by the lane's scores)
+      if (__any_sync(0xffffffffu, rise || fall)) {
+        const bool falls = kNarrow<T> && __any_sync(0xffffffffu, fall);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float v = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
           float up = fmaxf(m[x], base_of<T>(v));
-          if (sinks) {
+          if (falls) {
             float sum = l[x] + __shfl_xor_sync(0xffffffffu, l[x], 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (base_sinks(m[x], v, sum)) up = base_of<T>(v);
+            if (base_falls(m[x], v, sum)) up = base_of<T>(v);
           }
           const float f = up == minus_inf() ? 1.f : ex2(m[x] - up);
           m[x] = up;
